@@ -7,12 +7,13 @@ the library's kernels; importing the binding fails loudly if the library has
 not been built (``build()``).
 """
 from . import _build
-from .abi import (MOE_ERR_CUDA, MOE_ERR_DEVICE_DATA, MOE_ERR_INVALID_ARG, MOE_ERR_TIMEOUT,
+from .abi import (MOE_ACT_GELU, MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_SWIGLU, MOE_ERR_CUDA, MOE_ERR_DEVICE_DATA, MOE_ERR_INVALID_ARG, MOE_ERR_TIMEOUT,
                   MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_FP8_GLOBAL, MOE_FP8_PER_EXPERT,
                   MOE_FP8_PER_TOKEN, MOE_OK, MOE_SOFTMAX_TOPK, MOE_TOPK_SOFTMAX, Layout, MoeError,
                   alloc_workspace, moe_combine, moe_combine_backward, moe_combine_fp8, moe_dispatch,
                   moe_dispatch_backward, moe_dispatch_layout, moe_gate, moe_gate_backward, moe_get_status,
                   moe_quantize_rows, moe_route, moe_rows_max, moe_workspace_init, moe_workspace_size)
+from .experts import ExpertFFN, ExpertRows, FFNGrads, SavedLayer
 from .pipeline import RouteGraph, RoutePipeline, RoutePlan, RouteShape
 
 
@@ -22,7 +23,8 @@ def build(force: bool = False) -> str:
 
 
 __all__ = [
-    "build", "RoutePlan", "RoutePipeline", "RouteGraph", "RouteShape", "Layout", "MoeError", "alloc_workspace",
+    "build", "ExpertRows", "ExpertFFN", "FFNGrads", "SavedLayer", "MOE_ACT_NONE", "MOE_ACT_SILU", "MOE_ACT_GELU",
+    "MOE_ACT_SWIGLU", "RoutePlan", "RoutePipeline", "RouteGraph", "RouteShape", "Layout", "MoeError", "alloc_workspace",
     "moe_gate", "moe_dispatch_layout", "moe_dispatch", "moe_combine", "moe_get_status", "moe_route",
     "moe_quantize_rows", "moe_combine_fp8", "moe_combine_backward", "moe_dispatch_backward",
     "moe_gate_backward", "MOE_FP8_PER_TOKEN", "MOE_FP8_PER_EXPERT", "MOE_FP8_GLOBAL",

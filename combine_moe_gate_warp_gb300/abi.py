@@ -31,6 +31,11 @@ MOE_FP8_PER_TOKEN = 1
 MOE_FP8_PER_EXPERT = 2
 MOE_FP8_GLOBAL = 3
 
+MOE_ACT_NONE = 0
+MOE_ACT_SILU = 1
+MOE_ACT_GELU = 2
+MOE_ACT_SWIGLU = 3
+
 MOE_MAX_EXPERTS = 256
 MOE_MAX_TOPK = 16
 MOE_MAX_SHARED = 8
@@ -68,6 +73,12 @@ class moe_dedup(ctypes.Structure):
         ("send_offsets", ctypes.c_void_p), ("send_row", ctypes.c_void_p), ("send_token", ctypes.c_void_p),
         ("slot_local", ctypes.c_void_p), ("slot_gate", ctypes.c_void_p),
     ]
+
+
+class moe_rows(ctypes.Structure):
+    """Mirror of ``struct moe_rows`` (host struct of device pointers)."""
+    _fields_ = [("rows", ctypes.c_int32), ("E", ctypes.c_int32), ("offsets", ctypes.c_void_p),
+                ("ws", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -126,6 +137,15 @@ def lib():
     L.moe_dispatch_dedup.restype = I
     L.moe_combine_partials.argtypes = [P, ctypes.POINTER(moe_dedup), P, I, I, I, P, P]
     L.moe_combine_partials.restype = I
+    G = ctypes.POINTER(moe_rows)
+    L.moe_expert_linear.argtypes = [G, P, P, I, P, P, I, P, I, P, P, P, P, P]
+    L.moe_expert_linear.restype = I
+    L.moe_expert_dgrad.argtypes = [G, P, I, P, I, I, P, P, P, P, P]
+    L.moe_expert_dgrad.restype = I
+    L.moe_expert_wgrad.argtypes = [G, P, I, P, I, P, P, I, P]
+    L.moe_expert_wgrad.restype = I
+    L.moe_act_backward.argtypes = [G, P, I, I, P, P, P, P, P]
+    L.moe_act_backward.restype = I
     L.moe_get_status.argtypes = [P, P]
     L.moe_get_status.restype = I
     L.moe_status_string.argtypes = [I]

@@ -1,0 +1,89 @@
+// activation.cuh -- the activations of the expert products, their slopes, and
+// the 8-bit form of a saved layer (include/moe_experts.h).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "moe_experts.h"
+
+namespace moe {
+
+// The exponentials are __expf's: its error, a few fp32 ulps at these
+// magnitudes, is far below the bf16 rounding of every result.
+__device__ __forceinline__ float logistic(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
+
+__device__ __forceinline__ float act_value(float u, int act)
+{
+    if (act == MOE_ACT_SILU) return u * logistic(u);
+    if (act == MOE_ACT_GELU) return 0.5f * u * (1.0f + erff(u * 0.70710678118654752f));
+    return u;
+}
+
+// act'(u)
+__device__ __forceinline__ float act_slope(float u, int act)
+{
+    if (act == MOE_ACT_SILU) {
+        const float q = logistic(u);
+        return q * (1.0f + u * (1.0f - q));
+    }
+    if (act == MOE_ACT_GELU)
+        return 0.5f * (1.0f + erff(u * 0.70710678118654752f)) + u * __expf(-0.5f * u * u) * 0.39894228040143268f;
+    return 1.0f;
+}
+
+// Scale byte of a saved block from the bit pattern of its largest magnitude
+// (sign cleared): 127 + X, X the exponent of the smallest power of two with
+// amax <= 448 * 2^X = 1.75 * 2^(X + 8); 255 for a NaN or an infinity.
+__device__ __forceinline__ unsigned saved_byte(unsigned amax_bits)
+{
+    if (amax_bits >= 0x7F800000u) return 255u;
+    // amax's exponent byte, one more where its fraction passes 1.75; a
+    // subnormal has exponent byte 0 and lands below the clamp either way
+    const int b = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return (unsigned)max(b, 0);
+}
+// 1 / scale = 2^(127 - byte), exact (byte <= 247 for a finite amax)
+__device__ __forceinline__ float saved_inverse(unsigned byte)
+{
+    return byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - byte) << 23);
+}
+// scale = 2^(byte - 127); 2^-127 is a subnormal
+__device__ __forceinline__ float saved_scale(unsigned byte)
+{
+    return __uint_as_float(byte == 0u ? 0x400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+}
+
+// lo in the low byte
+__device__ __forceinline__ unsigned e4m3_pair(float lo, float hi)
+{
+    return (unsigned)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 e4m3_decode2(unsigned c)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xFFFFu), __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+// four codes times their block's scale
+__device__ __forceinline__ void saved_decode4(unsigned c, float scale, float *u)
+{
+    const float2 a = e4m3_decode2(c), b = e4m3_decode2(c >> 16);
+    u[0] = a.x * scale;
+    u[1] = a.y * scale;
+    u[2] = b.x * scale;
+    u[3] = b.y * scale;
+}
+
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const unsigned *>(&v);
+}
+__device__ __forceinline__ uint2 pack_bf16x4(const float *v)
+{
+    return make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+}
+
+}  // namespace moe

@@ -1,0 +1,276 @@
+"""The experts' products between dispatch and combine (include/moe_experts.h).
+
+``ExpertRows`` holds what the calls on one set of packed rows share (the
+layout's offsets and a workspace) and has the products as methods;
+``ExpertFFN`` is the two-layer expert network made of them, with its hidden
+layer saved in 8 bits between the passes.  Every method checks its arguments
+on the host, allocates the outputs it is not given (through PyTorch) and
+enqueues the library's kernels on the current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import abi
+
+ACTIVATIONS = {"none": abi.MOE_ACT_NONE, "silu": abi.MOE_ACT_SILU, "gelu": abi.MOE_ACT_GELU,
+               "swiglu": abi.MOE_ACT_SWIGLU}
+SAVED_BLOCK = 32  # columns that share one scale byte
+_STATUS_BYTES = 8192
+
+
+@dataclass
+class SavedLayer:
+    """A layer's activation inputs in 8 bits: e4m3 ``codes`` [rows, N] and
+    one scale byte per 32 columns, ``scales`` [rows, N / 32]; a value is
+    e4m3(code) * 2^(byte - 127).  Byte 255 marks a block that held a NaN or
+    an infinity."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @staticmethod
+    def empty(rows: int, N: int, device="cuda") -> "SavedLayer":
+        if N % SAVED_BLOCK:
+            raise ValueError(f"a saved layer's columns are a multiple of {SAVED_BLOCK}, got {N}")
+        return SavedLayer(torch.empty((rows, N), dtype=torch.uint8, device=device),
+                          torch.empty((rows, N // SAVED_BLOCK), dtype=torch.uint8, device=device))
+
+
+def _act(name: str) -> int:
+    try:
+        return ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError(f"act: one of {', '.join(ACTIVATIONS)}, got {name!r}") from None
+
+
+def _check(t, dtype, shape, name, device):
+    """A contiguous tensor of exactly this type, shape and device; its address."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the rows are on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+class ExpertRows:
+    """The packed rows of a layout: expert e has rows offsets[e] ..
+    offsets[e+1]-1 of buffers that hold ``rows`` rows.
+
+    ``offsets`` is the layout's device tensor (int32 [E+1]); None makes all
+    rows one group, for the shared experts' plain products (weights then
+    lack the expert axis: [N, K], bias [N]).  ``ws`` is a workspace whose
+    status word takes device-detected problems; one is made if none is
+    given."""
+
+    def __init__(self, offsets: torch.Tensor | None = None, *, rows: int, device="cuda", ws=None):
+        if rows < 0:
+            raise ValueError(f"rows: {rows}")
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.grouped = offsets is not None
+        self.E = 1
+        if offsets is not None:
+            if offsets.dim() != 1 or not 2 <= offsets.numel() <= abi.MOE_MAX_EXPERTS + 1:
+                raise ValueError(f"offsets: expected [E + 1] with E in 1..{abi.MOE_MAX_EXPERTS}, "
+                                 f"got {tuple(offsets.shape)}")
+            self.E = offsets.numel() - 1
+            _check(offsets, torch.int32, offsets.shape, "offsets", self.device)
+        self.rows, self.offsets = rows, offsets
+        if ws is None:
+            ws = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=self.device)
+        elif ws.numel() * ws.element_size() < _STATUS_BYTES or ws.device != self.device:
+            raise ValueError(f"ws: a workspace of at least {_STATUS_BYTES} bytes on {self.device}")
+        self.ws = ws
+        self._c = abi.moe_rows(rows, self.E, None if offsets is None else offsets.data_ptr(), ws.data_ptr())
+        self._ref = ctypes.byref(self._c)
+        self._lib = abi.lib()
+
+    @staticmethod
+    def of(plan) -> "ExpertRows":
+        """The packed rows of a RoutePlan; problems are recorded in its workspace."""
+        return ExpertRows(plan.layout.offsets, rows=plan.r_max, device=plan.layout.offsets.device, ws=plan.ws)
+
+    def status(self) -> int:
+        """Synchronise, return and clear the device status."""
+        return abi.moe_get_status(self.ws)
+
+    def new_saved(self, N: int) -> SavedLayer:
+        return SavedLayer.empty(self.rows, N, self.device)
+
+    # ------------------------------------------------------------------
+    def _stream(self):
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def _weights(self, w, dtype):
+        """(N, K, address) of weights [E, N, K], or [N, K] for one plain group."""
+        if not isinstance(w, torch.Tensor) or w.dim() != (3 if self.grouped else 2):
+            raise ValueError("w: expected a tensor of " + ("[E, N, K]" if self.grouped else "[N, K]"))
+        N, K = w.shape[-2:]
+        return N, K, _check(w, dtype, self._per_expert(N, K), "w", self.device)
+
+    def _per_expert(self, *shape):
+        return (self.E, *shape) if self.grouped else shape
+
+    def _opt(self, t, dtype, shape, name):
+        return None if t is None else _check(t, dtype, shape, name, self.device)
+
+    def _out(self, t, dtype, shape, name):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+            return t, t.data_ptr()
+        return t, _check(t, dtype, shape, name, self.device)
+
+    def _saved(self, saved, N):
+        return (_check(saved.codes, torch.uint8, (self.rows, N), "saved.codes", self.device),
+                _check(saved.scales, torch.uint8, (self.rows, N // SAVED_BLOCK), "saved.scales", self.device))
+
+    # ------------------------------------------------------------------
+    def linear(self, x, w, *, bias=None, act: str = "none", residual=None, saved: SavedLayer | None = None,
+               x_scales=None, w_scales=None, out=None):
+        """act(x w^T + bias) + residual for each expert's rows -> [rows, N]
+        ([rows, N / 2] for swiglu, whose columns are gates, then ups).
+
+        x [rows, K] and w [E, N, K] are bf16, or e4m3 codes (uint8) with
+        x_scales [rows, 2] (scale, zero) and w_scales [E, N, 2] (scale, sum).
+        ``saved`` receives the activation's inputs in 8 bits."""
+        a, fp8 = _act(act), x_scales is not None
+        if fp8 != (w_scales is not None):
+            raise ValueError("x_scales and w_scales go together")
+        dtype = torch.uint8 if fp8 else torch.bfloat16
+        N, K, wp = self._weights(w, dtype)
+        cols = N // 2 if a == abi.MOE_ACT_SWIGLU else N
+        xp = _check(x, dtype, (self.rows, K), "x", self.device)
+        xs = self._opt(x_scales, torch.float32, (self.rows, 2), "x_scales")
+        ws = self._opt(w_scales, torch.float32, self._per_expert(N, 2), "w_scales")
+        bp = self._opt(bias, torch.bfloat16, self._per_expert(N), "bias")
+        rp = self._opt(residual, torch.bfloat16, (self.rows, cols), "residual")
+        sc, ss = (None, None) if saved is None else self._saved(saved, N)
+        out, op = self._out(out, torch.bfloat16, (self.rows, cols), "out")
+        abi._check(self._lib.moe_expert_linear(self._ref, xp, xs, K, wp, ws, N, bp, a, rp, op, sc, ss,
+                                               self._stream()), "moe_expert_linear")
+        return out
+
+    def dgrad(self, dy, w, *, act: str = "none", saved: SavedLayer | None = None, out=None, a=None):
+        """dy w -> [rows, K]; with ``act`` and the ``saved`` input of the
+        activation that made this product's rows, the gradient with respect
+        to that input ([rows, K], swiglu: [rows, 2K]).  ``a`` [rows, K], if
+        given, receives act(saved)."""
+        code = _act(act)
+        N, K, wp = self._weights(w, torch.bfloat16)
+        if (saved is None) != (code == abi.MOE_ACT_NONE):
+            raise ValueError("act and saved go together")
+        if a is not None and saved is None:
+            raise ValueError("a: only with a saved layer")
+        cols = 2 * K if code == abi.MOE_ACT_SWIGLU else K
+        dp = _check(dy, torch.bfloat16, (self.rows, N), "dy", self.device)
+        sc, ss = (None, None) if saved is None else self._saved(saved, cols)
+        ap = self._opt(a, torch.bfloat16, (self.rows, K), "a")
+        out, op = self._out(out, torch.bfloat16, (self.rows, cols), "out")
+        abi._check(self._lib.moe_expert_dgrad(self._ref, dp, N, wp, K, code, sc, ss, op, ap, self._stream()),
+                   "moe_expert_dgrad")
+        return out
+
+    def wgrad(self, dy, x, *, bias: bool = False, dtype=torch.bfloat16, out=None, out_bias=None):
+        """(dw [E, N, K], db [E, N] or None) = sums of dy^T x and of dy over
+        each expert's rows; zeros for an expert without rows.  ``dtype`` is
+        bf16 or fp32."""
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"dtype: bfloat16 or float32, got {dtype}")
+        if dy.dim() != 2 or x.dim() != 2:
+            raise ValueError("dy and x: expected [rows, columns]")
+        N, K = dy.shape[1], x.shape[1]
+        dp = _check(dy, torch.bfloat16, (self.rows, N), "dy", self.device)
+        xp = _check(x, torch.bfloat16, (self.rows, K), "x", self.device)
+        out, op = self._out(out, dtype, self._per_expert(N, K), "out")
+        bp = None
+        if bias or out_bias is not None:
+            out_bias, bp = self._out(out_bias, dtype, self._per_expert(N), "out_bias")
+        abi._check(self._lib.moe_expert_wgrad(self._ref, dp, N, xp, K, op, bp, int(dtype == torch.float32),
+                                              self._stream()), "moe_expert_wgrad")
+        return out, out_bias
+
+    def act_backward(self, dy, *, act: str, saved: SavedLayer, out=None, a=None):
+        """The gradient through an activation whose input was saved:
+        dy * act'(saved) -> [rows, N].  ``a``, if given, receives act(saved)."""
+        code = _act(act)
+        if code == abi.MOE_ACT_NONE:
+            raise ValueError("act: 'none' has no backward pass")
+        N = saved.codes.shape[-1]
+        cols = N // 2 if code == abi.MOE_ACT_SWIGLU else N
+        dp = _check(dy, torch.bfloat16, (self.rows, cols), "dy", self.device)
+        sc, ss = self._saved(saved, N)
+        ap = self._opt(a, torch.bfloat16, (self.rows, cols), "a")
+        out, op = self._out(out, torch.bfloat16, (self.rows, N), "out")
+        abi._check(self._lib.moe_act_backward(self._ref, dp, N, code, sc, ss, op, ap, self._stream()),
+                   "moe_act_backward")
+        return out
+
+    def linear_backward(self, dy, x, w, *, act: str = "none", saved: SavedLayer | None = None, bias: bool = False,
+                        dtype=torch.bfloat16):
+        """(dx, dw, db) of ``linear``; with an activation, through the layer
+        it saved.  The residual's gradient is dy."""
+        if (saved is None) != (_act(act) == abi.MOE_ACT_NONE):
+            raise ValueError("act and saved go together")
+        du = dy if saved is None else self.act_backward(dy, act=act, saved=saved)
+        dx = self.dgrad(du, w)
+        dw, db = self.wgrad(du, x, bias=bias, dtype=dtype)
+        return dx, dw, db
+
+
+@dataclass
+class FFNGrads:
+    dx: torch.Tensor
+    dw1: torch.Tensor
+    dw2: torch.Tensor
+    db1: torch.Tensor | None = None
+    db2: torch.Tensor | None = None
+
+
+class ExpertFFN:
+    """The experts' network y = act(x w1^T + b1) w2^T + b2 over packed rows.
+
+    Between the passes only the activation's input is kept, in 8 bits
+    (1 + 1/32 bytes per value): the backward pass recomputes the activation
+    from it, in the same kernel that takes the gradient through it.  w1 is
+    [E, N, H], w2 [E, H, F] with N = F (2F for swiglu); without the expert
+    axis for one plain group."""
+
+    def __init__(self, rows: ExpertRows, w1, w2, *, b1=None, b2=None, act: str = "swiglu", dtype=torch.bfloat16):
+        N, H, _ = rows._weights(w1, torch.bfloat16)
+        H2, F, _ = rows._weights(w2, torch.bfloat16)
+        if _act(act) == abi.MOE_ACT_NONE:
+            raise ValueError("act: an expert network has an activation")
+        if H2 != H or N != (2 * F if act == "swiglu" else F):
+            raise ValueError(f"w1 {tuple(w1.shape)} and w2 {tuple(w2.shape)} do not fit together for act {act!r}")
+        self.rows, self.w1, self.w2, self.b1, self.b2, self.act, self.dtype = rows, w1, w2, b1, b2, act, dtype
+        bf16 = dict(dtype=torch.bfloat16, device=rows.device)
+        self.saved = rows.new_saved(N)
+        self.hidden = torch.empty((rows.rows, F), **bf16)   # act(u): forward, and again in the backward pass
+        self._du = None
+
+    def forward(self, x, *, residual=None, out=None):
+        """x [rows, H] -> [rows, H] (+ residual)."""
+        r = self.rows
+        r.linear(x, self.w1, bias=self.b1, act=self.act, saved=self.saved, out=self.hidden)
+        return r.linear(self.hidden, self.w2, bias=self.b2, residual=residual, out=out)
+
+    def backward(self, dy, x) -> FFNGrads:
+        """Gradients of the last forward pass; x is its input."""
+        r = self.rows
+        if self._du is None:
+            self._du = torch.empty(self.saved.codes.shape, dtype=torch.bfloat16, device=r.device)
+        du = r.dgrad(dy, self.w2, act=self.act, saved=self.saved, out=self._du, a=self.hidden)
+        dw2, db2 = r.wgrad(dy, self.hidden, bias=self.b2 is not None, dtype=self.dtype)
+        dx = r.dgrad(du, self.w1)
+        dw1, db1 = r.wgrad(du, x, bias=self.b1 is not None, dtype=self.dtype)
+        return FFNGrads(dx, dw1, dw2, db1, db2)
