@@ -24,6 +24,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "experts.h"
@@ -34,27 +35,41 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kEpiWarp = 4;      // first epilogue warp
-constexpr int kTileM = 128;      // rows of A per block
-constexpr int kChunk = 16;       // accumulator columns staged at a time
+constexpr int kThreads = 384;
+constexpr int kEpiWarp = 4;            // first epilogue warp; two groups of four follow
+constexpr int kTileM = 128;            // rows of A per block
 constexpr int kStageA = kTileM * 128;  // bytes
 
-constexpr int kLinear = 0, kDgrad = 1, kWgrad = 2;
+constexpr int kLinear = 0, kDgrad = 1, kWgrad = 2, kDgradSaved = 3;
+
+// accumulator columns (packed rows) that an epilogue group takes at a time
+__host__ __device__ constexpr int chunk(int MODE) { return MODE == kDgradSaved ? 16 : 32; }
+
+// Shared memory of one epilogue group.  A row of 128 output columns is padded
+// by 16 bytes (by 32 where it has 64, for swiglu), so that neighbouring rows
+// start in other banks.
+constexpr int kPitch = 272, kPitchGlu = 160, kPitchCode = 144;
+constexpr int kOutBytes = 32 * kPitch;
+constexpr int kCodeBytes = 32 * kPitchCode;
+__host__ __device__ constexpr int group_bytes(int MODE)
+{
+    return MODE == kWgrad        ? 0
+           : MODE == kDgradSaved ? 3 * 16 * kPitch + 2 * 16 * kPitchCode + 128
+                                 : kOutBytes + kCodeBytes + 256 + 1024;
+}
+constexpr int kControl = 4096;
 
 __host__ __device__ constexpr int stage_bytes(int CG, int BN) { return kStageA + BN / CG * 128; }
-constexpr int kStaging = 2 * kChunk * kTileM * 4;  // bytes
-constexpr int kControl = 4096;
-// ring depth: what is left of 227 KB beside the staging buffers, the barriers
-// and tile counts, and the alignment to 1 KB; at most 12 stages
-__host__ __device__ constexpr int stages(int CG, int BN)
+// ring depth: what is left of 227 KB beside the epilogue, the barriers and tile
+// counts, and the alignment to 1 KB; at most 12 stages
+__host__ __device__ constexpr int stages(int CG, int BN, int MODE)
 {
-    const int n = (227 * 1024 - kStaging - kControl - 1024) / stage_bytes(CG, BN);
+    const int n = (227 * 1024 - 2 * group_bytes(MODE) - kControl - 1024) / stage_bytes(CG, BN);
     return n > 12 ? 12 : n;
 }
-__host__ __device__ constexpr int smem_bytes(int CG, int BN)
+__host__ __device__ constexpr int smem_bytes(int CG, int BN, int MODE)
 {
-    return 1024 + stages(CG, BN) * stage_bytes(CG, BN) + kStaging + kControl;
+    return 1024 + stages(CG, BN, MODE) * stage_bytes(CG, BN) + 2 * group_bytes(MODE) + kControl;
 }
 __host__ __device__ constexpr int tmem_cols(int BN) { return 2 * BN < 32 ? 32 : 2 * BN; }
 
@@ -79,7 +94,7 @@ struct Control {
     uint64_t full[12], empty[12], acc_full[2], acc_empty[2], tail;
     uint32_t tmem;
     int abort;
-    int part[8];
+    int part[12];
     int row0[MOE_MAX_EXPERTS], rows[MOE_MAX_EXPERTS];  // of each expert, checked
     int tile0[MOE_MAX_EXPERTS + 1];                    // its first tile
 };
@@ -91,11 +106,11 @@ static_assert(sizeof(Control) <= kControl, "barriers and tile counts");
 __device__ __forceinline__ bool poll(uint64_t *bar, uint32_t parity, Control *c, void *ws)
 {
     for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_timer_ns();
     for (;;) {
         for (int i = 0; i < 16; ++i)
-            if (mbar_try_wait_cluster(bar, parity)) return true;
+            if (mbar_try_wait(bar, parity)) return true;
         if (*(volatile int *)&c->abort) return false;
         if (global_timer_ns() - t0 > kSpinLimitNs) {
             *(volatile int *)&c->abort = 1;
@@ -145,129 +160,334 @@ struct Walk {
     }
 };
 
-// Largest magnitude over 2^STEPS lanes, as bit patterns with the sign cleared
-// (a NaN is then larger than any value).
-template <int STEPS>
-__device__ __forceinline__ unsigned lane_max(unsigned bits)
-{
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 1 << i));
-    return bits;
-}
 __device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// What one lane keeps for the 4 accumulator rows (columns of the output) it
-// finishes in every row of a tile.
-struct LaneColumns {
-    int col;        // first output column (linear: of u; swiglu: of the gates)
-    bool on;
-    float bias[4];
-    float ws[4], wsum[4];
+__device__ __forceinline__ void group_sync(int g)
+{
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + g) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_bf16(unsigned char *p, float v)
+{
+    *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(v);
+}
+
+// `rows` rows of `units` 16-byte vectors from shared memory (row pitch
+// `pitch`) to global memory (row pitch `gpitch` bytes); vectors from `on` up
+// lie past the last column.  128 threads, tid in 0..127, at most ROWS rows.
+template <int UNITS, int ROWS>
+__device__ __forceinline__ void copy_out(const unsigned char *s, int pitch, void *gbase, size_t gpitch, int rows,
+                                         int on, int tid)
+{
+    unsigned char *g = static_cast<unsigned char *>(gbase);
+    const int c = tid % UNITS;
+#pragma unroll
+    for (int i = 0; i < (ROWS * UNITS + 127) / 128; ++i) {
+        const int r = tid / UNITS + i * (128 / UNITS);
+        if (r < rows && c < on)
+            *reinterpret_cast<uint4 *>(g + (size_t)r * gpitch + c * 16) =
+                *reinterpret_cast<const uint4 *>(s + r * pitch + c * 16);
+    }
+}
+// The other way, into registers (zeros past the edges), and on to shared memory.
+template <int UNITS, int ROWS>
+__device__ __forceinline__ void fetch(uint4 *v, const void *gbase, size_t gpitch, int rows, int on, int tid)
+{
+    const unsigned char *g = static_cast<const unsigned char *>(gbase);
+    const int c = tid % UNITS;
+#pragma unroll
+    for (int i = 0; i < (ROWS * UNITS + 127) / 128; ++i) {
+        const int r = tid / UNITS + i * (128 / UNITS);
+        v[i] = r < rows && c < on ? *reinterpret_cast<const uint4 *>(g + (size_t)r * gpitch + c * 16)
+                                  : make_uint4(0, 0, 0, 0);
+    }
+}
+template <int UNITS, int ROWS>
+__device__ __forceinline__ void place(const uint4 *v, unsigned char *s, int pitch, int tid)
+{
+    const int c = tid % UNITS;
+#pragma unroll
+    for (int i = 0; i < (ROWS * UNITS + 127) / 128; ++i)
+        *reinterpret_cast<uint4 *>(s + (tid / UNITS + i * (128 / UNITS)) * pitch + c * 16) = v[i];
+}
+
+// --------------------------------------------------------------------------
+// linear and plain dgrad.  A lane holds one accumulator row, i.e. one column
+// of u (swiglu: even lanes a gate, odd lanes its up), for 32 packed rows, so
+// bias, weight scale and activation need no memory in the loop.  Results go
+// through shared memory as bf16 and leave in whole row segments.
+// --------------------------------------------------------------------------
+template <bool FP8>
+struct LinearEpilogue {
+    const Params &p;
+    unsigned char *out, *codes;
+    float2 *xs;
+    unsigned *top;  // [4 warps][2][32]
+    int g, q, lane, tid;
+    // of a tile
+    int col0, cols;  // first output column of the block's tile, how many exist
+    float bias, ws, wsum;
+    uint4 res[4];
+
+    __device__ LinearEpilogue(const Params &p_, unsigned char *base, int g_, int q_, int lane_)
+        : p(p_), out(base), codes(base + kOutBytes), xs(reinterpret_cast<float2 *>(base + kOutBytes + kCodeBytes)),
+          top(reinterpret_cast<unsigned *>(base + kOutBytes + kCodeBytes + 256)), g(g_), q(q_), lane(lane_),
+          tid(q_ * 32 + lane_)
+    {
+    }
+    __device__ __forceinline__ int out_cols() const { return p.glu ? p.M / 2 : p.M; }
+
+    __device__ __forceinline__ void tile(int e, int m0)
+    {
+        const int n = out_cols();
+        col0 = p.glu ? m0 / 2 : m0;
+        cols = min(p.glu ? 64 : 128, n - col0);
+        const int c = p.glu ? q * 16 + lane / 2 : q * 32 + lane;
+        const size_t at = (size_t)e * p.M + (p.glu ? (lane & 1) * n : 0) + col0 + c;
+        bias = ws = wsum = 0.0f;
+        if (c < cols) {
+            if (p.bias) bias = __bfloat162float(p.bias[at]);
+            if (FP8) {
+                const float2 w = p.w_scales[at];
+                ws = w.x;
+                wsum = w.y;
+            }
+        }
+    }
+    // residual rows of a chunk, ahead of their use
+    __device__ __forceinline__ void ahead(int row, int rows)
+    {
+        if (!p.residual || rows <= 0) return;
+        const __nv_bfloat16 *at = p.residual + (size_t)row * out_cols() + col0;
+        if (p.glu) fetch<8, 32>(res, at, 2 * (size_t)out_cols(), rows, cols / 8, tid);
+        else fetch<16, 32>(res, at, 2 * (size_t)out_cols(), rows, cols / 8, tid);
+    }
+    __device__ __forceinline__ void finish(uint32_t (&v)[32], int row, int rows, int next_rows)
+    {
+        const int pitch = p.glu ? kPitchGlu : kPitch;
+        if (p.residual || FP8) {
+            if (p.residual) {
+                if (p.glu) place<8, 32>(res, out, pitch, tid);
+                else place<16, 32>(res, out, pitch, tid);
+                ahead(row + 64, next_rows);
+            }
+            if (FP8 && q == 0 && lane < rows) xs[lane] = p.x_scales[row + lane];
+            group_sync(g);
+        }
+        float u[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            u[i] = __uint_as_float(v[i]);
+            if (FP8) {
+                const float2 x = xs[i];
+                u[i] = fmaf(x.x, ws * u[i], x.y * wsum);
+            }
+            u[i] += bias;
+        }
+        if (p.saved) save(u, row, rows);
+        if (p.glu) {
+            // lanes 2i and 2i+1 hold gate and up of a column: of each two
+            // rows the even lane finishes the first, the odd lane the second
+            const bool odd = lane & 1;
+            unsigned char *o = out + (odd ? pitch : 0) + (q * 16 + lane / 2) * 2;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? u[i] : u[i + 1], 1);
+                const float gate = odd ? got : u[i], up = odd ? u[i + 1] : got;
+                float y = gate * logistic(gate) * up;
+                if (p.residual) y += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(o + i * pitch));
+                st_shared_bf16(o + i * pitch, y);
+            }
+        } else {
+            unsigned char *o = out + (q * 32 + lane) * 2;
+            if (p.act == MOE_ACT_SILU) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = act_value(u[i], MOE_ACT_SILU);
+            } else if (p.act == MOE_ACT_GELU) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = act_value(u[i], MOE_ACT_GELU);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (p.residual) u[i] += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(o + i * kPitch));
+                st_shared_bf16(o + i * kPitch, u[i]);
+            }
+        }
+        group_sync(g);
+        const size_t n = out_cols();
+        __nv_bfloat16 *y = p.y + (size_t)row * n + col0;
+        if (p.glu) copy_out<8, 32>(out, kPitchGlu, y, 2 * n, rows, cols / 8, tid);
+        else copy_out<16, 32>(out, kPitch, y, 2 * n, rows, cols / 8, tid);
+        if (p.saved) {
+            uint8_t *s = p.saved + (size_t)row * p.M + col0;
+            if (p.glu) {
+                copy_out<4, 32>(codes, kPitchCode, s, p.M, rows, cols / 16, tid);
+                copy_out<4, 32>(codes + 64, kPitchCode, s + n, p.M, rows, cols / 16, tid);
+            } else {
+                copy_out<8, 32>(codes, kPitchCode, s, p.M, rows, cols / 16, tid);
+            }
+        }
+        group_sync(g);
+    }
+    // u in 8 bits: the 32 columns of a block are the 32 lanes of a warp, or
+    // for swiglu every other lane of two warps
+    __device__ __forceinline__ void save(const float (&u)[32], int row, int rows)
+    {
+        if (p.glu) {
+            const bool odd = lane & 1;
+            const unsigned mask = odd ? 0xAAAAAAAAu : 0x55555555u;
+            unsigned keep0 = 0, keep1 = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const unsigned m = __reduce_max_sync(mask, mag(u[i]));
+                if (lane / 2 == (i & 15)) {
+                    if (i < 16) keep0 = m;
+                    else keep1 = m;
+                }
+            }
+            unsigned *mine = top + (q * 2 + (lane & 1)) * 32;
+            mine[lane / 2] = keep0;
+            mine[16 + lane / 2] = keep1;
+            group_sync(g);
+            const unsigned *pair = top + ((q & 2) * 2 + (lane & 1)) * 32;  // warps q & 2 and (q & 2) + 1
+            uint8_t *c = codes + (odd ? 64 : 0) + q * 16 + lane / 2;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float i0 = saved_inverse(saved_byte(max(pair[i], pair[64 + i])));
+                const float i1 = saved_inverse(saved_byte(max(pair[i + 1], pair[64 + i + 1])));
+                const unsigned two = e4m3_pair(u[i] * i0, u[i + 1] * i1);
+                c[i * kPitchCode] = (uint8_t)two;
+                c[(i + 1) * kPitchCode] = (uint8_t)(two >> 8);
+            }
+            // 2 blocks of gates and 2 of ups for 32 rows: one byte a thread
+            const int r = tid & 31, b = tid >> 5, half = b & 1, side = b >> 1;
+            if (r < rows && half * 32 < cols) {
+                const unsigned *t = top + (half * 4 + side) * 32 + r;
+                p.saved_scales[(size_t)(row + r) * (p.M / 32) + (side * out_cols() + col0) / 32 + half] =
+                    (uint8_t)saved_byte(max(t[0], t[64]));
+            }
+        } else {
+            unsigned keep = 0;
+            uint8_t *c = codes + q * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const unsigned b0 = saved_byte(__reduce_max_sync(0xFFFFFFFFu, mag(u[i])));
+                const unsigned b1 = saved_byte(__reduce_max_sync(0xFFFFFFFFu, mag(u[i + 1])));
+                const unsigned two = e4m3_pair(u[i] * saved_inverse(b0), u[i + 1] * saved_inverse(b1));
+                c[i * kPitchCode] = (uint8_t)two;
+                c[(i + 1) * kPitchCode] = (uint8_t)(two >> 8);
+                if (lane == i) keep = b0;
+                if (lane == i + 1) keep = b1;
+            }
+            if (lane < rows && q * 32 < cols)
+                p.saved_scales[(size_t)(row + lane) * (p.M / 32) + col0 / 32 + q] = (uint8_t)keep;
+        }
+    }
 };
 
 // --------------------------------------------------------------------------
-// linear: one output row r, four values of u (swiglu: gate, up, gate, up)
+// dgrad through a saved layer.  A lane holds one column of d for 16 packed
+// rows; the codes of that column come through shared memory, and up to three
+// results (du, for swiglu of gate and up, and the activation) leave through it.
 // --------------------------------------------------------------------------
-template <bool FP8>
-__device__ __forceinline__ void finish_linear(const Params &p, const LaneColumns &lc, int r, float4 v, int lane)
-{
-    float u[4] = {v.x, v.y, v.z, v.w};
-    if (FP8) {
-        const float2 xs = p.x_scales[r];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = fmaf(xs.x, lc.ws[i] * u[i], xs.y * lc.wsum[i]);
+struct SavedEpilogue {
+    const Params &p;
+    unsigned char *out, *codes;
+    uint8_t *scale;  // [16 rows][4 gate blocks, 4 up blocks]
+    int g, q, lane, tid;
+    int col0, cols;
+    uint4 pre[2];
+    unsigned pre_scale;
+
+    __device__ SavedEpilogue(const Params &p_, unsigned char *base, int g_, int q_, int lane_)
+        : p(p_), out(base), codes(base + 3 * 16 * kPitch), scale(base + 3 * 16 * kPitch + 2 * 16 * kPitchCode), g(g_),
+          q(q_), lane(lane_), tid(q_ * 32 + lane_)
+    {
     }
+    __device__ __forceinline__ bool glu() const { return p.act == MOE_ACT_SWIGLU; }
+    __device__ __forceinline__ size_t saved_cols() const { return glu() ? 2 * (size_t)p.M : p.M; }
+    __device__ __forceinline__ void tile(int, int m0)
+    {
+        col0 = m0;
+        cols = min(128, p.M - m0);
+    }
+    __device__ __forceinline__ void ahead(int row, int rows)
+    {
+        if (rows <= 0) return;
+        const size_t C = saved_cols();
+        const uint8_t *s = p.saved + (size_t)row * C + col0;
+        fetch<8, 16>(pre, s, C, rows, cols / 16, tid);
+        if (glu()) fetch<8, 16>(pre + 1, s + p.M, C, rows, cols / 16, tid);
+        const int r = tid >> 3, b = tid & 3, up = (tid >> 2) & 1;
+        pre_scale = 0;
+        if (r < rows && b * 32 < cols && (glu() || !up))
+            pre_scale = p.saved_scales[(size_t)(row + r) * (C / 32) + (up * p.M + col0) / 32 + b];
+    }
+    __device__ __forceinline__ void finish(uint32_t (&v)[16], int row, int rows, int next_rows)
+    {
+        place<8, 16>(pre, codes, kPitchCode, tid);
+        if (glu()) place<8, 16>(pre + 1, codes + 16 * kPitchCode, kPitchCode, tid);
+        scale[tid] = (uint8_t)pre_scale;
+        ahead(row + 32, next_rows);
+        group_sync(g);
+        const uint8_t *c = codes + q * 32 + lane;
+        unsigned char *o = out + (q * 32 + lane) * 2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] += lc.bias[i];
-    const int out = p.glu ? p.M / 2 : p.M;
-    if (p.saved) {
-        if (p.glu) {  // 32 gates (and their ups) lie in 16 lanes
-            const unsigned bg = saved_byte(lane_max<4>(lc.on ? max(mag(u[0]), mag(u[2])) : 0u));
-            const unsigned bu = saved_byte(lane_max<4>(lc.on ? max(mag(u[1]), mag(u[3])) : 0u));
-            if (lc.on) {
-                const float ig = saved_inverse(bg), iu = saved_inverse(bu);
-                uint8_t *s = p.saved + (size_t)r * p.M + lc.col;
-                *reinterpret_cast<uint16_t *>(s) = (uint16_t)e4m3_pair(u[0] * ig, u[2] * ig);
-                *reinterpret_cast<uint16_t *>(s + out) = (uint16_t)e4m3_pair(u[1] * iu, u[3] * iu);
-                if ((lane & 15) == 0) {
-                    uint8_t *b = p.saved_scales + (size_t)r * (p.M / 32) + lc.col / 32;
-                    b[0] = (uint8_t)bg;
-                    b[out / 32] = (uint8_t)bu;
+        for (int i = 0; i < 16; i += 2) {
+            const float2 x = e4m3_decode2(c[i * kPitchCode] | ((unsigned)c[(i + 1) * kPitchCode] << 8));
+            const float u[2] = {x.x * saved_scale(scale[i * 8 + q]), x.y * saved_scale(scale[i * 8 + 8 + q])};
+            const float d[2] = {__uint_as_float(v[i]), __uint_as_float(v[i + 1])};
+            if (glu()) {
+                const uint8_t *cu = c + 16 * kPitchCode;
+                const float2 z = e4m3_decode2(cu[i * kPitchCode] | ((unsigned)cu[(i + 1) * kPitchCode] << 8));
+                const float up[2] = {z.x * saved_scale(scale[i * 8 + 4 + q]),
+                                     z.y * saved_scale(scale[i * 8 + 12 + q])};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float s = logistic(u[j]), silu = u[j] * s;
+                    unsigned char *at = o + (i + j) * kPitch;
+                    st_shared_bf16(at, d[j] * up[j] * (s * (1.0f + u[j] * (1.0f - s))));
+                    st_shared_bf16(at + 16 * kPitch, d[j] * silu);
+                    if (p.a) st_shared_bf16(at + 32 * kPitch, silu * up[j]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    unsigned char *at = o + (i + j) * kPitch;
+                    st_shared_bf16(at, d[j] * act_slope(u[j], p.act));
+                    if (p.a) st_shared_bf16(at + 32 * kPitch, act_value(u[j], p.act));
                 }
             }
-        } else {
-            const unsigned m4 = max(max(mag(u[0]), mag(u[1])), max(mag(u[2]), mag(u[3])));
-            const unsigned by = saved_byte(lane_max<3>(lc.on ? m4 : 0u));
-            if (lc.on) {
-                const float inv = saved_inverse(by);
-                *reinterpret_cast<unsigned *>(p.saved + (size_t)r * p.M + lc.col) =
-                    e4m3_pair(u[0] * inv, u[1] * inv) | (e4m3_pair(u[2] * inv, u[3] * inv) << 16);
-                if ((lane & 7) == 0) p.saved_scales[(size_t)r * (p.M / 32) + lc.col / 32] = (uint8_t)by;
-            }
         }
+        group_sync(g);
+        const size_t C = saved_cols();
+        __nv_bfloat16 *y = p.y + (size_t)row * C + col0;
+        copy_out<16, 16>(out, kPitch, y, 2 * C, rows, cols / 8, tid);
+        if (glu()) copy_out<16, 16>(out + 16 * kPitch, kPitch, y + p.M, 2 * C, rows, cols / 8, tid);
+        if (p.a)
+            copy_out<16, 16>(out + 32 * kPitch, kPitch, p.a + (size_t)row * p.M + col0, 2 * (size_t)p.M, rows,
+                             cols / 8, tid);
+        group_sync(g);
     }
-    if (!lc.on) return;
-    const size_t at = (size_t)r * out + lc.col;
-    if (p.glu) {
-        float y0 = act_value(u[0], MOE_ACT_SILU) * u[1], y1 = act_value(u[2], MOE_ACT_SILU) * u[3];
-        if (p.residual) {
-            const unsigned q = *reinterpret_cast<const unsigned *>(p.residual + at);
-            y0 += bf16lo(q);
-            y1 += bf16hi(q);
-        }
-        *reinterpret_cast<unsigned *>(p.y + at) = pack_bf16(y0, y1);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = act_value(u[i], p.act);
-        if (p.residual) {
-            const uint2 q = *reinterpret_cast<const uint2 *>(p.residual + at);
-            u[0] += bf16lo(q.x);
-            u[1] += bf16hi(q.x);
-            u[2] += bf16lo(q.y);
-            u[3] += bf16hi(q.y);
-        }
-        *reinterpret_cast<uint2 *>(p.y + at) = pack_bf16x4(u);
-    }
-}
+};
 
-// --------------------------------------------------------------------------
-// dgrad: one row r, four columns of d, plain or through the saved layer
-// --------------------------------------------------------------------------
-__device__ __forceinline__ void finish_dgrad(const Params &p, const LaneColumns &lc, int r, float4 v)
+// 32 consecutive values of a row of dw, `n` of them (a multiple of 8) inside it.
+__device__ __forceinline__ void store_row(const Params &p, size_t at, const uint32_t (&v)[32], int n)
 {
-    if (!lc.on) return;
-    const float d[4] = {v.x, v.y, v.z, v.w};
-    const size_t at = (size_t)r * p.M + lc.col;
-    if (p.act == MOE_ACT_NONE) {
-        *reinterpret_cast<uint2 *>(p.y + at) = pack_bf16x4(d);
+    if (p.fp32) {
+        float *o = static_cast<float *>(p.dw) + at;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+            if (j < n) *reinterpret_cast<uint4 *>(o + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         return;
     }
-    const size_t C = p.act == MOE_ACT_SWIGLU ? 2 * (size_t)p.M : p.M;
-    const uint8_t *s = p.saved + r * C + lc.col;
-    const uint8_t *b = p.saved_scales + r * (C / 32) + lc.col / 32;
-    __nv_bfloat16 *o = p.y + r * C + lc.col;
-    float u[4], du[4], av[4];
-    saved_decode4(*reinterpret_cast<const unsigned *>(s), saved_scale(b[0]), u);
-    if (p.act == MOE_ACT_SWIGLU) {
-        float up[4], dup[4];
-        saved_decode4(*reinterpret_cast<const unsigned *>(s + p.M), saved_scale(b[p.M / 32]), up);
+    uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float q = logistic(u[i]), silu = u[i] * q;
-            du[i] = d[i] * up[i] * (q * (1.0f + u[i] * (1.0f - q)));
-            dup[i] = d[i] * silu;
-            av[i] = silu * up[i];
-        }
-        *reinterpret_cast<uint2 *>(o + p.M) = pack_bf16x4(dup);
-    } else {
+    for (int j = 0; j < 16; ++j) w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.dw) + at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            du[i] = d[i] * act_slope(u[i], p.act);
-            av[i] = act_value(u[i], p.act);
-        }
-    }
-    *reinterpret_cast<uint2 *>(o) = pack_bf16x4(du);
-    if (p.a) *reinterpret_cast<uint2 *>(p.a + at) = pack_bf16x4(av);
+    for (int j = 0; j < 4; ++j)
+        if (j * 8 < n) *reinterpret_cast<uint4 *>(o + j * 8) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
 // --------------------------------------------------------------------------
@@ -276,7 +496,7 @@ __device__ __forceinline__ void finish_dgrad(const Params &p, const LaneColumns 
 template <int CG, int BN, int MODE, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ Params p)
 {
-    constexpr int kStages = stages(CG, BN);
+    constexpr int kStages = stages(CG, BN, MODE);
     constexpr int kStage = stage_bytes(CG, BN);
     constexpr int kHalfN = BN / CG;  // rows of B per block
     constexpr int kBM = kTileM * CG;
@@ -286,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    float *stg = reinterpret_cast<float *>(smem + kStages * kStage);
-    Control *c = reinterpret_cast<Control *>(smem + kStages * kStage + kStaging);
+    unsigned char *stg = smem + kStages * kStage;
+    Control *c = reinterpret_cast<Control *>(stg + 2 * group_bytes(MODE));
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0u;
@@ -299,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->acc_full[i], 1);
-            mbar_init(&c->acc_empty[i], 4 * CG);
+            mbar_init(&c->acc_empty[i], 8 * CG);
         }
         mbar_init(&c->tail, 1);
         c->abort = 0;
@@ -395,13 +615,13 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                         mbar_arrive_expect_tx(&c->tail, kStage);
                         bar = cluster_addr(&c->tail, rank);
                     } else {
-                        mbar_arrive_expect_tx_cluster(full, kStage);
+                        mbar_arrive_expect_tx_remote(full, kStage);
                     }
                     const int k0 = i * kElems;
                     if (MODE == kLinear) {
                         tma_load_4d<CG>(sa, &p.ma, k0, 0, p.glu ? m0 / 2 : m0, t.e, bar);
                         tma_load_2d<CG>(sb, &p.mb, k0, t.row0 + n0, bar);
-                    } else if (MODE == kDgrad) {
+                    } else if (MODE == kDgrad || MODE == kDgradSaved) {
                         for (int j = 0; j < 2; ++j)
                             tma_load_4d<CG>(sa + j * 8192, &p.ma, m0 + 64 * j, k0, t.e, 0, bar);
                         tma_load_2d<CG>(sb, &p.mb, k0, t.row0 + n0, bar);
@@ -423,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                             *reinterpret_cast<uint4 *>(sa + j * 8192 + o) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(full);
+                    if (lane == 0) mbar_arrive_release_cluster(full);
                 }
                 if (++s == kStages) {
                     s = 0;
@@ -457,6 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             for (int i = 0; i < iters; ++i) {
                 ok = wait(&c->full[s], ph, c, p.ws);
                 if (!ok) break;
+                // the zeroed rows of a tail come from the peer's generic writes too
+                if (MODE == kWgrad && CG == 2 && i == iters - 1) fence_cluster();
                 tc_fence_after();
                 if (lane == 0) {
                     const uint32_t sa = smem_addr(smem + s * kStage);
@@ -478,92 +700,65 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         }
     } else if (warp >= kEpiWarp) {
         // ---- epilogue ------------------------------------------------------
-        const int q = warp - kEpiWarp;  // == warp % 4: the lanes of tensor memory it may read
-        int acc = 0, buf = 0;
+        // Two groups of four warps take the chunks of a tile in turn.
+        constexpr int kChunk = chunk(MODE);
+        const int q = warp & 3, g = (warp - kEpiWarp) >> 2;  // q: the lanes of tensor memory a warp may read
+        int acc = 0, turn = 0;
         uint32_t aph = 0;
+        using Epilogue = std::conditional_t<MODE == kDgradSaved, SavedEpilogue, LinearEpilogue<FP8>>;
+        Epilogue ep(p, stg + g * group_bytes(MODE), g, q, lane);
         while (walk.next(t)) {
             const int iters = iterations(t);
             const int m0 = t.m * kBM + (int)rank * kTileM, n0 = t.n * BN;
             const int cols = min(BN, (MODE == kWgrad ? p.N : t.rows) - n0);
+            const int c_first = ((g + turn) & 1) * kChunk;
+            turn += (cols + kChunk - 1) / kChunk;
+            const int row0 = t.row0 + n0;
+            if (MODE != kWgrad) {
+                ep.tile(t.e, m0);
+                ep.ahead(row0 + c_first, min(kChunk, cols - c_first));
+            }
             if (iters != 0) {
                 // all four warps go on, or none
                 const bool ok = wait(&c->acc_full[acc], aph, c, p.ws);
                 int all;
                 asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                             "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                             "barrier.cta.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                              : "=r"(all)
-                             : "r"((int)ok)
+                             : "r"((int)ok), "r"(1 + g)
                              : "memory");
                 if (!all) break;
                 tc_fence_after();
             }
             const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + acc * BN;
-            LaneColumns lc;
-            if (MODE != kWgrad) {
-                lc.col = p.glu ? m0 / 2 + 2 * lane : m0 + 4 * lane;
-                const int half = p.M / 2;
-                lc.on = lc.col < (p.glu ? half : p.M);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = p.glu ? (i & 1) * half + lc.col + (i >> 1) : lc.col + i;
-                    const size_t at = (size_t)t.e * p.M + row;
-                    lc.bias[i] = MODE == kLinear && p.bias && lc.on ? __bfloat162float(p.bias[at]) : 0.0f;
-                    const float2 w = FP8 && lc.on ? p.w_scales[at] : make_float2(0.0f, 0.0f);
-                    lc.ws[i] = w.x;
-                    lc.wsum[i] = w.y;
-                }
-            }
-            for (int c0 = 0; c0 < cols; c0 += kChunk) {
+            bool released = iters == 0;
+            for (int c0 = c_first; c0 < cols; c0 += 2 * kChunk) {
                 uint32_t v[kChunk];
                 if (iters != 0) {
-                    tmem_ld16(from + c0, v);
+                    tmem_ld(from + c0, v);
                     tmem_wait_ld();
-                    if (c0 + kChunk >= cols) {  // the accumulator is free again
+                    if (c0 + 2 * kChunk >= cols) {  // this warp's last look at the accumulator
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(cluster_addr(&c->acc_empty[acc], 0));
+                        if (lane == 0) mbar_arrive_remote(cluster_addr(&c->acc_empty[acc], 0));
+                        released = true;
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) v[i] = 0u;
                 }
-                if (MODE == kWgrad) {
-                    // lane = one row of dw, 16 consecutive values of it
+                if constexpr (MODE == kWgrad) {
+                    // lane = one row of dw, 32 consecutive values of it
                     const int m = m0 + q * 32 + lane;
-                    if (m < p.M) {
-                        const size_t at = ((size_t)t.e * p.M + m) * p.N + n0 + c0;
-#pragma unroll
-                        for (int j = 0; j < kChunk; j += 8) {
-                            if (c0 + j >= cols) break;
-                            float f[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[j + i]);
-                            if (p.fp32) {
-                                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.dw) + at + j);
-                                o[0] = make_float4(f[0], f[1], f[2], f[3]);
-                                o[1] = make_float4(f[4], f[5], f[6], f[7]);
-                            } else {
-                                const uint2 lo = pack_bf16x4(f), hi = pack_bf16x4(f + 4);
-                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.dw) + at + j) =
-                                    make_uint4(lo.x, lo.y, hi.x, hi.y);
-                            }
-                        }
-                    }
+                    if (m < p.M) store_row(p, ((size_t)t.e * p.M + m) * p.N + n0 + c0, v, min(kChunk, cols - c0));
+                    __syncwarp();
                 } else {
-                    // lane = one column of the output, 16 rows: transposed
-                    // through shared memory, then a warp finishes whole rows
-                    float *b = stg + buf * (kChunk * kTileM);
-                    buf ^= 1;
-#pragma unroll
-                    for (int i = 0; i < kChunk; ++i) b[i * kTileM + q * 32 + lane] = __uint_as_float(v[i]);
-                    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-                    for (int i = q; i < kChunk && c0 + i < cols; i += 4) {
-                        const float4 u = *reinterpret_cast<const float4 *>(b + i * kTileM + lane * 4);
-                        const int r = t.row0 + n0 + c0 + i;
-                        if (MODE == kLinear) finish_linear<FP8>(p, lc, r, u, lane);
-                        else finish_dgrad(p, lc, r, u);
-                    }
+                    ep.finish(v, row0 + c0, min(kChunk, cols - c0), min(kChunk, cols - c0 - 2 * kChunk));
                 }
+            }
+            if (!released) {  // no chunk of this tile was this group's
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(cluster_addr(&c->acc_empty[acc], 0));
             }
             if (iters != 0) {
                 acc ^= 1;
@@ -635,7 +830,7 @@ cudaError_t launch(const Params &p, cudaStream_t s)
     // No programmatic dependent launch here: the kernel takes whole SMs and
     // their tensor memory, so the next one has nowhere to start early.
     const auto fn = experts_kernel<CG, BN, MODE, FP8>;
-    cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes(CG, BN));
+    cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes(CG, BN, MODE));
     if (err != cudaSuccess) return err;
     // the most tiles that offsets over these rows can give
     const long long tm = (p.M + kTileM * CG - 1) / (kTileM * CG);
@@ -648,7 +843,7 @@ cudaError_t launch(const Params &p, cudaStream_t s)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks * CG));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes(CG, BN);
+    cfg.dynamicSmemBytes = smem_bytes(CG, BN, MODE);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -733,6 +928,10 @@ cudaError_t launch_expert_dgrad(const moe_rows *G, const void *dy, int N, const 
     cudaError_t err = encode(&p.ma, false, w, 4, d, st, b);
     if (err == cudaSuccess) err = encode_rows(&p.mb, false, dy, N, G->rows, 64, bn / cg);
     if (err != cudaSuccess) return err;
+    if (act != MOE_ACT_NONE)
+        return bn == 32    ? launch<1, 32, kDgradSaved, false>(p, s)
+               : bn == 128 ? launch<1, 128, kDgradSaved, false>(p, s)
+                           : launch<2, 256, kDgradSaved, false>(p, s);
     return bn == 32    ? launch<1, 32, kDgrad, false>(p, s)
            : bn == 128 ? launch<1, 128, kDgrad, false>(p, s)
                        : launch<2, 256, kDgrad, false>(p, s);
