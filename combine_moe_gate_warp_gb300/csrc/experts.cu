@@ -662,42 +662,55 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         }
     } else if (warp == 1 && rank == 0) {
         // ---- matrix instructions ------------------------------------------
-        constexpr uint32_t kLeadA = kMnA ? 8192 : 16, kLeadB = kMnB ? 8192 : 16;
-        constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
-        int s = 0, acc = 0;
-        uint32_t ph = 0, aph = 0;
-        bool ok = true;
-        while (ok && walk.next(t)) {
-            const int iters = iterations(t);
-            if (iters == 0) continue;
-            const uint32_t idesc = mma_idesc(FP8, kMnA, kMnB, kBM, width(t));
-            ok = wait(&c->acc_empty[acc], aph ^ 1, c, p.ws);
-            if (!ok) break;
-            tc_fence_after();
-            for (int i = 0; i < iters; ++i) {
-                ok = wait(&c->full[s], ph, c, p.ws);
+        // One thread.  It looks at the next stage's barrier before it issues
+        // the current stage's instructions: the answer (about 100 cycles) is
+        // there when the issue, which blocks while the tensor cores' queue is
+        // full, has gone through.
+        if (lane == 0) {
+            constexpr uint32_t kLeadA = kMnA ? 8192 : 16, kLeadB = kMnB ? 8192 : 16;
+            constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
+            const uint64_t da0 = smem_desc(smem_addr(smem), kLeadA, 1024);
+            const uint64_t db0 = smem_desc(smem_addr(smem) + kStageA, kLeadB, 1024);
+            int s = 0, acc = 0;
+            uint32_t ph = 0, aph = 0;
+            bool ok = true, ready = false, more = walk.next(t);
+            while (more) {
+                const int iters = iterations(t);
+                if (iters == 0) {
+                    more = walk.next(t);
+                    continue;
+                }
+                const uint32_t idesc = mma_idesc(FP8, kMnA, kMnB, kBM, width(t));
+                const uint32_t d = tmem + acc * BN;
+                ok = poll(&c->acc_empty[acc], aph ^ 1, c, p.ws);
                 if (!ok) break;
-                // the zeroed rows of a tail come from the peer's generic writes too
-                if (MODE == kWgrad && CG == 2 && i == iters - 1) fence_cluster();
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t sa = smem_addr(smem + s * kStage);
-                    const uint64_t da = smem_desc(sa, kLeadA, 1024), db = smem_desc(sa + kStageA, kLeadB, 1024);
+                for (int i = 0; i < iters; ++i) {
+                    ok = ready || poll(&c->full[s], ph, c, p.ws);
+                    if (!ok) break;
+                    // the zeroed rows of a tail come from the peer's generic writes too
+                    if (MODE == kWgrad && CG == 2 && i == iters - 1) mbar_try_wait_acquire_cluster(&c->full[s], ph);
+                    tc_fence_after();
+                    const int now = s;
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                    ready = mbar_try_wait(&c->full[s], ph);
+                    const uint64_t da = da0 + (uint64_t)(now * (kStage >> 4)), db = db0 + (uint64_t)(now * (kStage >> 4));
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ss<CG, FP8>(tmem + acc * BN, da + k * kStepA, db + k * kStepB, idesc, (i | k) != 0);
-                    mma_commit<CG>(&c->empty[s]);
-                    if (i == iters - 1) mma_commit<CG>(&c->acc_full[acc]);
+                        mma_ss<CG, FP8>(d, da + k * kStepA, db + k * kStepB, idesc, (i | k) != 0);
+                    mma_commit<CG>(&c->empty[now]);
+                    if (i == 0) more = walk.next(t);  // the divisions of the next tile hide behind this one
                 }
-                __syncwarp();
-                if (++s == kStages) {
-                    s = 0;
-                    ph ^= 1;
-                }
+                if (!ok) break;
+                mma_commit<CG>(&c->acc_full[acc]);
+                acc ^= 1;
+                aph ^= acc == 0;
             }
-            acc ^= 1;
-            aph ^= acc == 0;
         }
+        __syncwarp();
     } else if (warp >= kEpiWarp) {
         // ---- epilogue ------------------------------------------------------
         // Two groups of four warps take the chunks of a tile in turn.
