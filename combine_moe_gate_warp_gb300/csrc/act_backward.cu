@@ -1,10 +1,10 @@
-// experts_elementwise.cu -- beside the expert products: the gradient through
-// an activation whose input was saved in 8 bits, and the bias gradient.  Both
-// are bound by HBM: each value is read once and written once.
+// act_backward.cu -- beside the expert products: the gradient through
+// an activation whose input was saved in 8 bits, where no product precedes it
+// to take it into its epilogue.  Bound by HBM: each value is read once and
+// written once.
 #include "activation.cuh"
 #include "experts.h"
 #include "launchers.h"
-#include "umma.cuh"
 
 namespace moe {
 
@@ -84,67 +84,6 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const __nv_bfloat16 *
     }
 }
 
-// db[e, n] = sum of dy[r, n] over the expert's rows.  A cluster of 8 blocks
-// takes 256 columns of one expert: each warp adds every 64th row (8 columns
-// per lane), the block adds its warps, block 0 of the cluster adds the blocks
-// over distributed shared memory.  The order is fixed by the sizes.
-constexpr int kSumBlocks = 8;
-__global__ void __cluster_dims__(kSumBlocks, 1, 1) __launch_bounds__(256)
-    row_sums_kernel(const __nv_bfloat16 *dy, int N, void *db, int fp32, const int32_t *offsets, int E, int rows,
-                    void *ws)
-{
-    __shared__ float part[8][256];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_cta_rank(), e = blockIdx.y, col0 = (int)(blockIdx.x / kSumBlocks) * 256;
-    int lo = offsets ? offsets[e] : 0, hi = offsets ? offsets[e + 1] : rows;
-    // an offset below an earlier one would give rows to two experts
-    const bool low = offsets && (int)threadIdx.x <= e && lo < max(0, offsets[threadIdx.x]);
-    if (__syncthreads_or(low) || hi < lo || hi > rows) {
-        if (threadIdx.x == 0) record_status(ws, MOE_ERR_DEVICE_DATA);
-        lo = hi = 0;
-    }
-    const int col = col0 + lane * 8;
-    float s[8] = {};
-    if (col < N) {
-#pragma unroll 4
-        for (int r = lo + rank * 8 + warp; r < hi; r += 8 * kSumBlocks) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(dy + (size_t)r * N + col);
-            s[0] += bf16lo(v.x);
-            s[1] += bf16hi(v.x);
-            s[2] += bf16lo(v.y);
-            s[3] += bf16hi(v.y);
-            s[4] += bf16lo(v.z);
-            s[5] += bf16hi(v.z);
-            s[6] += bf16lo(v.w);
-            s[7] += bf16hi(v.w);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) part[warp][lane * 8 + i] = s[i];
-    __syncthreads();
-    float sum = 0.0f;
-    for (int i = 0; i < 8; ++i) sum += part[i][threadIdx.x];
-    __syncthreads();
-    part[0][threadIdx.x] = sum;
-    cluster_sync_all();
-    if (rank == 0 && col0 + (int)threadIdx.x < N) {
-        sum = 0.0f;
-        for (int i = 0; i < kSumBlocks; ++i) {
-            float v;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                         : "=f"(v)
-                         : "r"(cluster_addr(&part[0][threadIdx.x], (uint32_t)i))
-                         : "memory");
-            sum += v;
-        }
-        const size_t at = (size_t)e * N + col0 + threadIdx.x;
-        if (fp32) static_cast<float *>(db)[at] = sum;
-        else static_cast<__nv_bfloat16 *>(db)[at] = __float2bfloat16_rn(sum);
-    }
-    __syncwarp();
-    cluster_sync_all();  // the peers' shared memory stays until it has been read
-}
-
 }  // namespace
 
 cudaError_t launch_act_backward(const moe_rows *G, const void *dy, int N, int act, const void *saved,
@@ -159,15 +98,6 @@ cudaError_t launch_act_backward(const moe_rows *G, const void *dy, int N, int ac
         static_cast<const __nv_bfloat16 *>(dy), out, act, static_cast<const uint8_t *>(saved),
         static_cast<const uint8_t *>(saved_scales), static_cast<__nv_bfloat16 *>(du),
         static_cast<__nv_bfloat16 *>(a), G->offsets, G->E, G->rows, G->ws);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_row_sums(const moe_rows *G, const void *dy, int N, void *db, int fp32, cudaStream_t s)
-{
-    if (G->rows == 0) return cudaMemsetAsync(db, 0, (size_t)G->E * N * (fp32 ? 4 : 2), s);
-    const dim3 grid((unsigned)((N + 255) / 256 * kSumBlocks), (unsigned)G->E);
-    row_sums_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(dy), N, db, fp32, G->offsets, G->E,
-                                         G->rows, G->ws);
     return cudaGetLastError();
 }
 

@@ -45,7 +45,7 @@ constexpr int kLinear = 0, kDgrad = 1, kWgrad = 2, kDgradSaved = 3;
 // accumulator columns (packed rows) that an epilogue group takes at a time
 __host__ __device__ constexpr int chunk(int MODE) { return MODE == kDgradSaved ? 16 : 32; }
 
-// Shared memory of one epilogue group.  A row of 128 output columns is padded
+// Shared memory of one epilogue group (wgrad: of the bias sums' ones).  A row of 128 output columns is padded
 // by 16 bytes (by 32 where it has 64, for swiglu), so that neighbouring rows
 // start in other banks.
 constexpr int kPitch = 272, kPitchGlu = 160, kPitchCode = 144;
@@ -53,7 +53,7 @@ constexpr int kOutBytes = 32 * kPitch;
 constexpr int kCodeBytes = 32 * kPitchCode;
 __host__ __device__ constexpr int group_bytes(int MODE)
 {
-    return MODE == kWgrad        ? 0
+    return MODE == kWgrad        ? 1024
            : MODE == kDgradSaved ? 3 * 16 * kPitch + 2 * 16 * kPitchCode + 128
                                  : kOutBytes + kCodeBytes + 256 + 1024;
 }
@@ -86,12 +86,12 @@ struct Params {
     const __nv_bfloat16 *bias, *residual;
     const float2 *x_scales, *w_scales;
     __nv_bfloat16 *y, *a;
-    void *dw;
+    void *dw, *db;
     uint8_t *saved, *saved_scales;
 };
 
 struct Control {
-    uint64_t full[12], empty[12], acc_full[2], acc_empty[2], tail;
+    uint64_t full[12], empty[12], tail[12], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int abort;
     int part[12];
@@ -516,18 +516,23 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&c->full[i], CG);
             mbar_init(&c->empty[i], 1);
+            mbar_init(&c->tail[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->acc_full[i], 1);
             mbar_init(&c->acc_empty[i], 8 * CG);
         }
-        mbar_init(&c->tail, 1);
         c->abort = 0;
         mbar_fence_init();
         tmap_prefetch(&p.ma);
         tmap_prefetch(&p.mb);
     }
     if (warp == 2) tmem_alloc<CG>(&c->tmem, tmem_cols(BN));
+    if (MODE == kWgrad && tid < 128) {
+        // the bias sums' B operand: 2 KB of bf16 ones (any layout of them is the same)
+        reinterpret_cast<uint4 *>(stg)[tid] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        fence_proxy_async_smem();
+    }
 
     // rows and first tile of every expert: thread e looks at expert e
     const int tm = (p.M + kBM - 1) / kBM;
@@ -556,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 if (blockIdx.x == 0) record_status(p.ws, MOE_ERR_DEVICE_DATA);
                 lo = hi = 0;
             }
-            tiles = tm * (((MODE == kWgrad ? p.N : hi - lo) + BN - 1) / BN);
+            tiles = tm * (((MODE == kWgrad ? p.N : hi - lo) + BN - 1) / BN + (MODE == kWgrad && p.db ? 1 : 0));
             c->row0[tid] = lo;
             c->rows[tid] = hi - lo;
         }
@@ -584,8 +589,13 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     const auto iterations = [&](const Tile &q) {
         return MODE == kWgrad ? (q.rows + 63) / 64 : (p.K + 127) / 128;
     };
+    // wgrad: the tile after the last of n is the bias gradient's, the product
+    // of dy^T with ones: no rows of x to load, 16 columns (32 for a pair)
+    const int tn_bias = MODE == kWgrad ? (p.N + BN - 1) / BN : -1;
+    const auto is_bias = [&](const Tile &q) { return MODE == kWgrad && q.n == tn_bias; };
     // columns of the accumulator in use: what is left of the ragged axis
     const auto width = [&](const Tile &q) {
+        if (is_bias(q)) return kStepN;
         const int left = (MODE == kWgrad ? p.N : q.rows) - q.n * BN;
         return min(BN, (left + kStepN - 1) / kStepN * kStepN);
     };
@@ -593,29 +603,26 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     if (warp == 0) {
         // ---- loads -------------------------------------------------------
         int s = 0;
-        uint32_t ph = 0, tail_ph = 0;
+        uint32_t ph = 0;
         bool ok = true;
         while (ok && walk.next(t)) {
             const int iters = iterations(t);
             const int m0 = t.m * kBM + (int)rank * kTileM;
             const int n0 = t.n * BN + (int)rank * (width(t) / CG);
+            const bool no_b = is_bias(t);
+            const uint32_t bytes = no_b ? kStageA : kStage;
             for (int i = 0; i < iters; ++i) {
                 ok = wait(&c->empty[s], ph ^ 1, c, p.ws);
                 if (!ok) break;
-                // the last rows of an expert do not fill 64 of k: the rows
-                // after them are another expert's (or nobody's, with any
-                // bits), and are zeroed in both tiles once they have landed
-                const int keep = MODE == kWgrad ? t.rows - i * 64 : 64;
-                const bool tail = keep < 64;
-                unsigned char *sa = smem + s * kStage, *sb = sa + kStageA;
-                const uint32_t full = cluster_addr(&c->full[s], 0);
                 if (lane == 0) {
-                    uint32_t bar = full;
-                    if (tail) {
-                        mbar_arrive_expect_tx(&c->tail, kStage);
-                        bar = cluster_addr(&c->tail, rank);
+                    unsigned char *sa = smem + s * kStage, *sb = sa + kStageA;
+                    uint32_t bar;
+                    if (MODE == kWgrad && t.rows - i * 64 < 64) {  // a tail: see warp 3
+                        mbar_arrive_expect_tx(&c->tail[s], bytes);
+                        bar = cluster_addr(&c->tail[s], rank);
                     } else {
-                        mbar_arrive_expect_tx_remote(full, kStage);
+                        bar = cluster_addr(&c->full[s], 0);
+                        mbar_arrive_expect_tx_remote(bar, bytes);
                     }
                     const int k0 = i * kElems;
                     if (MODE == kLinear) {
@@ -628,23 +635,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     } else {
                         for (int j = 0; j < 2; ++j)
                             tma_load_2d<CG>(sa + j * 8192, &p.ma, m0 + 64 * j, t.row0 + k0, bar);
-                        for (int j = 0; j < kHalfN / 64; ++j)
-                            tma_load_2d<CG>(sb + j * 8192, &p.mb, n0 + 64 * j, t.row0 + k0, bar);
+                        if (!no_b)
+                            for (int j = 0; j < kHalfN / 64; ++j)
+                                tma_load_2d<CG>(sb + j * 8192, &p.mb, n0 + 64 * j, t.row0 + k0, bar);
                     }
                 }
                 __syncwarp();
-                if (MODE == kWgrad && tail) {
-                    ok = wait(&c->tail, tail_ph, c, p.ws);
-                    if (!ok) break;
-                    tail_ph ^= 1;
-                    // row k of a tile is the 128 bytes at 128 * k of each 8 KB
-                    for (int j = 0; j < 2 + kHalfN / 64; ++j)
-                        for (int o = keep * 128 + lane * 16; o < 8192; o += 512)
-                            *reinterpret_cast<uint4 *>(sa + j * 8192 + o) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_release_cluster(full);
-                }
                 if (++s == kStages) {
                     s = 0;
                     ph ^= 1;
@@ -660,6 +656,32 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 ph ^= 1;
             }
         }
+    } else if (MODE == kWgrad && warp == 3) {
+        // ---- tails ---------------------------------------------------------
+        // The last rows of an expert rarely fill 64 of k; the rows after them
+        // are another expert's, or nobody's with any bits in them.  That
+        // stage lands on a barrier of its own, its rows past the end are
+        // zeroed in both tiles, and then it counts as full.
+        int s = 0;
+        uint32_t phases = 0;  // of each stage's barrier
+        bool ok = true;
+        while (ok && walk.next(t)) {
+            const int iters = iterations(t), keep = t.rows & 63;
+            s = (s + iters) % kStages;
+            if (keep == 0) continue;
+            const int at = s == 0 ? kStages - 1 : s - 1;  // the tile's last stage
+            ok = wait(&c->tail[at], (phases >> at) & 1, c, p.ws);
+            if (!ok) break;
+            phases ^= 1u << at;
+            // row k of a tile is the 128 bytes at 128 * k of each 8 KB
+            unsigned char *sa = smem + at * kStage;
+            for (int j = 0; j < (is_bias(t) ? 2 : 2 + kHalfN / 64); ++j)
+                for (int o = keep * 128 + lane * 16; o < 8192; o += 512)
+                    *reinterpret_cast<uint4 *>(sa + j * 8192 + o) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_release_cluster(cluster_addr(&c->full[at], 0));
+        }
     } else if (warp == 1 && rank == 0) {
         // ---- matrix instructions ------------------------------------------
         // One thread.  It looks at the next stage's barrier before it issues
@@ -671,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
             const uint64_t da0 = smem_desc(smem_addr(smem), kLeadA, 1024);
             const uint64_t db0 = smem_desc(smem_addr(smem) + kStageA, kLeadB, 1024);
+            const uint64_t ones = smem_desc(smem_addr(stg), kLeadB, 1024);
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true, ready = false, more = walk.next(t);
@@ -682,6 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 }
                 const uint32_t idesc = mma_idesc(FP8, kMnA, kMnB, kBM, width(t));
                 const uint32_t d = tmem + acc * BN;
+                const bool bias = is_bias(t);
                 ok = poll(&c->acc_empty[acc], aph ^ 1, c, p.ws);
                 if (!ok) break;
                 tc_fence_after();
@@ -700,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     const uint64_t da = da0 + (uint64_t)(now * (kStage >> 4)), db = db0 + (uint64_t)(now * (kStage >> 4));
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ss<CG, FP8>(d, da + k * kStepA, db + k * kStepB, idesc, (i | k) != 0);
+                        mma_ss<CG, FP8>(d, da + k * kStepA, bias ? ones : db + k * kStepB, idesc, (i | k) != 0);
                     mma_commit<CG>(&c->empty[now]);
                     if (i == 0) more = walk.next(t);  // the divisions of the next tile hide behind this one
                 }
@@ -723,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         while (walk.next(t)) {
             const int iters = iterations(t);
             const int m0 = t.m * kBM + (int)rank * kTileM, n0 = t.n * BN;
-            const int cols = min(BN, (MODE == kWgrad ? p.N : t.rows) - n0);
+            const int cols = is_bias(t) ? 1 : min(BN, (MODE == kWgrad ? p.N : t.rows) - n0);
             const int c_first = ((g + turn) & 1) * kChunk;
             turn += (cols + kChunk - 1) / kChunk;
             const int row0 = t.row0 + n0;
@@ -763,7 +787,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 if constexpr (MODE == kWgrad) {
                     // lane = one row of dw, 32 consecutive values of it
                     const int m = m0 + q * 32 + lane;
-                    if (m < p.M) store_row(p, ((size_t)t.e * p.M + m) * p.N + n0 + c0, v, min(kChunk, cols - c0));
+                    const size_t r = (size_t)t.e * p.M + m;
+                    if (m < p.M) {
+                        if (!is_bias(t)) store_row(p, r * p.N + n0 + c0, v, min(kChunk, cols - c0));
+                        else if (p.fp32) static_cast<float *>(p.db)[r] = __uint_as_float(v[0]);
+                        else static_cast<__nv_bfloat16 *>(p.db)[r] = __float2bfloat16_rn(__uint_as_float(v[0]));
+                    }
                     __syncwarp();
                 } else {
                     ep.finish(v, row0 + c0, min(kChunk, cols - c0), min(kChunk, cols - c0 - 2 * kChunk));
@@ -847,7 +876,7 @@ cudaError_t launch(const Params &p, cudaStream_t s)
     if (err != cudaSuccess) return err;
     // the most tiles that offsets over these rows can give
     const long long tm = (p.M + kTileM * CG - 1) / (kTileM * CG);
-    const long long tn = MODE == kWgrad ? (long long)p.E * ((p.N + BN - 1) / BN)
+    const long long tn = MODE == kWgrad ? (long long)p.E * ((p.N + BN - 1) / BN + 1)
                                         : p.rows / BN + (p.rows < p.E ? p.rows : p.E);
     long long blocks = device_sm_count() / CG;
     if (tm * tn < blocks) blocks = tm * tn;
@@ -950,10 +979,14 @@ cudaError_t launch_expert_dgrad(const moe_rows *G, const void *dy, int N, const 
                        : launch<2, 256, kDgrad, false>(p, s);
 }
 
-cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const void *x, int K, void *dw, int fp32,
-                                cudaStream_t s)
+cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const void *x, int K, void *dw, void *db,
+                                int fp32, cudaStream_t s)
 {
-    if (G->rows == 0) return cudaMemsetAsync(dw, 0, (size_t)G->E * N * K * (fp32 ? 4 : 2), s);
+    if (G->rows == 0) {
+        const size_t n = (size_t)G->E * N * (fp32 ? 4 : 2);
+        const cudaError_t err = db ? cudaMemsetAsync(db, 0, n, s) : cudaSuccess;
+        return err == cudaSuccess ? cudaMemsetAsync(dw, 0, n * K, s) : err;
+    }
     Params p = {};
     p.offsets = G->offsets;
     p.ws = G->ws;
@@ -963,6 +996,7 @@ cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const 
     p.N = K;
     p.fp32 = fp32;
     p.dw = dw;
+    p.db = db;
     cudaError_t err = encode_rows(&p.ma, false, dy, N, G->rows, 64, 64);
     if (err == cudaSuccess) err = encode_rows(&p.mb, false, x, K, G->rows, 64, 64);
     if (err != cudaSuccess) return err;

@@ -10,9 +10,8 @@ cudaError_t launch_expert_linear(const moe_rows *G, const void *x, const float *
                                  void *y, void *saved, void *saved_scales, cudaStream_t s);
 cudaError_t launch_expert_dgrad(const moe_rows *G, const void *dy, int N, const void *w, int K, int act,
                                 const void *saved, const void *saved_scales, void *dx, void *a, cudaStream_t s);
-cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const void *x, int K, void *dw, int fp32,
-                                cudaStream_t s);
-cudaError_t launch_row_sums(const moe_rows *G, const void *dy, int N, void *db, int fp32, cudaStream_t s);
+cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const void *x, int K, void *dw, void *db,
+                                int fp32, cudaStream_t s);
 cudaError_t launch_act_backward(const moe_rows *G, const void *dy, int N, int act, const void *saved,
                                 const void *saved_scales, void *du, void *a, cudaStream_t s);
 }  // namespace moe

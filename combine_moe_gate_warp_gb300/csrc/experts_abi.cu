@@ -90,9 +90,7 @@ moe_status moe_expert_wgrad(const moe_rows *G, const void *dy, int N, const void
     if (st != MOE_OK) return st;
     if (!dw || (G->rows > 0 && (!dy || !x))) return MOE_ERR_INVALID_ARG;
     if (!aligned16(dy) || !aligned16(x) || !aligned16(dw) || !aligned16(db)) return MOE_ERR_INVALID_ARG;
-    cudaError_t err = moe::launch_expert_wgrad(G, dy, N, x, K, dw, fp32 != 0, stream_of(stream));
-    if (err == cudaSuccess && db) err = moe::launch_row_sums(G, dy, N, db, fp32 != 0, stream_of(stream));
-    return from_cuda(err);
+    return from_cuda(moe::launch_expert_wgrad(G, dy, N, x, K, dw, db, fp32 != 0, stream_of(stream)));
 }
 
 moe_status moe_act_backward(const moe_rows *G, const void *dy, int N, int act, const void *saved,

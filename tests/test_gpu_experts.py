@@ -180,8 +180,7 @@ def check_wgrad(dw, db, dy, x, counts, dtype):
         d, v = dy[lo:hi].double(), x[lo:hi].double()
         want, err = d.T @ v, sum_error(hi - lo, d.abs().T @ v.abs())
         assert_near(dw[e], want, err + half * (want.abs() + err), f"dw[{e}]")
-        # depth of the bias sums: rows / 64, then 8 + 8
-        want, err = d.sum(0), ((hi - lo) / 64 + 17) * 2.0 ** -24 * d.abs().sum(0)
+        want, err = d.sum(0), sum_error(hi - lo, d.abs().sum(0))
         assert_near(db[e], want, err + half * (want.abs() + err), f"db[{e}]")
 
 
