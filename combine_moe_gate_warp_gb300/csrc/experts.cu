@@ -512,6 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0u;
 
+    int lo = 0, hi = 0;  // read first: the tiles wait for them
+    if (tid < p.E) {
+        lo = p.offsets ? p.offsets[tid] : 0;
+        hi = p.offsets ? p.offsets[tid + 1] : p.rows;
+    }
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&c->full[i], CG);
@@ -537,44 +542,40 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     // rows and first tile of every expert: thread e looks at expert e
     const int tm = (p.M + kBM - 1) / kBM;
     {
-        int lo = 0, hi = 0, tiles = 0;
-        if (tid < p.E) {
-            lo = p.offsets ? p.offsets[tid] : 0;
-            hi = p.offsets ? p.offsets[tid + 1] : p.rows;
-        }
-        // the largest offset so far: rows below it belong to an earlier
-        // expert, and two experts never write the same row
-        int top = max(lo, hi);
+        const auto tiles_of = [&](int rows) {
+            return tm * (((MODE == kWgrad ? p.N : rows) + BN - 1) / BN + (MODE == kWgrad && p.db ? 1 : 0));
+        };
+        const auto scan = [&](int v) {  // inclusive, over a warp
 #pragma unroll
-        for (int i = 1; i < 32; i *= 2) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, top, i);
-            if (lane >= i) top = max(top, v);
-        }
-        int before = __shfl_up_sync(0xFFFFFFFFu, top, 1);
-        if (lane == 0) before = 0;
-        if (lane == 31) c->part[warp] = top;
-        __syncthreads();
-        for (int i = 0; i < warp; ++i) before = max(before, c->part[i]);
-        __syncthreads();
-        if (tid < p.E) {
-            if (lo < before || hi < lo || hi > p.rows) {
+            for (int i = 1; i < 32; i *= 2) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, v, i);
+                if (lane >= i) v += u;
+            }
+            return v;
+        };
+        int sum = scan(tid < p.E ? tiles_of(max(hi - lo, 0)) : 0);
+        if (lane == 31) c->part[warp] = sum;
+        // offsets that only rise and stay inside the rows need no second look
+        if (!__syncthreads_and(tid >= p.E || (lo >= 0 && hi >= lo && hi <= p.rows))) {
+            // the largest offset so far: rows below it belong to an earlier
+            // expert, and two experts never write the same row
+            int before = 0;
+            if (p.offsets)
+                for (int i = 0; i <= tid && i < p.E; ++i) before = max(before, p.offsets[i]);
+            if (tid < p.E && (lo < before || hi < lo || hi > p.rows)) {
                 if (blockIdx.x == 0) record_status(p.ws, MOE_ERR_DEVICE_DATA);
                 lo = hi = 0;
             }
-            tiles = tm * (((MODE == kWgrad ? p.N : hi - lo) + BN - 1) / BN + (MODE == kWgrad && p.db ? 1 : 0));
+            sum = scan(tid < p.E ? tiles_of(hi - lo) : 0);
+            if (lane == 31) c->part[warp] = sum;
+            __syncthreads();
+        }
+        for (int i = 0; i < warp; ++i) sum += c->part[i];
+        if (tid < p.E) {
             c->row0[tid] = lo;
             c->rows[tid] = hi - lo;
+            c->tile0[tid + 1] = sum;
         }
-        int sum = tiles;
-#pragma unroll
-        for (int i = 1; i < 32; i *= 2) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, i);
-            if (lane >= i) sum += v;
-        }
-        if (lane == 31) c->part[warp] = sum;
-        __syncthreads();
-        for (int i = 0; i < warp; ++i) sum += c->part[i];
-        if (tid < p.E) c->tile0[tid + 1] = sum;
         if (tid == 0) c->tile0[0] = 0;
     }
     __syncwarp();
@@ -713,7 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     ok = ready || poll(&c->full[s], ph, c, p.ws);
                     if (!ok) break;
                     // the zeroed rows of a tail come from the peer's generic writes too
-                    if (MODE == kWgrad && CG == 2 && i == iters - 1) mbar_try_wait_acquire_cluster(&c->full[s], ph);
+                    if (MODE == kWgrad && CG == 2 && i == iters - 1 && (t.rows & 63))
+                        mbar_try_wait_acquire_cluster(&c->full[s], ph);
                     tc_fence_after();
                     const int now = s;
                     if (++s == kStages) {

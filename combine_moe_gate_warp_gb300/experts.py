@@ -46,8 +46,8 @@ def _act(name: str) -> int:
         raise ValueError(f"act: one of {', '.join(ACTIVATIONS)}, got {name!r}") from None
 
 
-def _check(t, dtype, shape, name, device):
-    """A contiguous tensor of exactly this type, shape and device; its address."""
+def _refuse(t, dtype, shape, name, device):
+    """Say what is wrong with a tensor that _check turned down."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype != dtype:
@@ -56,9 +56,17 @@ def _check(t, dtype, shape, name, device):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, the rows are on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _check(t, dtype, shape, name, device):
+    """A contiguous tensor of exactly this type, shape and device; its address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, shape, name, device)
 
 
 class ExpertRows:
@@ -109,14 +117,19 @@ class ExpertRows:
 
     # ------------------------------------------------------------------
     def _stream(self):
-        return torch.cuda.current_stream(self.device).cuda_stream
+        if self.device.type != "cuda":
+            raise ValueError(f"the rows are on {self.device}: a CUDA device is needed")
+        # the current stream's handle, without the Stream object around it
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def _weights(self, w, dtype):
         """(N, K, address) of weights [E, N, K], or [N, K] for one plain group."""
-        if not isinstance(w, torch.Tensor) or w.dim() != (3 if self.grouped else 2):
+        shape = w.shape if isinstance(w, torch.Tensor) else ()
+        if len(shape) != (3 if self.grouped else 2):
             raise ValueError("w: expected a tensor of " + ("[E, N, K]" if self.grouped else "[N, K]"))
-        N, K = w.shape[-2:]
-        return N, K, _check(w, dtype, self._per_expert(N, K), "w", self.device)
+        if self.grouped and shape[0] != self.E:
+            raise ValueError(f"w: {shape[0]} experts, the rows have {self.E}")
+        return shape[-2], shape[-1], _check(w, dtype, shape, "w", self.device)
 
     def _per_expert(self, *shape):
         return (self.E, *shape) if self.grouped else shape
@@ -143,21 +156,33 @@ class ExpertRows:
         x [rows, K] and w [E, N, K] are bf16, or e4m3 codes (uint8) with
         x_scales [rows, 2] (scale, zero) and w_scales [E, N, 2] (scale, sum).
         ``saved`` receives the activation's inputs in 8 bits."""
-        a, fp8 = _act(act), x_scales is not None
-        if fp8 != (w_scales is not None):
-            raise ValueError("x_scales and w_scales go together")
-        dtype = torch.uint8 if fp8 else torch.bfloat16
+        a, dev, rows = _act(act), self.device, self.rows
+        dtype = torch.bfloat16
+        xs = ws = bp = rp = sc = ss = None
+        if x_scales is not None or w_scales is not None:
+            if x_scales is None or w_scales is None:
+                raise ValueError("x_scales and w_scales go together")
+            dtype = torch.uint8
         N, K, wp = self._weights(w, dtype)
+        xp = _check(x, dtype, (rows, K), "x", dev)
+        if x_scales is not None:
+            xs = _check(x_scales, torch.float32, (rows, 2), "x_scales", dev)
+            ws = _check(w_scales, torch.float32, self._per_expert(N, 2), "w_scales", dev)
+        if bias is not None:
+            bp = _check(bias, torch.bfloat16, self._per_expert(N), "bias", dev)
         cols = N // 2 if a == abi.MOE_ACT_SWIGLU else N
-        xp = _check(x, dtype, (self.rows, K), "x", self.device)
-        xs = self._opt(x_scales, torch.float32, (self.rows, 2), "x_scales")
-        ws = self._opt(w_scales, torch.float32, self._per_expert(N, 2), "w_scales")
-        bp = self._opt(bias, torch.bfloat16, self._per_expert(N), "bias")
-        rp = self._opt(residual, torch.bfloat16, (self.rows, cols), "residual")
-        sc, ss = (None, None) if saved is None else self._saved(saved, N)
-        out, op = self._out(out, torch.bfloat16, (self.rows, cols), "out")
-        abi._check(self._lib.moe_expert_linear(self._ref, xp, xs, K, wp, ws, N, bp, a, rp, op, sc, ss,
-                                               self._stream()), "moe_expert_linear")
+        if residual is not None:
+            rp = _check(residual, torch.bfloat16, (rows, cols), "residual", dev)
+        if saved is not None:
+            sc, ss = self._saved(saved, N)
+        if out is None:
+            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+            op = out.data_ptr()
+        else:
+            op = _check(out, torch.bfloat16, (rows, cols), "out", dev)
+        st = self._lib.moe_expert_linear(self._ref, xp, xs, K, wp, ws, N, bp, a, rp, op, sc, ss, self._stream())
+        if st:
+            abi._check(st, "moe_expert_linear")
         return out
 
     def dgrad(self, dy, w, *, act: str = "none", saved: SavedLayer | None = None, out=None, a=None):
