@@ -54,8 +54,8 @@ constexpr int kCodeBytes = 32 * kPitchCode;
 __host__ __device__ constexpr int group_bytes(int MODE)
 {
     return MODE == kWgrad        ? 1024
-           : MODE == kDgradSaved ? 3 * 16 * kPitch + 2 * 16 * kPitchCode + 128
-                                 : kOutBytes + kCodeBytes + 256 + 1024;
+           : MODE == kDgradSaved ? 3 * 16 * kPitch + 2 * 16 * kPitchCode + 512
+                                 : kOutBytes + kCodeBytes + 256 + 1024 + 512;
 }
 constexpr int kControl = 4096;
 
@@ -222,7 +222,8 @@ struct LinearEpilogue {
     const Params &p;
     unsigned char *out, *codes;
     float2 *xs;
-    unsigned *top;  // [4 warps][2][32]
+    unsigned *top;   // [4 warps][gates, ups][32 rows], largest magnitudes
+    float *inverse;  // [4 blocks][32 rows], 1 / scale
     int g, q, lane, tid;
     // of a tile
     int col0, cols;  // first output column of the block's tile, how many exist
@@ -231,7 +232,8 @@ struct LinearEpilogue {
 
     __device__ LinearEpilogue(const Params &p_, unsigned char *base, int g_, int q_, int lane_)
         : p(p_), out(base), codes(base + kOutBytes), xs(reinterpret_cast<float2 *>(base + kOutBytes + kCodeBytes)),
-          top(reinterpret_cast<unsigned *>(base + kOutBytes + kCodeBytes + 256)), g(g_), q(q_), lane(lane_),
+          top(reinterpret_cast<unsigned *>(base + kOutBytes + kCodeBytes + 256)),
+          inverse(reinterpret_cast<float *>(base + kOutBytes + kCodeBytes + 256 + 1024)), g(g_), q(q_), lane(lane_),
           tid(q_ * 32 + lane_)
     {
     }
@@ -335,52 +337,58 @@ struct LinearEpilogue {
     {
         if (p.glu) {
             const bool odd = lane & 1;
-            const unsigned mask = odd ? 0xAAAAAAAAu : 0x55555555u;
-            unsigned keep0 = 0, keep1 = 0;
+            unsigned gates = 0, ups = 0;  // of row `lane`
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const unsigned m = __reduce_max_sync(mask, mag(u[i]));
-                if (lane / 2 == (i & 15)) {
-                    if (i < 16) keep0 = m;
-                    else keep1 = m;
+                const unsigned m = mag(u[i]);
+                const unsigned mg = __reduce_max_sync(0xFFFFFFFFu, odd ? 0u : m);
+                const unsigned mu = __reduce_max_sync(0xFFFFFFFFu, odd ? m : 0u);
+                if (lane == i) {
+                    gates = mg;
+                    ups = mu;
                 }
             }
-            unsigned *mine = top + (q * 2 + (lane & 1)) * 32;
-            mine[lane / 2] = keep0;
-            mine[16 + lane / 2] = keep1;
+            top[q * 64 + lane] = gates;
+            top[q * 64 + 32 + lane] = ups;
             group_sync(g);
-            const unsigned *pair = top + ((q & 2) * 2 + (lane & 1)) * 32;  // warps q & 2 and (q & 2) + 1
+            // 2 blocks of gates and 2 of ups for 32 rows: one a thread
+            const int r = tid & 31, b = tid >> 5, half = b >> 1, side = b & 1;
+            const unsigned *t = top + half * 128 + side * 32 + r;
+            const unsigned byte = saved_byte(max(t[0], t[64]));
+            inverse[tid] = saved_inverse(byte);
+            if (r < rows && half * 32 < cols)
+                p.saved_scales[(size_t)(row + r) * (p.M / 32) + (side * out_cols() + col0) / 32 + half] = (uint8_t)byte;
+            group_sync(g);
+            const float2 *inv = reinterpret_cast<const float2 *>(inverse + ((q & 2) + (lane & 1)) * 32);
             uint8_t *c = codes + (odd ? 64 : 0) + q * 16 + lane / 2;
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-                const float i0 = saved_inverse(saved_byte(max(pair[i], pair[64 + i])));
-                const float i1 = saved_inverse(saved_byte(max(pair[i + 1], pair[64 + i + 1])));
-                const unsigned two = e4m3_pair(u[i] * i0, u[i + 1] * i1);
+                const float2 f = inv[i / 2];
+                const unsigned two = e4m3_pair(u[i] * f.x, u[i + 1] * f.y);
                 c[i * kPitchCode] = (uint8_t)two;
                 c[(i + 1) * kPitchCode] = (uint8_t)(two >> 8);
             }
-            // 2 blocks of gates and 2 of ups for 32 rows: one byte a thread
-            const int r = tid & 31, b = tid >> 5, half = b & 1, side = b >> 1;
-            if (r < rows && half * 32 < cols) {
-                const unsigned *t = top + (half * 4 + side) * 32 + r;
-                p.saved_scales[(size_t)(row + r) * (p.M / 32) + (side * out_cols() + col0) / 32 + half] =
-                    (uint8_t)saved_byte(max(t[0], t[64]));
-            }
         } else {
-            unsigned keep = 0;
+            unsigned keep = 0;  // of row `lane`
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const unsigned m = __reduce_max_sync(0xFFFFFFFFu, mag(u[i]));
+                if (lane == i) keep = m;
+            }
+            const unsigned byte = saved_byte(keep);
+            if (lane < rows && q * 32 < cols)
+                p.saved_scales[(size_t)(row + lane) * (p.M / 32) + col0 / 32 + q] = (uint8_t)byte;
+            float *mine = inverse + q * 32;  // read by this warp alone
+            mine[lane] = saved_inverse(byte);
+            __syncwarp();
             uint8_t *c = codes + q * 32 + lane;
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-                const unsigned b0 = saved_byte(__reduce_max_sync(0xFFFFFFFFu, mag(u[i])));
-                const unsigned b1 = saved_byte(__reduce_max_sync(0xFFFFFFFFu, mag(u[i + 1])));
-                const unsigned two = e4m3_pair(u[i] * saved_inverse(b0), u[i + 1] * saved_inverse(b1));
+                const float2 f = *reinterpret_cast<const float2 *>(mine + i);
+                const unsigned two = e4m3_pair(u[i] * f.x, u[i + 1] * f.y);
                 c[i * kPitchCode] = (uint8_t)two;
                 c[(i + 1) * kPitchCode] = (uint8_t)(two >> 8);
-                if (lane == i) keep = b0;
-                if (lane == i + 1) keep = b1;
             }
-            if (lane < rows && q * 32 < cols)
-                p.saved_scales[(size_t)(row + lane) * (p.M / 32) + col0 / 32 + q] = (uint8_t)keep;
         }
     }
 };
@@ -393,15 +401,15 @@ struct LinearEpilogue {
 struct SavedEpilogue {
     const Params &p;
     unsigned char *out, *codes;
-    uint8_t *scale;  // [16 rows][4 gate blocks, 4 up blocks]
+    float *scale;  // [16 rows][4 gate blocks, 4 up blocks]
     int g, q, lane, tid;
     int col0, cols;
     uint4 pre[2];
     unsigned pre_scale;
 
     __device__ SavedEpilogue(const Params &p_, unsigned char *base, int g_, int q_, int lane_)
-        : p(p_), out(base), codes(base + 3 * 16 * kPitch), scale(base + 3 * 16 * kPitch + 2 * 16 * kPitchCode), g(g_),
-          q(q_), lane(lane_), tid(q_ * 32 + lane_)
+        : p(p_), out(base), codes(base + 3 * 16 * kPitch), scale(reinterpret_cast<float *>(base + 3 * 16 * kPitch + 2 * 16 * kPitchCode)),
+          g(g_), q(q_), lane(lane_), tid(q_ * 32 + lane_)
     {
     }
     __device__ __forceinline__ bool glu() const { return p.act == MOE_ACT_SWIGLU; }
@@ -427,7 +435,7 @@ struct SavedEpilogue {
     {
         place<8, 16>(pre, codes, kPitchCode, tid);
         if (glu()) place<8, 16>(pre + 1, codes + 16 * kPitchCode, kPitchCode, tid);
-        scale[tid] = (uint8_t)pre_scale;
+        scale[tid] = saved_scale(pre_scale);
         ahead(row + 32, next_rows);
         group_sync(g);
         const uint8_t *c = codes + q * 32 + lane;
@@ -435,13 +443,13 @@ struct SavedEpilogue {
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
             const float2 x = e4m3_decode2(c[i * kPitchCode] | ((unsigned)c[(i + 1) * kPitchCode] << 8));
-            const float u[2] = {x.x * saved_scale(scale[i * 8 + q]), x.y * saved_scale(scale[i * 8 + 8 + q])};
+            const float u[2] = {x.x * scale[i * 8 + q], x.y * scale[i * 8 + 8 + q]};
             const float d[2] = {__uint_as_float(v[i]), __uint_as_float(v[i + 1])};
             if (glu()) {
                 const uint8_t *cu = c + 16 * kPitchCode;
                 const float2 z = e4m3_decode2(cu[i * kPitchCode] | ((unsigned)cu[(i + 1) * kPitchCode] << 8));
-                const float up[2] = {z.x * saved_scale(scale[i * 8 + 4 + q]),
-                                     z.y * saved_scale(scale[i * 8 + 12 + q])};
+                const float up[2] = {z.x * scale[i * 8 + 4 + q],
+                                     z.y * scale[i * 8 + 12 + q]};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float s = logistic(u[j]), silu = u[j] * s;
