@@ -1,4 +1,4 @@
-// experts.cu -- the experts' matrix products over the packed rows, on the
+// experts.cuh -- the experts' matrix products over the packed rows, on the
 // tcgen05 tensor cores (include/moe_experts.h).
 //
 // One kernel serves the three products of a layer.  Every product is
@@ -20,6 +20,8 @@
 // accumulators in tensor memory, warps 4-7 drain the other one.  The blocks
 // walk the tiles in a fixed order, derived from the offsets on the device;
 // no result depends on timing.
+#pragma once
+
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
@@ -60,16 +62,20 @@ __host__ __device__ constexpr int group_bytes(int MODE)
 constexpr int kControl = 4096;
 
 __host__ __device__ constexpr int stage_bytes(int CG, int BN) { return kStageA + BN / CG * 128; }
+// the other blocks' sums of a tile whose k is split over a cluster
+__host__ __device__ constexpr int join_bytes(bool SPLIT, int BN) { return SPLIT ? BN * kTileM * 4 : 0; }
 // ring depth: what is left of 227 KB beside the epilogue, the barriers and tile
 // counts, and the alignment to 1 KB; at most 12 stages
-__host__ __device__ constexpr int stages(int CG, int BN, int MODE)
+__host__ __device__ constexpr int stages(int CG, int BN, int MODE, bool SPLIT)
 {
-    const int n = (227 * 1024 - 2 * group_bytes(MODE) - kControl - 1024) / stage_bytes(CG, BN);
+    const int n =
+        (227 * 1024 - 2 * group_bytes(MODE) - join_bytes(SPLIT, BN) - kControl - 1024) / stage_bytes(CG, BN);
     return n > 12 ? 12 : n;
 }
-__host__ __device__ constexpr int smem_bytes(int CG, int BN, int MODE)
+__host__ __device__ constexpr int smem_bytes(int CG, int BN, int MODE, bool SPLIT)
 {
-    return 1024 + stages(CG, BN, MODE) * stage_bytes(CG, BN) + 2 * group_bytes(MODE) + kControl;
+    return 1024 + stages(CG, BN, MODE, SPLIT) * stage_bytes(CG, BN) + 2 * group_bytes(MODE) + join_bytes(SPLIT, BN) +
+           kControl;
 }
 __host__ __device__ constexpr int tmem_cols(int BN) { return 2 * BN < 32 ? 32 : 2 * BN; }
 
@@ -83,6 +89,7 @@ struct Params {
     int K;         // linear, dgrad: extent of k, in bytes
     int act, glu;  // glu: A's rows alternate gate and up columns
     int fp32;
+    int split;     // blocks that share a tile's k (a cluster of 2, 4 or 8), or 1
     const __nv_bfloat16 *bias, *residual;
     const float2 *x_scales, *w_scales;
     __nv_bfloat16 *y, *a;
@@ -91,7 +98,7 @@ struct Params {
 };
 
 struct Control {
-    uint64_t full[12], empty[12], tail[12], acc_full[2], acc_empty[2];
+    uint64_t full[12], empty[12], tail[12], acc_full[2], acc_empty[2], joined, taken;
     uint32_t tmem;
     int abort;
     int part[12];
@@ -501,10 +508,10 @@ __device__ __forceinline__ void store_row(const Params &p, size_t at, const uint
 // --------------------------------------------------------------------------
 // the kernel
 // --------------------------------------------------------------------------
-template <int CG, int BN, int MODE, bool FP8>
+template <int CG, int BN, int MODE, bool FP8, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ Params p)
 {
-    constexpr int kStages = stages(CG, BN, MODE);
+    constexpr int kStages = stages(CG, BN, MODE, SPLIT);
     constexpr int kStage = stage_bytes(CG, BN);
     constexpr int kHalfN = BN / CG;  // rows of B per block
     constexpr int kBM = kTileM * CG;
@@ -515,10 +522,16 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char *stg = smem + kStages * kStage;
-    Control *c = reinterpret_cast<Control *>(stg + 2 * group_bytes(MODE));
+    float *join = reinterpret_cast<float *>(stg + 2 * group_bytes(MODE));
+    Control *c = reinterpret_cast<Control *>(stg + 2 * group_bytes(MODE) + join_bytes(SPLIT, BN));
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0u;
+    static_assert(CG == 1 || !SPLIT, "a pair does not share its k");
+    constexpr bool kCluster = CG == 2 || SPLIT;
+    const uint32_t self = kCluster ? cluster_cta_rank() : 0u;
+    const uint32_t rank = CG == 2 ? self : 0u;   // of the pair: which half of m
+    const uint32_t lead = CG == 2 ? 0u : self;   // whose barriers the matrix instructions wait on
+    const int split = SPLIT ? p.split : 1;
 
     int lo = 0, hi = 0;  // read first: the tiles wait for them
     if (tid < p.E) {
@@ -535,6 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             mbar_init(&c->acc_full[i], 1);
             mbar_init(&c->acc_empty[i], 8 * CG);
         }
+        mbar_init(&c->joined, 8 * split);
+        mbar_init(&c->taken, 8 * split);
         c->abort = 0;
         mbar_fence_init();
         tmap_prefetch(&p.ma);
@@ -588,15 +603,24 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     }
     __syncwarp();
     tc_fence_before();
-    if (CG == 2) cluster_sync_all();
+    if (kCluster) cluster_sync_all();
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c->tmem;
 
-    Walk walk(c, p.E, tm, blockIdx.x / CG, gridDim.x / CG);
+    const int sharers = CG == 2 ? 2 : split;  // blocks of a cluster
+    Walk walk(c, p.E, tm, blockIdx.x / sharers, gridDim.x / sharers);
     Tile t;
-    const auto iterations = [&](const Tile &q) {
-        return MODE == kWgrad ? (q.rows + 63) / 64 : (p.K + 127) / 128;
+    // this block's part of a tile's k, in stages
+    struct Span {
+        int first, count;
+        bool last;
+    };
+    const auto span = [&](const Tile &q) {
+        const int all = MODE == kWgrad ? (q.rows + 63) / 64 : (p.K + 127) / 128;
+        if (!SPLIT) return Span{0, all, true};
+        const int lo_k = all * (int)self / split, hi_k = all * ((int)self + 1) / split;
+        return Span{lo_k, hi_k - lo_k, hi_k == all};
     };
     // wgrad: the tile after the last of n is the bias gradient's, the product
     // of dy^T with ones: no rows of x to load, 16 columns (32 for a pair)
@@ -615,12 +639,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         uint32_t ph = 0;
         bool ok = true;
         while (ok && walk.next(t)) {
-            const int iters = iterations(t);
+            const Span part = span(t);
             const int m0 = t.m * kBM + (int)rank * kTileM;
             const int n0 = t.n * BN + (int)rank * (width(t) / CG);
             const bool no_b = is_bias(t);
             const uint32_t bytes = no_b ? kStageA : kStage;
-            for (int i = 0; i < iters; ++i) {
+            for (int i = part.first; i < part.first + part.count; ++i) {
                 ok = wait(&c->empty[s], ph ^ 1, c, p.ws);
                 if (!ok) break;
                 if (lane == 0) {
@@ -628,9 +652,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     uint32_t bar;
                     if (MODE == kWgrad && t.rows - i * 64 < 64) {  // a tail: see warp 3
                         mbar_arrive_expect_tx(&c->tail[s], bytes);
-                        bar = cluster_addr(&c->tail[s], rank);
+                        bar = cluster_addr(&c->tail[s], self);
                     } else {
-                        bar = cluster_addr(&c->full[s], 0);
+                        bar = cluster_addr(&c->full[s], lead);
                         mbar_arrive_expect_tx_remote(bar, bytes);
                     }
                     const int k0 = i * kElems;
@@ -675,9 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         uint32_t phases = 0;  // of each stage's barrier
         bool ok = true;
         while (ok && walk.next(t)) {
-            const int iters = iterations(t), keep = t.rows & 63;
-            s = (s + iters) % kStages;
-            if (keep == 0) continue;
+            const Span part = span(t);
+            const int keep = t.rows & 63;
+            s = (s + part.count) % kStages;
+            if (keep == 0 || !part.last || part.count == 0) continue;
             const int at = s == 0 ? kStages - 1 : s - 1;  // the tile's last stage
             ok = wait(&c->tail[at], (phases >> at) & 1, c, p.ws);
             if (!ok) break;
@@ -689,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     *reinterpret_cast<uint4 *>(sa + j * 8192 + o) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_release_cluster(cluster_addr(&c->full[at], 0));
+            if (lane == 0) mbar_arrive_release_cluster(cluster_addr(&c->full[at], lead));
         }
     } else if (warp == 1 && rank == 0) {
         // ---- matrix instructions ------------------------------------------
@@ -707,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             uint32_t ph = 0, aph = 0;
             bool ok = true, ready = false, more = walk.next(t);
             while (more) {
-                const int iters = iterations(t);
+                const int iters = span(t).count;
                 if (iters == 0) {
                     more = walk.next(t);
                     continue;
@@ -754,63 +779,115 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         uint32_t aph = 0;
         using Epilogue = std::conditional_t<MODE == kDgradSaved, SavedEpilogue, LinearEpilogue<FP8>>;
         Epilogue ep(p, stg + g * group_bytes(MODE), g, q, lane);
+        // all four warps of the group go on, or none
+        const auto agree = [&](bool ok) {
+            int all;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                         "barrier.cta.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                         : "=r"(all)
+                         : "r"((int)ok), "r"(1 + g)
+                         : "memory");
+            return all != 0;
+        };
+        // `n` finished columns of the accumulator, from column c0 of the tile on
+        const auto finish = [&](uint32_t(&v)[kChunk], int m0, int n0, int c0, int n, int next) {
+            if constexpr (MODE == kWgrad) {
+                // lane = one row of dw, consecutive values of it
+                const int m = m0 + q * 32 + lane;
+                const size_t r = (size_t)t.e * p.M + m;
+                if (m < p.M) {
+                    if (!is_bias(t)) store_row(p, r * p.N + n0 + c0, v, n);
+                    else if (p.fp32) static_cast<float *>(p.db)[r] = __uint_as_float(v[0]);
+                    else static_cast<__nv_bfloat16 *>(p.db)[r] = __float2bfloat16_rn(__uint_as_float(v[0]));
+                }
+                __syncwarp();
+            } else {
+                ep.finish(v, t.row0 + n0 + c0, n, next);
+            }
+        };
         while (walk.next(t)) {
-            const int iters = iterations(t);
+            const int iters = span(t).count;
             const int m0 = t.m * kBM + (int)rank * kTileM, n0 = t.n * BN;
             const int cols = is_bias(t) ? 1 : min(BN, (MODE == kWgrad ? p.N : t.rows) - n0);
-            const int c_first = ((g + turn) & 1) * kChunk;
-            turn += (cols + kChunk - 1) / kChunk;
-            const int row0 = t.row0 + n0;
-            if (MODE != kWgrad) {
-                ep.tile(t.e, m0);
-                ep.ahead(row0 + c_first, min(kChunk, cols - c_first));
-            }
-            if (iters != 0) {
-                // all four warps go on, or none
-                const bool ok = wait(&c->acc_full[acc], aph, c, p.ws);
-                int all;
-                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                             "barrier.cta.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                             : "=r"(all)
-                             : "r"((int)ok), "r"(1 + g)
-                             : "memory");
-                if (!all) break;
-                tc_fence_after();
-            }
             const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + acc * BN;
-            bool released = iters == 0;
-            for (int c0 = c_first; c0 < cols; c0 += 2 * kChunk) {
-                uint32_t v[kChunk];
-                if (iters != 0) {
-                    tmem_ld(from + c0, v);
-                    tmem_wait_ld();
-                    if (c0 + 2 * kChunk >= cols) {  // this warp's last look at the accumulator
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(cluster_addr(&c->acc_empty[acc], 0));
-                        released = true;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kChunk; ++i) v[i] = 0u;
-                }
-                if constexpr (MODE == kWgrad) {
-                    // lane = one row of dw, 32 consecutive values of it
-                    const int m = m0 + q * 32 + lane;
-                    const size_t r = (size_t)t.e * p.M + m;
-                    if (m < p.M) {
-                        if (!is_bias(t)) store_row(p, r * p.N + n0 + c0, v, min(kChunk, cols - c0));
-                        else if (p.fp32) static_cast<float *>(p.db)[r] = __uint_as_float(v[0]);
-                        else static_cast<__nv_bfloat16 *>(p.db)[r] = __float2bfloat16_rn(__uint_as_float(v[0]));
-                    }
-                    __syncwarp();
-                } else {
-                    ep.finish(v, row0 + c0, min(kChunk, cols - c0), min(kChunk, cols - c0 - 2 * kChunk));
-                }
-            }
-            if (!released) {  // no chunk of this tile was this group's
+            const auto release = [&] {  // this warp's last look at the accumulator
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(cluster_addr(&c->acc_empty[acc], 0));
+                if (lane == 0) mbar_arrive_remote(cluster_addr(&c->acc_empty[acc], lead));
+            };
+            if constexpr (!SPLIT) {
+                const int c_first = ((g + turn) & 1) * kChunk;
+                turn += (cols + kChunk - 1) / kChunk;
+                if (MODE != kWgrad) {
+                    ep.tile(t.e, m0);
+                    ep.ahead(t.row0 + n0 + c_first, min(kChunk, cols - c_first));
+                }
+                if (iters != 0) {
+                    if (!agree(wait(&c->acc_full[acc], aph, c, p.ws))) break;
+                    tc_fence_after();
+                    if (c_first >= cols) release();
+                }
+                for (int c0 = c_first; c0 < cols; c0 += 2 * kChunk) {
+                    uint32_t v[kChunk];
+                    if (iters != 0) {
+                        tmem_ld(from + c0, v);
+                        tmem_wait_ld();
+                        if (c0 + 2 * kChunk >= cols) release();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) v[i] = 0u;
+                    }
+                    finish(v, m0, n0, c0, min(kChunk, cols - c0), min(kChunk, cols - c0 - 2 * kChunk));
+                }
+            } else {
+                // Every block has sums over its part of k for all columns; it
+                // finishes BN / split of the columns.  Each sends the others'
+                // columns to them and adds what arrives in the order of k.
+                const int w = BN / split, shift = __ffs(w) - 1, mine = (int)self * w, own = min(w, cols - mine);
+                if (MODE != kWgrad) {
+                    ep.tile(t.e, m0);
+                    ep.ahead(t.row0 + n0 + mine + g * kChunk, min(kChunk, own - g * kChunk));
+                }
+                bool ok = iters == 0 || wait(&c->acc_full[acc], aph, c, p.ws);
+                ok = wait(&c->taken, turn ^ 1, c, p.ws) && ok;  // the last tile's sums have been read
+                if (!agree(ok)) break;
+                tc_fence_after();
+                for (int c0 = g * kChunk; c0 < cols; c0 += 2 * kChunk) {
+                    uint32_t v[kChunk];
+                    if (iters != 0) {
+                        tmem_ld(from + c0, v);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) {
+                        const int col = c0 + i;
+                        if (col >= cols) break;
+                        st_cluster(cluster_addr(join + ((int)self * w + (col & (w - 1))) * kTileM + q * 32 + lane,
+                                                col >> shift),
+                                   iters != 0 ? v[i] : 0u);
+                    }
+                }
+                if (iters != 0) release();
+                fence_cluster();
+                __syncwarp();
+                if (lane < split) mbar_arrive_remote(cluster_addr(&c->joined, lane));
+                if (!agree(wait(&c->joined, turn, c, p.ws))) break;
+                fence_cluster();
+                for (int c0 = g * kChunk; c0 < own; c0 += 2 * kChunk) {
+                    uint32_t v[kChunk];
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) {
+                        float sum = 0.0f;
+                        if (c0 + i < own)
+                            for (int o = 0; o < split; ++o) sum += join[(o * w + c0 + i) * kTileM + q * 32 + lane];
+                        v[i] = __float_as_uint(sum);
+                    }
+                    finish(v, m0, n0, mine + c0, min(kChunk, own - c0), min(kChunk, own - c0 - 2 * kChunk));
+                }
+                fence_cluster();
+                __syncwarp();
+                if (lane < split) mbar_arrive_remote(cluster_addr(&c->taken, lane));
+                turn ^= 1;
             }
             if (iters != 0) {
                 acc ^= 1;
@@ -826,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     }
     __syncwarp();
     tc_fence_before();
-    if (CG == 2) cluster_sync_all();
+    if (kCluster) cluster_sync_all();
     else __syncthreads();
     if (warp == 2) tmem_free<CG>(tmem, tmem_cols(BN));
 }
@@ -876,59 +953,118 @@ cudaError_t encode_rows(CUtensorMap *m, bool fp8, const void *base, int cols, in
     return encode(m, fp8, base, 2, d, st, b);
 }
 
-template <int CG, int BN, int MODE, bool FP8>
+template <int CG, int BN, int MODE, bool FP8, bool SPLIT>
 cudaError_t launch(const Params &p, cudaStream_t s)
 {
     // No programmatic dependent launch here: the kernel takes whole SMs and
     // their tensor memory, so the next one has nowhere to start early.
-    const auto fn = experts_kernel<CG, BN, MODE, FP8>;
-    cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes(CG, BN, MODE));
+    const auto fn = experts_kernel<CG, BN, MODE, FP8, SPLIT>;
+    cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes(CG, BN, MODE, SPLIT));
     if (err != cudaSuccess) return err;
     // the most tiles that offsets over these rows can give
     const long long tm = (p.M + kTileM * CG - 1) / (kTileM * CG);
     const long long tn = MODE == kWgrad ? (long long)p.E * ((p.N + BN - 1) / BN + 1)
                                         : p.rows / BN + (p.rows < p.E ? p.rows : p.E);
-    long long blocks = device_sm_count() / CG;
-    if (tm * tn < blocks) blocks = tm * tn;
-    if (blocks < 1) blocks = 1;
+    const int cluster = SPLIT ? p.split : CG;
 
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks * CG));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes(CG, BN, MODE);
+    cfg.dynamicSmemBytes = smem_bytes(CG, BN, MODE, SPLIT);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 1 : 0;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.gridDim = dim3((unsigned)cluster);
+    long long blocks = device_sm_count() / cluster;
+    if (cluster > 2) {
+        // how many such clusters the GPCs hold at once: asked once per device and size
+        static std::atomic<int> held[64][2];
+        int dev = 0;
+        err = cudaGetDevice(&dev);
+        if (err != cudaSuccess) return err;
+        int n = dev < 64 ? held[dev][cluster / 8].load(std::memory_order_relaxed) : 0;
+        if (n == 0) {
+            err = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+            if (err != cudaSuccess) return err;
+            if (dev < 64) held[dev][cluster / 8].store(n, std::memory_order_relaxed);
+        }
+        if (n < blocks) blocks = n;
+    }
+    if (tm * tn < blocks) blocks = tm * tn;
+    if (blocks < 1) blocks = 1;
+    cfg.gridDim = dim3((unsigned)(blocks * cluster));
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
-// Tile width along the ragged axis: the rows an expert has on average.
-int pick_width(int rows, int E)
+// How a product is cut: columns of n per tile (256: a pair of SMs and 256 of
+// m; else one SM and 128), and blocks that share a tile's k.
+struct Cut {
+    int bn, split;
+};
+
+// The cut with the least time for tiles in whole waves over the SMs.  The
+// constants are cycles, measured: a stage of 64 (e4m3: 128) of k takes about
+// 550 for 256 and 128 columns (32 KB a block; the pair does four times the
+// work in it) and 350 for 32 (20 KB); after the last stage the accumulator
+// takes about 1000 per 32 columns and group, and a joint sum about 2500.
+// `live` experts have `n` of the ragged axis together (`each`: wgrad, whose n
+// is the same for every expert); their sizes are not known on the host, half
+// a tile each is taken for lost.
+Cut pick(int m, long long n, int live, bool each, long long k_stages, bool narrow)
 {
-    const int mean = rows / E;
-    return mean <= 32 ? 32 : mean <= 128 ? 128 : 256;
+    Cut best = {256, 1};
+    double least = 0.0;
+    const int sms = device_sm_count();
+    for (int bn = 256; bn >= (narrow ? 32 : 128); bn = bn == 256 ? 128 : 32) {
+        const int cg = bn == 256 ? 2 : 1;
+        const long long tm = (m + 128 * cg - 1) / (128 * cg);
+        long long tn = live == 1 || each ? (n + bn - 1) / bn * (each ? live : 1) : n / bn + (live + 1) / 2;
+        if (tn < live) tn = live;
+        for (int split = 1; split <= (cg == 2 ? 1 : 8); split *= 2) {
+            if (split > 1 && k_stages < 4 * split) break;
+            // clusters of 4 and 8 leave some SMs of a GPC over
+            const long long slots = split < 4 ? sms / (cg * split) : sms * 7 / 8 / split;
+            const long long waves = (tm * tn + slots - 1) / slots;
+            const double cycles = (double)waves * k_stages / split * (bn == 32 ? 350 : 550) +
+                                  1000.0 * ((bn / split + 63) / 64) + (split > 1 ? 2500.0 * waves : 0.0);
+            if (least == 0.0 || cycles < least) {
+                least = cycles;
+                best = {bn, split};
+            }
+        }
+        if (bn == 32) break;
+    }
+    return best;
 }
 
-}  // namespace
-
-cudaError_t launch_expert_linear(const moe_rows *G, const void *x, const float *x_scales, int K, const void *w,
-                                 const float *w_scales, int N, const void *bias, int act, const void *residual,
-                                 void *y, void *saved, void *saved_scales, cudaStream_t s)
+template <int MODE, bool FP8>
+cudaError_t launch_cut(Params &p, const Cut &c, cudaStream_t s)
 {
-    if (G->rows == 0) return cudaSuccess;
-    const bool fp8 = x_scales != nullptr;
+    p.split = c.split;
+    if (c.bn == 256) return launch<2, 256, MODE, FP8, false>(p, s);
+    if constexpr (MODE != kWgrad)
+        if (c.bn == 32)
+            return c.split > 1 ? launch<1, 32, MODE, FP8, true>(p, s) : launch<1, 32, MODE, FP8, false>(p, s);
+    return c.split > 1 ? launch<1, 128, MODE, FP8, true>(p, s) : launch<1, 128, MODE, FP8, false>(p, s);
+}
+
+
+template <bool FP8>
+cudaError_t linear(const moe_rows *G, const void *x, const float *x_scales, int K, const void *w,
+                   const float *w_scales, int N, const void *bias, int act, const void *residual, void *y,
+                   void *saved, void *saved_scales, cudaStream_t s)
+{
     Params p = {};
     p.offsets = G->offsets;
     p.ws = G->ws;
     p.E = G->E;
     p.rows = G->rows;
     p.M = N;
-    p.K = fp8 ? K : 2 * K;
+    p.K = FP8 ? K : 2 * K;
     p.act = act;
     p.glu = act == MOE_ACT_SWIGLU;
     p.bias = static_cast<const __nv_bfloat16 *>(bias);
@@ -938,29 +1074,24 @@ cudaError_t launch_expert_linear(const moe_rows *G, const void *x, const float *
     p.y = static_cast<__nv_bfloat16 *>(y);
     p.saved = static_cast<uint8_t *>(saved);
     p.saved_scales = static_cast<uint8_t *>(saved_scales);
-    const int bn = pick_width(G->rows, G->E), cg = bn == 256 ? 2 : 1, elems = fp8 ? 128 : 64;
+    const int elems = FP8 ? 128 : 64;
+    const Cut cut = pick(N, G->rows, G->rows < G->E ? G->rows : G->E, false, (K + elems - 1) / elems, true);
     // w as [E][N/halves][halves][K] with the halves inside: one load brings
     // gate and up rows alternating, so that a pair of them ends in one lane
     const uint64_t h = p.glu ? 2 : 1, n = (uint64_t)N / h;
     const uint64_t d[4] = {(uint64_t)K, h, n, (uint64_t)G->E};
     const uint64_t st[3] = {n * K, (uint64_t)K, (uint64_t)N * K};
     const uint32_t b[4] = {(uint32_t)elems, (uint32_t)h, (uint32_t)(kTileM / h), 1};
-    cudaError_t err = encode(&p.ma, fp8, w, 4, d, st, b);
-    if (err == cudaSuccess) err = encode_rows(&p.mb, fp8, x, K, G->rows, elems, bn / cg);
+    cudaError_t err = encode(&p.ma, FP8, w, 4, d, st, b);
+    if (err == cudaSuccess) err = encode_rows(&p.mb, FP8, x, K, G->rows, elems, cut.bn == 256 ? 128 : cut.bn);
     if (err != cudaSuccess) return err;
-    if (fp8)
-        return bn == 32    ? launch<1, 32, kLinear, true>(p, s)
-               : bn == 128 ? launch<1, 128, kLinear, true>(p, s)
-                           : launch<2, 256, kLinear, true>(p, s);
-    return bn == 32    ? launch<1, 32, kLinear, false>(p, s)
-           : bn == 128 ? launch<1, 128, kLinear, false>(p, s)
-                       : launch<2, 256, kLinear, false>(p, s);
+    return launch_cut<kLinear, FP8>(p, cut, s);
 }
 
-cudaError_t launch_expert_dgrad(const moe_rows *G, const void *dy, int N, const void *w, int K, int act,
-                                const void *saved, const void *saved_scales, void *dx, void *a, cudaStream_t s)
+template <int MODE>
+cudaError_t dgrad(const moe_rows *G, const void *dy, int N, const void *w, int K, int act, const void *saved,
+                  const void *saved_scales, void *dx, void *a, cudaStream_t s)
 {
-    if (G->rows == 0) return cudaSuccess;
     Params p = {};
     p.offsets = G->offsets;
     p.ws = G->ws;
@@ -973,46 +1104,15 @@ cudaError_t launch_expert_dgrad(const moe_rows *G, const void *dy, int N, const 
     p.a = static_cast<__nv_bfloat16 *>(a);
     p.saved = static_cast<uint8_t *>(const_cast<void *>(saved));
     p.saved_scales = static_cast<uint8_t *>(const_cast<void *>(saved_scales));
-    const int bn = pick_width(G->rows, G->E), cg = bn == 256 ? 2 : 1;
+    const Cut cut = pick(K, G->rows, G->rows < G->E ? G->rows : G->E, false, (N + 63) / 64, true);
     const uint64_t d[4] = {(uint64_t)K, (uint64_t)N, (uint64_t)G->E, 1};
     const uint64_t st[3] = {(uint64_t)K, (uint64_t)N * K, (uint64_t)N * K};
     const uint32_t b[4] = {64, 64, 1, 1};
     cudaError_t err = encode(&p.ma, false, w, 4, d, st, b);
-    if (err == cudaSuccess) err = encode_rows(&p.mb, false, dy, N, G->rows, 64, bn / cg);
+    if (err == cudaSuccess) err = encode_rows(&p.mb, false, dy, N, G->rows, 64, cut.bn == 256 ? 128 : cut.bn);
     if (err != cudaSuccess) return err;
-    if (act != MOE_ACT_NONE)
-        return bn == 32    ? launch<1, 32, kDgradSaved, false>(p, s)
-               : bn == 128 ? launch<1, 128, kDgradSaved, false>(p, s)
-                           : launch<2, 256, kDgradSaved, false>(p, s);
-    return bn == 32    ? launch<1, 32, kDgrad, false>(p, s)
-           : bn == 128 ? launch<1, 128, kDgrad, false>(p, s)
-                       : launch<2, 256, kDgrad, false>(p, s);
+    return launch_cut<MODE, false>(p, cut, s);
 }
 
-cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const void *x, int K, void *dw, void *db,
-                                int fp32, cudaStream_t s)
-{
-    if (G->rows == 0) {
-        const size_t n = (size_t)G->E * N * (fp32 ? 4 : 2);
-        const cudaError_t err = db ? cudaMemsetAsync(db, 0, n, s) : cudaSuccess;
-        return err == cudaSuccess ? cudaMemsetAsync(dw, 0, n * K, s) : err;
-    }
-    Params p = {};
-    p.offsets = G->offsets;
-    p.ws = G->ws;
-    p.E = G->E;
-    p.rows = G->rows;
-    p.M = N;
-    p.N = K;
-    p.fp32 = fp32;
-    p.dw = dw;
-    p.db = db;
-    cudaError_t err = encode_rows(&p.ma, false, dy, N, G->rows, 64, 64);
-    if (err == cudaSuccess) err = encode_rows(&p.mb, false, x, K, G->rows, 64, 64);
-    if (err != cudaSuccess) return err;
-    // few tiles: one SM per tile of half the size keeps more of them busy
-    const long long pairs = (long long)G->E * ((N + 255) / 256) * ((K + 255) / 256);
-    return pairs * 2 <= device_sm_count() ? launch<1, 128, kWgrad, false>(p, s) : launch<2, 256, kWgrad, false>(p, s);
-}
-
+}  // namespace
 }  // namespace moe

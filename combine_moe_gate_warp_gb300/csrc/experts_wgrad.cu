@@ -1,0 +1,31 @@
+// experts_wgrad.cu -- the weights' and bias gradients (experts.cuh).
+#include "experts.cuh"
+
+namespace moe {
+
+cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const void *x, int K, void *dw, void *db,
+                                int fp32, cudaStream_t s)
+{
+    if (G->rows == 0) {
+        const size_t n = (size_t)G->E * N * (fp32 ? 4 : 2);
+        const cudaError_t err = db ? cudaMemsetAsync(db, 0, n, s) : cudaSuccess;
+        return err == cudaSuccess ? cudaMemsetAsync(dw, 0, n * K, s) : err;
+    }
+    Params p = {};
+    p.offsets = G->offsets;
+    p.ws = G->ws;
+    p.E = G->E;
+    p.rows = G->rows;
+    p.M = N;
+    p.N = K;
+    p.fp32 = fp32;
+    p.dw = dw;
+    p.db = db;
+    cudaError_t err = encode_rows(&p.ma, false, dy, N, G->rows, 64, 64);
+    if (err == cudaSuccess) err = encode_rows(&p.mb, false, x, K, G->rows, 64, 64);
+    if (err != cudaSuccess) return err;
+    const Cut cut = pick(N, K, G->E, true, (G->rows / G->E + 63) / 64, false);
+    return launch_cut<kWgrad, false>(p, cut, s);
+}
+
+}  // namespace moe

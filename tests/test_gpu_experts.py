@@ -21,8 +21,9 @@ def _built():
 
 
 def rows_for(counts, mean):
-    """Rows of buffers that hold these groups and make `mean` rows per expert
-    (the library picks its tile width by them)."""
+    """Rows of buffers that hold these groups and make `mean` rows per expert:
+    the library cuts its tiles by the rows that buffers hold, 32 wide for few
+    of them and 256 wide for pairs of SMs for the most."""
     return max(sum(counts), mean * len(counts))
 
 
@@ -32,10 +33,10 @@ def padded(t, rows, fill=float("nan")):
     return out
 
 
-@pytest.mark.parametrize("mean", [8, 100, 300])
+@pytest.mark.parametrize("mean", [8, 300, 9000])
 @pytest.mark.parametrize("K,N", [(64, 128), (8, 8), (72, 264), (520, 96), (1032, 520)])
 def test_linear_plain(mean, K, N):
-    counts = COUNTS if mean > 8 else [0, 1, 7, 0, 20, 33, 3]
+    counts = COUNTS if mean != 8 else [0, 1, 7, 0, 20, 33, 3]
     R, rows = sum(counts), rows_for(counts, mean)
     x, w = normal(R, K, seed=1), normal(len(counts), N, K, seed=2, std=K ** -0.5)
     r = ExpertRows(offsets_of(counts), rows=rows)
@@ -48,7 +49,7 @@ def test_linear_plain(mean, K, N):
 
 
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "swiglu"])
-@pytest.mark.parametrize("mean", [8, 100, 300])
+@pytest.mark.parametrize("mean", [8, 300, 9000])
 @pytest.mark.parametrize("bias,residual,save", [(True, False, False), (True, True, True), (False, True, False)])
 def test_linear_epilogues(act, mean, bias, residual, save):
     counts, K, N = COUNTS, 200, 448
@@ -88,12 +89,12 @@ def check_saved(saved, u, e, R):
     assert_near(got, u, half + e, "saved")
 
 
-@pytest.mark.parametrize("mean", [8, 100, 300])
+@pytest.mark.parametrize("mean", [8, 300, 9000])
 @pytest.mark.parametrize("act,K,N", [("none", 16, 24), ("swiglu", 400, 288), ("silu", 1040, 136)])
 def test_linear_e4m3(mean, act, K, N):
     """x = zero + scale * code, w = scale * code: from the codes in 64 bits.
     The sums are fp32 (products of codes, then three fp32 steps)."""
-    counts = COUNTS if mean > 8 else [5, 0, 1, 17, 40]
+    counts = COUNTS if mean != 8 else [5, 0, 1, 17, 40]
     R, rows, E = sum(counts), rows_for(counts, mean), len(counts)
     g = torch.Generator().manual_seed(9)
     # codes of magnitude up to 448, no NaN patterns
@@ -121,10 +122,10 @@ def test_linear_e4m3(mean, act, K, N):
     assert_near(y[:R], want, err + BF16 * (want.abs() + err), "y")
 
 
-@pytest.mark.parametrize("mean", [8, 100, 300])
+@pytest.mark.parametrize("mean", [8, 300, 9000])
 @pytest.mark.parametrize("K,N", [(128, 64), (8, 8), (264, 72), (96, 1000)])
 def test_dgrad(mean, K, N):
-    counts = COUNTS if mean > 8 else [0, 1, 7, 0, 20, 33, 3]
+    counts = COUNTS if mean != 8 else [0, 1, 7, 0, 20, 33, 3]
     R, rows, E = sum(counts), rows_for(counts, mean), len(counts)
     dy, w = normal(R, N, seed=11), normal(E, N, K, seed=12, std=N ** -0.5)
     r = ExpertRows(offsets_of(counts), rows=rows)
@@ -137,7 +138,7 @@ def test_dgrad(mean, K, N):
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu", "swiglu"])
-@pytest.mark.parametrize("mean", [8, 100, 300])
+@pytest.mark.parametrize("mean", [8, 300, 9000])
 @pytest.mark.parametrize("recompute", [True, False])
 def test_dgrad_through_saved(act, mean, recompute):
     counts, K, N = ([3, 0, 1, 40] if mean == 8 else COUNTS), 160, 200
@@ -196,7 +197,7 @@ def test_wgrad_many_tiles(E, N, K):
     check_wgrad(dw, db, dy, x, counts, torch.bfloat16)
 
 
-@pytest.mark.parametrize("mean", [40, 300])
+@pytest.mark.parametrize("mean", [40, 3000])
 def test_linear_many_tiles(mean):
     counts = [(53 * e) % 400 + (700 if e == 5 else 0) for e in range(24)]
     rows = max(sum(counts), 24 * mean)
@@ -210,6 +211,79 @@ def test_linear_many_tiles(mean):
     dx = r.dgrad(y, w)
     d, e = linear64(y[:R], w.mT, counts)
     assert_near(dx[:R], d, e + BF16 * (d.abs() + e), "dx")
+
+
+@pytest.mark.parametrize("counts,K,N", [
+    ([4], 2048, 256), ([33], 2048, 4096), ([20], 1040, 8192), ([1000], 4096, 1024), ([512], 4096, 512),
+    ([3, 0, 40, 1], 2048, 512), ([130, 5, 0, 200], 2056, 272)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_split_sums(counts, K, N, act):
+    """Few tiles and a long k: blocks of a cluster share it and join their
+    sums.  Forward with everything in the epilogue, the rows' gradient plain
+    and through the saved layer, the weights' gradient."""
+    R, E = sum(counts), len(counts)
+    rows = R + 3
+    x, w, b = normal(R, K, seed=60), normal(E, N, K, seed=61, std=K ** -0.5), normal(E, N, seed=62)
+    cols = N // 2 if act == "swiglu" else N
+    res = normal(R, cols, seed=63)
+    r = ExpertRows(offsets_of(counts), rows=rows)
+    can_save = N % 64 == 0
+    saved = r.new_saved(N) if can_save else None
+    out = torch.full((rows, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    r.linear(padded(x, rows), w, bias=b, act=act, residual=padded(res, rows), saved=saved, out=out)
+    assert r.status() == 0
+    u, e = linear64(x, w, counts, b)
+    want, err = act64(u, act) + res.double(), act_error(u, e, act)
+    err = err + 2.0 ** -23 * want.abs()
+    assert_near(out[:R], want, err + BF16 * (want.abs() + err), "y")
+    assert bool((out[R:] == 7.0).all())
+    if can_save:
+        check_saved(saved, u, e, R)
+    # dgrad with the long axis as its k
+    wt = normal(E, K, N, seed=64, std=K ** -0.5)
+    dy = normal(R, K, seed=65)
+    d, e = linear64(dy, wt.mT, counts)
+    dx = r.dgrad(padded(dy, rows), wt)
+    assert_near(dx[:R], d, e + BF16 * (d.abs() + e), "dx")
+    if can_save:
+        C = 2 * N if act == "swiglu" else N
+        codes, scales = encode_saved(normal(R, C, seed=66, std=1.5))
+        name = "gelu" if act == "none" else act
+        du = r.dgrad(padded(dy, rows), wt, act=name, saved=SavedLayer(padded(codes, rows, 0x7F),
+                                                                      padded(scales, rows, 0xFF)))
+        u = decode64(codes, scales)
+        want, err = grad64(u, d, name), grad_error(u, d, e, name)
+        assert_near(du[:R], want, err + BF16 * (want.abs() + err), "du")
+    assert r.status() == 0
+
+
+@pytest.mark.parametrize("counts", [[4000], [2111], [1500, 0, 700], [64, 3000]])
+@pytest.mark.parametrize("N,K", [(256, 256), (136, 72), (1024, 512)])
+def test_wgrad_split(counts, N, K):
+    """Many rows and few tiles: blocks share the rows of a tile."""
+    R = sum(counts)
+    dy, x = normal(R, N, seed=67), normal(R, K, seed=68)
+    r = ExpertRows(offsets_of(counts), rows=R + 9)
+    for dtype in (torch.bfloat16, torch.float32):
+        dw, db = r.wgrad(padded(dy, R + 9), padded(x, R + 9), bias=True, dtype=dtype)
+        assert r.status() == 0
+        check_wgrad(dw, db, dy, x, counts, dtype)
+
+
+@pytest.mark.parametrize("mean", [8, 9000])
+def test_same_bits_twice(mean):
+    """No result depends on timing."""
+    counts = [50, 0, 31, 129]
+    rows = rows_for(counts, mean)
+    x, w = normal(210, 2048, seed=69), normal(4, 512, 2048, seed=70, std=0.02)
+    r = ExpertRows(offsets_of(counts), rows=rows)
+    xp = padded(x, rows, 0.0)
+    y, dw = r.linear(xp, w)[:210].clone(), None
+    for _ in range(5):
+        assert torch.equal(r.linear(xp, w)[:210], y)
+        again = r.wgrad(xp, xp, bias=True, dtype=torch.float32)
+        assert dw is None or (torch.equal(again[0], dw[0]) and torch.equal(again[1], dw[1]))
+        dw = again
 
 
 @pytest.mark.parametrize("T", [1, 4, 33, 129, 1000])
@@ -255,7 +329,7 @@ def test_no_row_reads_another():
     x[20:50] = float("nan")
     dy[25] = float("inf")
     w[1] = float("nan")
-    for mean in (8, 300):
+    for mean in (8, 300, 9000):
         buf = max(rows, 5 * mean)
         r = ExpertRows(offsets_of(counts), rows=buf)
         xp, dp = padded(x, buf), padded(dy, buf, float("inf"))
