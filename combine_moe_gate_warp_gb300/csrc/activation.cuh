@@ -15,10 +15,29 @@ namespace moe {
 // magnitudes, is far below the bf16 rounding of every result.
 __device__ __forceinline__ float logistic(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
 
+// The normal distribution function Phi(u) = (1 + erf(u / sqrt 2)) / 2 and
+// exp(-u^2 / 2), by formula 7.1.26 of Abramowitz and Stegun, Handbook of
+// Mathematical Functions: erfc(z) = (a1 t + ... + a5 t^5) exp(-z^2) with
+// t = 1 / (1 + 0.3275911 z), off by at most 1.5e-7.  A third of erff's
+// instructions, and both come from one exponential.
+__device__ __forceinline__ float normal_cdf(float u, float &density)
+{
+    const float z = fabsf(u) * 0.70710678118654752f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, z, 1.0f));
+    float poly = fmaf(1.061405429f, t, -1.453152027f);
+    poly = fmaf(poly, t, 1.421413741f);
+    poly = fmaf(poly, t, -0.284496736f);
+    poly = fmaf(poly, t, 0.254829592f);
+    density = __expf(-z * z);
+    const float tail = 0.5f * poly * t * density;
+    return u > 0.0f ? 1.0f - tail : tail;
+}
+
 __device__ __forceinline__ float act_value(float u, int act)
 {
+    float d;
     if (act == MOE_ACT_SILU) return u * logistic(u);
-    if (act == MOE_ACT_GELU) return 0.5f * u * (1.0f + erff(u * 0.70710678118654752f));
+    if (act == MOE_ACT_GELU) return u * normal_cdf(u, d);
     return u;
 }
 
@@ -29,8 +48,11 @@ __device__ __forceinline__ float act_slope(float u, int act)
         const float q = logistic(u);
         return q * (1.0f + u * (1.0f - q));
     }
-    if (act == MOE_ACT_GELU)
-        return 0.5f * (1.0f + erff(u * 0.70710678118654752f)) + u * __expf(-0.5f * u * u) * 0.39894228040143268f;
+    if (act == MOE_ACT_GELU) {
+        float d;
+        const float cdf = normal_cdf(u, d);
+        return fmaf(u * d, 0.39894228040143268f, cdf);
+    }
     return 1.0f;
 }
 

@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     }
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&c->full[i], CG);
+            mbar_init(&c->full[i], MODE == kWgrad ? CG : 1);
             mbar_init(&c->empty[i], 1);
             mbar_init(&c->tail[i], 1);
         }
@@ -635,60 +635,70 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
 
     if (warp == 0) {
         // ---- loads -------------------------------------------------------
-        int s = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        while (ok && walk.next(t)) {
-            const Span part = span(t);
-            const int m0 = t.m * kBM + (int)rank * kTileM;
-            const int n0 = t.n * BN + (int)rank * (width(t) / CG);
-            const bool no_b = is_bias(t);
-            const uint32_t bytes = no_b ? kStageA : kStage;
-            for (int i = part.first; i < part.first + part.count; ++i) {
-                ok = wait(&c->empty[s], ph ^ 1, c, p.ws);
-                if (!ok) break;
-                if (lane == 0) {
+        // One thread, as for the matrix instructions: what it does for a
+        // stage (about 400 cycles with warp-wide waits) bounds narrow tiles.
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 1;
+            bool ok = true;
+            while (ok && walk.next(t)) {
+                const Span part = span(t);
+                const int m0 = t.m * kBM + (int)rank * kTileM;
+                const int row = t.row0 + t.n * BN + (int)rank * (width(t) / CG);
+                const int a0 = MODE == kLinear && p.glu ? m0 / 2 : m0;
+                const bool no_b = is_bias(t);
+                const uint32_t bytes = no_b ? kStageA : kStage;
+                for (int i = part.first; i < part.first + part.count; ++i) {
+                    ok = poll(&c->empty[s], ph, c, p.ws);
+                    if (!ok) break;
                     unsigned char *sa = smem + s * kStage, *sb = sa + kStageA;
-                    uint32_t bar;
-                    if (MODE == kWgrad && t.rows - i * 64 < 64) {  // a tail: see warp 3
-                        mbar_arrive_expect_tx(&c->tail[s], bytes);
-                        bar = cluster_addr(&c->tail[s], self);
-                    } else {
-                        bar = cluster_addr(&c->full[s], lead);
-                        mbar_arrive_expect_tx_remote(bar, bytes);
-                    }
                     const int k0 = i * kElems;
-                    if (MODE == kLinear) {
-                        tma_load_4d<CG>(sa, &p.ma, k0, 0, p.glu ? m0 / 2 : m0, t.e, bar);
-                        tma_load_2d<CG>(sb, &p.mb, k0, t.row0 + n0, bar);
-                    } else if (MODE == kDgrad || MODE == kDgradSaved) {
-                        for (int j = 0; j < 2; ++j)
-                            tma_load_4d<CG>(sa + j * 8192, &p.ma, m0 + 64 * j, k0, t.e, 0, bar);
-                        tma_load_2d<CG>(sb, &p.mb, k0, t.row0 + n0, bar);
-                    } else {
+                    uint32_t bar = smem_addr(&c->full[s]);
+                    if constexpr (MODE == kWgrad) {
+                        if (t.rows - k0 < 64) {  // a tail: see warp 3
+                            bar = smem_addr(&c->tail[s]);
+                            mbar_arrive_expect_tx(&c->tail[s], bytes);
+                        } else if (CG == 1 || self == 0) {
+                            mbar_arrive_expect_tx(&c->full[s], bytes);
+                        } else {
+                            bar = cluster_addr(&c->full[s], 0);
+                            mbar_arrive_expect_tx_remote(bar, bytes);
+                        }
                         for (int j = 0; j < 2; ++j)
                             tma_load_2d<CG>(sa + j * 8192, &p.ma, m0 + 64 * j, t.row0 + k0, bar);
                         if (!no_b)
                             for (int j = 0; j < kHalfN / 64; ++j)
-                                tma_load_2d<CG>(sb + j * 8192, &p.mb, n0 + 64 * j, t.row0 + k0, bar);
+                                tma_load_2d<CG>(sb + j * 8192, &p.mb,
+                                                t.n * BN + (int)rank * (width(t) / CG) + 64 * j, t.row0 + k0, bar);
+                    } else {
+                        // the pair's first block expects the bytes of both
+                        if (CG == 1 || self == 0) mbar_arrive_expect_tx(&c->full[s], CG * kStage);
+                        else bar = cluster_addr(&c->full[s], 0);
+                        if constexpr (MODE == kLinear) {
+                            tma_load_4d<CG>(sa, &p.ma, k0, 0, a0, t.e, bar);
+                        } else {
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_4d<CG>(sa + j * 8192, &p.ma, a0 + 64 * j, k0, t.e, 0, bar);
+                        }
+                        tma_load_2d<CG>(sb, &p.mb, k0, row, bar);
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1;
                     }
                 }
-                __syncwarp();
+            }
+            // every stage read: no copy and no arrival is on its way to this
+            // block's shared memory when it ends
+            for (int i = 0; ok && i < kStages; ++i) {
+                ok = poll(&c->empty[s], ph, c, p.ws);
                 if (++s == kStages) {
                     s = 0;
                     ph ^= 1;
                 }
             }
         }
-        // every stage read: no copy and no arrival is on its way to this
-        // block's shared memory when it ends
-        for (int i = 0; ok && i < kStages; ++i) {
-            ok = wait(&c->empty[s], ph ^ 1, c, p.ws);
-            if (++s == kStages) {
-                s = 0;
-                ph ^= 1;
-            }
-        }
+        __syncwarp();
     } else if (MODE == kWgrad && warp == 3) {
         // ---- tails ---------------------------------------------------------
         // The last rows of an expert rarely fill 64 of k; the rows after them
@@ -718,16 +728,18 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         }
     } else if (warp == 1 && rank == 0) {
         // ---- matrix instructions ------------------------------------------
-        // One thread.  It looks at the next stage's barrier before it issues
-        // the current stage's instructions: the answer (about 100 cycles) is
-        // there when the issue, which blocks while the tensor cores' queue is
-        // full, has gone through.
-        if (lane == 0) {
+        // One elected thread issues; the warp walks the loop together, so that
+        // descriptors and addresses stay in uniform registers.  The next
+        // stage's barrier is looked at before the current stage's
+        // instructions: the answer is there when their issue, which blocks
+        // while the tensor cores' queue is full, has gone through.
+        {
             constexpr uint32_t kLeadA = kMnA ? 8192 : 16, kLeadB = kMnB ? 8192 : 16;
             constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
             const uint64_t da0 = smem_desc(smem_addr(smem), kLeadA, 1024);
             const uint64_t db0 = smem_desc(smem_addr(smem) + kStageA, kLeadB, 1024);
             const uint64_t ones = smem_desc(smem_addr(stg), kLeadB, 1024);
+            const bool one = elect_one();
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true, ready = false, more = walk.next(t);
@@ -740,31 +752,36 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 const uint32_t idesc = mma_idesc(FP8, kMnA, kMnB, kBM, width(t));
                 const uint32_t d = tmem + acc * BN;
                 const bool bias = is_bias(t);
-                ok = poll(&c->acc_empty[acc], aph ^ 1, c, p.ws);
+                const bool tail = MODE == kWgrad && CG == 2 && (t.rows & 63);
+                ok = wait(&c->acc_empty[acc], aph ^ 1, c, p.ws);
                 if (!ok) break;
                 tc_fence_after();
                 for (int i = 0; i < iters; ++i) {
-                    ok = ready || poll(&c->full[s], ph, c, p.ws);
+                    ok = ready || wait(&c->full[s], ph, c, p.ws);
                     if (!ok) break;
                     // the zeroed rows of a tail come from the peer's generic writes too
-                    if (MODE == kWgrad && CG == 2 && i == iters - 1 && (t.rows & 63))
-                        mbar_try_wait_acquire_cluster(&c->full[s], ph);
+                    if (tail && i == iters - 1) mbar_try_wait_acquire_cluster(&c->full[s], ph);
                     tc_fence_after();
                     const int now = s;
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1;
                     }
-                    ready = mbar_try_wait(&c->full[s], ph);
+                    const bool next = mbar_test_wait(&c->full[s], ph);
                     const uint64_t da = da0 + (uint64_t)(now * (kStage >> 4)), db = db0 + (uint64_t)(now * (kStage >> 4));
+                    if (one) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss<CG, FP8>(d, da + k * kStepA, bias ? ones : db + k * kStepB, idesc, (i | k) != 0);
-                    mma_commit<CG>(&c->empty[now]);
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss<CG, FP8>(d, da + k * kStepA, bias ? ones : db + k * kStepB, idesc, (i | k) != 0);
+                        mma_commit<CG>(&c->empty[now]);
+                    }
+                    __syncwarp();
                     if (i == 0) more = walk.next(t);  // the divisions of the next tile hide behind this one
+                    ready = __all_sync(0xFFFFFFFFu, next);
                 }
                 if (!ok) break;
-                mma_commit<CG>(&c->acc_full[acc]);
+                if (one) mma_commit<CG>(&c->acc_full[acc]);
+                __syncwarp();
                 acc ^= 1;
                 aph ^= acc == 0;
             }

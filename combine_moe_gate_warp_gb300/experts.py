@@ -198,11 +198,15 @@ class ExpertRows:
             raise ValueError("a: only with a saved layer")
         cols = 2 * K if code == abi.MOE_ACT_SWIGLU else K
         dp = _check(dy, torch.bfloat16, (self.rows, N), "dy", self.device)
-        sc, ss = (None, None) if saved is None else self._saved(saved, cols)
-        ap = self._opt(a, torch.bfloat16, (self.rows, K), "a")
+        sc = ss = ap = None
+        if saved is not None:
+            sc, ss = self._saved(saved, cols)
+            if a is not None:
+                ap = _check(a, torch.bfloat16, (self.rows, K), "a", self.device)
         out, op = self._out(out, torch.bfloat16, (self.rows, cols), "out")
-        abi._check(self._lib.moe_expert_dgrad(self._ref, dp, N, wp, K, code, sc, ss, op, ap, self._stream()),
-                   "moe_expert_dgrad")
+        st = self._lib.moe_expert_dgrad(self._ref, dp, N, wp, K, code, sc, ss, op, ap, self._stream())
+        if st:
+            abi._check(st, "moe_expert_dgrad")
         return out
 
     def wgrad(self, dy, x, *, bias: bool = False, dtype=torch.bfloat16, out=None, out_bias=None):
@@ -268,7 +272,11 @@ class ExpertFFN:
     (1 + 1/32 bytes per value): the backward pass recomputes the activation
     from it, in the same kernel that takes the gradient through it.  w1 is
     [E, N, H], w2 [E, H, F] with N = F (2F for swiglu); without the expert
-    axis for one plain group."""
+    axis for one plain group.
+
+    Like a RoutePlan the network owns the buffers of its results: ``y`` and
+    the gradients hold those of the last pass, and the next one overwrites
+    them."""
 
     def __init__(self, rows: ExpertRows, w1, w2, *, b1=None, b2=None, act: str = "swiglu", dtype=torch.bfloat16):
         N, H, _ = rows._weights(w1, torch.bfloat16)
@@ -281,21 +289,26 @@ class ExpertFFN:
         bf16 = dict(dtype=torch.bfloat16, device=rows.device)
         self.saved = rows.new_saved(N)
         self.hidden = torch.empty((rows.rows, F), **bf16)   # act(u): forward, and again in the backward pass
-        self._du = None
+        self.y = torch.empty((rows.rows, H), **bf16)
+        self.grads = self._du = None
 
     def forward(self, x, *, residual=None, out=None):
-        """x [rows, H] -> [rows, H] (+ residual)."""
+        """x [rows, H] -> [rows, H] (+ residual), in ``y`` or ``out``."""
         r = self.rows
         r.linear(x, self.w1, bias=self.b1, act=self.act, saved=self.saved, out=self.hidden)
-        return r.linear(self.hidden, self.w2, bias=self.b2, residual=residual, out=out)
+        return r.linear(self.hidden, self.w2, bias=self.b2, residual=residual, out=self.y if out is None else out)
 
     def backward(self, dy, x) -> FFNGrads:
         """Gradients of the last forward pass; x is its input."""
         r = self.rows
-        if self._du is None:
+        if self.grads is None:
             self._du = torch.empty(self.saved.codes.shape, dtype=torch.bfloat16, device=r.device)
+            like = lambda w: None if w is None else torch.empty_like(w, dtype=self.dtype)  # noqa: E731
+            self.grads = FFNGrads(torch.empty_like(self.y), like(self.w1), like(self.w2), like(self.b1),
+                                  like(self.b2))
+        g = self.grads
         du = r.dgrad(dy, self.w2, act=self.act, saved=self.saved, out=self._du, a=self.hidden)
-        dw2, db2 = r.wgrad(dy, self.hidden, bias=self.b2 is not None, dtype=self.dtype)
-        dx = r.dgrad(du, self.w1)
-        dw1, db1 = r.wgrad(du, x, bias=self.b1 is not None, dtype=self.dtype)
-        return FFNGrads(dx, dw1, dw2, db1, db2)
+        r.wgrad(dy, self.hidden, dtype=self.dtype, out=g.dw2, out_bias=g.db2)
+        r.dgrad(du, self.w1, out=g.dx)
+        r.wgrad(du, x, dtype=self.dtype, out=g.dw1, out_bias=g.db1)
+        return g
