@@ -89,6 +89,8 @@ struct Params {
     int K;         // linear, dgrad: extent of k, in bytes
     int act, glu;  // glu: A's rows alternate gate and up columns
     int fp32;
+    int whole_a, whole_b;  // an MN-major operand whose columns are whole blocks of 64
+    int bn;        // columns of n per tile, at most BN
     int split;     // blocks that share a tile's k (a cluster of 2, 4 or 8), or 1
     const __nv_bfloat16 *bias, *residual;
     const float2 *x_scales, *w_scales;
@@ -301,6 +303,7 @@ struct LinearEpilogue {
             unsigned char *o = out + (odd ? pitch : 0) + (q * 16 + lane / 2) * 2;
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
+                if (i % 8 == 0 && i >= rows) break;  // few rows: nothing is done for the others
                 const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? u[i] : u[i + 1], 1);
                 const float gate = odd ? got : u[i], up = odd ? u[i + 1] : got;
                 float y = gate * logistic(gate) * up;
@@ -309,17 +312,22 @@ struct LinearEpilogue {
             }
         } else {
             unsigned char *o = out + (q * 32 + lane) * 2;
-            if (p.act == MOE_ACT_SILU) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = act_value(u[i], MOE_ACT_SILU);
-            } else if (p.act == MOE_ACT_GELU) {
+            for (int j = 0; j < 32; j += 8) {
+                if (j >= rows) break;  // few rows: nothing is done for the others
+                if (p.act == MOE_ACT_SILU) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = act_value(u[i], MOE_ACT_GELU);
-            }
+                    for (int i = j; i < j + 8; ++i) u[i] = act_value(u[i], MOE_ACT_SILU);
+                } else if (p.act == MOE_ACT_GELU) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                if (p.residual) u[i] += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(o + i * kPitch));
-                st_shared_bf16(o + i * kPitch, u[i]);
+                    for (int i = j; i < j + 8; ++i) u[i] = act_value(u[i], MOE_ACT_GELU);
+                }
+#pragma unroll
+                for (int i = j; i < j + 8; ++i) {
+                    if (p.residual)
+                        u[i] += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(o + i * kPitch));
+                    st_shared_bf16(o + i * kPitch, u[i]);
+                }
             }
         }
         group_sync(g);
@@ -449,6 +457,7 @@ struct SavedEpilogue {
         unsigned char *o = out + (q * 32 + lane) * 2;
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
+            if (i % 8 == 0 && i >= rows) break;
             const float2 x = e4m3_decode2(c[i * kPitchCode] | ((unsigned)c[(i + 1) * kPitchCode] << 8));
             const float u[2] = {x.x * scale[i * 8 + q], x.y * scale[i * 8 + 8 + q]};
             const float d[2] = {__uint_as_float(v[i]), __uint_as_float(v[i + 1])};
@@ -513,10 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
 {
     constexpr int kStages = stages(CG, BN, MODE, SPLIT);
     constexpr int kStage = stage_bytes(CG, BN);
-    constexpr int kHalfN = BN / CG;  // rows of B per block
     constexpr int kBM = kTileM * CG;
     constexpr bool kMnA = MODE != kLinear, kMnB = MODE == kWgrad;
-    constexpr int kStepN = CG == 2 ? 32 : 16;
+    constexpr int kStepN = MODE == kWgrad ? 64 * CG : CG == 2 ? 32 : 16;
     constexpr int kElems = FP8 ? 128 : 64;  // values of k per stage
 
     extern __shared__ unsigned char smem_raw[];
@@ -566,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     const int tm = (p.M + kBM - 1) / kBM;
     {
         const auto tiles_of = [&](int rows) {
-            return tm * (((MODE == kWgrad ? p.N : rows) + BN - 1) / BN + (MODE == kWgrad && p.db ? 1 : 0));
+            return tm * (((MODE == kWgrad ? p.N : rows) + p.bn - 1) / p.bn + (MODE == kWgrad && p.db ? 1 : 0));
         };
         const auto scan = [&](int v) {  // inclusive, over a warp
 #pragma unroll
@@ -608,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     tc_fence_after();
     const uint32_t tmem = c->tmem;
 
+    const int chunks_b = MODE == kWgrad ? p.bn / CG / 64 : 0;  // 64 columns each
     const int sharers = CG == 2 ? 2 : split;  // blocks of a cluster
     Walk walk(c, p.E, tm, blockIdx.x / sharers, gridDim.x / sharers);
     Tile t;
@@ -624,81 +633,97 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     };
     // wgrad: the tile after the last of n is the bias gradient's, the product
     // of dy^T with ones: no rows of x to load, 16 columns (32 for a pair)
-    const int tn_bias = MODE == kWgrad ? (p.N + BN - 1) / BN : -1;
+    const int tn_bias = MODE == kWgrad ? (p.N + p.bn - 1) / p.bn : -1;
     const auto is_bias = [&](const Tile &q) { return MODE == kWgrad && q.n == tn_bias; };
     // columns of the accumulator in use: what is left of the ragged axis
     const auto width = [&](const Tile &q) {
-        if (is_bias(q)) return kStepN;
-        const int left = (MODE == kWgrad ? p.N : q.rows) - q.n * BN;
-        return min(BN, (left + kStepN - 1) / kStepN * kStepN);
+        if (is_bias(q)) return 16 * CG;
+        const int left = (MODE == kWgrad ? p.N : q.rows) - q.n * p.bn;
+        return min(p.bn, (left + kStepN - 1) / kStepN * kStepN);
     };
 
     if (warp == 0) {
         // ---- loads -------------------------------------------------------
-        // One thread, as for the matrix instructions: what it does for a
-        // stage (about 400 cycles with warp-wide waits) bounds narrow tiles.
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 1;
-            bool ok = true;
-            while (ok && walk.next(t)) {
-                const Span part = span(t);
-                const int m0 = t.m * kBM + (int)rank * kTileM;
-                const int row = t.row0 + t.n * BN + (int)rank * (width(t) / CG);
-                const int a0 = MODE == kLinear && p.glu ? m0 / 2 : m0;
-                const bool no_b = is_bias(t);
-                const uint32_t bytes = no_b ? kStageA : kStage;
-                for (int i = part.first; i < part.first + part.count; ++i) {
-                    ok = poll(&c->empty[s], ph, c, p.ws);
-                    if (!ok) break;
-                    unsigned char *sa = smem + s * kStage, *sb = sa + kStageA;
-                    const int k0 = i * kElems;
-                    uint32_t bar = smem_addr(&c->full[s]);
-                    if constexpr (MODE == kWgrad) {
-                        if (t.rows - k0 < 64) {  // a tail: see warp 3
-                            bar = smem_addr(&c->tail[s]);
-                            mbar_arrive_expect_tx(&c->tail[s], bytes);
-                        } else if (CG == 1 || self == 0) {
-                            mbar_arrive_expect_tx(&c->full[s], bytes);
-                        } else {
-                            bar = cluster_addr(&c->full[s], 0);
-                            mbar_arrive_expect_tx_remote(bar, bytes);
-                        }
-                        for (int j = 0; j < 2; ++j)
-                            tma_load_2d<CG>(sa + j * 8192, &p.ma, m0 + 64 * j, t.row0 + k0, bar);
-                        if (!no_b)
-                            for (int j = 0; j < kHalfN / 64; ++j)
-                                tma_load_2d<CG>(sb + j * 8192, &p.mb,
-                                                t.n * BN + (int)rank * (width(t) / CG) + 64 * j, t.row0 + k0, bar);
-                    } else {
-                        // the pair's first block expects the bytes of both
-                        if (CG == 1 || self == 0) mbar_arrive_expect_tx(&c->full[s], CG * kStage);
-                        else bar = cluster_addr(&c->full[s], 0);
-                        if constexpr (MODE == kLinear) {
-                            tma_load_4d<CG>(sa, &p.ma, k0, 0, a0, t.e, bar);
-                        } else {
-                            for (int j = 0; j < 2; ++j)
-                                tma_load_4d<CG>(sa + j * 8192, &p.ma, a0 + 64 * j, k0, t.e, 0, bar);
-                        }
-                        tma_load_2d<CG>(sb, &p.mb, k0, row, bar);
-                    }
-                    if (++s == kStages) {
-                        s = 0;
-                        ph ^= 1;
-                    }
-                }
-            }
-            // every stage read: no copy and no arrival is on its way to this
-            // block's shared memory when it ends
-            for (int i = 0; ok && i < kStages; ++i) {
-                ok = poll(&c->empty[s], ph, c, p.ws);
+        // As below: the warp walks together and one thread issues.  What it
+        // does for a stage bounds narrow tiles, so an operand whose columns
+        // are whole blocks of 64 comes with one instruction.
+        const bool one = elect_one();
+        const uint32_t load_bytes = kStageA + (MODE == kWgrad ? chunks_b * 8192 : p.bn / CG * 128);
+        int s = 0;
+        uint32_t ph = 1;
+        bool ok = true, ready = false;
+        while (ok && walk.next(t)) {
+            const Span part = span(t);
+            const int m0 = t.m * kBM + (int)rank * kTileM;
+            const int n0 = t.n * p.bn + (int)rank * (width(t) / CG);
+            const bool no_b = is_bias(t);
+            const uint32_t bytes = no_b ? kStageA : load_bytes;
+            for (int i = part.first; i < part.first + part.count; ++i) {
+                ok = ready || wait(&c->empty[s], ph, c, p.ws);
+                if (!ok) break;
+                const int now = s;
                 if (++s == kStages) {
                     s = 0;
                     ph ^= 1;
                 }
+                const bool next = mbar_test_wait(&c->empty[s], ph);
+                if (one) {
+                    unsigned char *sa = smem + now * kStage, *sb = sa + kStageA;
+                    const int k0 = i * kElems;
+                    uint32_t bar = smem_addr(&c->full[now]);
+                    if constexpr (MODE == kWgrad) {
+                        if (t.rows - k0 < 64) {  // a tail: see warp 3
+                            bar = smem_addr(&c->tail[now]);
+                            mbar_arrive_expect_tx(&c->tail[now], bytes);
+                        } else if (CG == 1 || self == 0) {
+                            mbar_arrive_expect_tx(&c->full[now], bytes);
+                        } else {
+                            bar = cluster_addr(&c->full[now], 0);
+                            mbar_arrive_expect_tx_remote(bar, bytes);
+                        }
+                        const int row = t.row0 + k0;
+                        if (p.whole_a) {
+                            tma_load_4d<CG>(sa, &p.ma, 0, row, m0 / 64, 0, bar);
+                        } else {
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_4d<CG>(sa + j * 8192, &p.ma, m0 + 64 * j, row, 0, 0, bar);
+                        }
+                        if (!no_b) {
+                            if (p.whole_b) {
+                                tma_load_4d<CG>(sb, &p.mb, 0, row, n0 / 64, 0, bar);
+                            } else {
+                                for (int j = 0; j < chunks_b; ++j)
+                                    tma_load_4d<CG>(sb + j * 8192, &p.mb, n0 + 64 * j, row, 0, 0, bar);
+                            }
+                        }
+                    } else {
+                        // the pair's first block expects the bytes of both
+                        if (CG == 1 || self == 0) mbar_arrive_expect_tx(&c->full[now], CG * load_bytes);
+                        else bar = cluster_addr(&c->full[now], 0);
+                        if constexpr (MODE == kLinear) {
+                            tma_load_4d<CG>(sa, &p.ma, k0, 0, p.glu ? m0 / 2 : m0, t.e, bar);
+                        } else if (p.whole_a) {
+                            tma_load_4d<CG>(sa, &p.ma, 0, k0, m0 / 64, t.e, bar);
+                        } else {
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_4d<CG>(sa + j * 8192, &p.ma, m0 + 64 * j, k0, 0, t.e, bar);
+                        }
+                        tma_load_2d<CG>(sb, &p.mb, k0, t.row0 + n0, bar);
+                    }
+                }
+                __syncwarp();
+                ready = __all_sync(0xFFFFFFFFu, next);
             }
         }
-        __syncwarp();
+        // every stage read: no copy and no arrival is on its way to this
+        // block's shared memory when it ends
+        for (int i = 0; ok && i < kStages; ++i) {
+            ok = wait(&c->empty[s], ph, c, p.ws);
+            if (++s == kStages) {
+                s = 0;
+                ph ^= 1;
+            }
+        }
     } else if (MODE == kWgrad && warp == 3) {
         // ---- tails ---------------------------------------------------------
         // The last rows of an expert rarely fill 64 of k; the rows after them
@@ -719,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             phases ^= 1u << at;
             // row k of a tile is the 128 bytes at 128 * k of each 8 KB
             unsigned char *sa = smem + at * kStage;
-            for (int j = 0; j < (is_bias(t) ? 2 : 2 + kHalfN / 64); ++j)
+            for (int j = 0; j < (is_bias(t) ? 2 : 2 + chunks_b); ++j)
                 for (int o = keep * 128 + lane * 16; o < 8192; o += 512)
                     *reinterpret_cast<uint4 *>(sa + j * 8192 + o) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
@@ -824,8 +849,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         };
         while (walk.next(t)) {
             const int iters = span(t).count;
-            const int m0 = t.m * kBM + (int)rank * kTileM, n0 = t.n * BN;
-            const int cols = is_bias(t) ? 1 : min(BN, (MODE == kWgrad ? p.N : t.rows) - n0);
+            const int m0 = t.m * kBM + (int)rank * kTileM, n0 = t.n * p.bn;
+            const int cols = is_bias(t) ? 1 : min(p.bn, (MODE == kWgrad ? p.N : t.rows) - n0);
             const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + acc * BN;
             const auto release = [&] {  // this warp's last look at the accumulator
                 tc_fence_before();
@@ -970,6 +995,25 @@ cudaError_t encode_rows(CUtensorMap *m, bool fp8, const void *base, int cols, in
     return encode(m, fp8, base, 2, d, st, b);
 }
 
+// An MN-major operand: `cols` columns (the m or n of the product) of `rows`
+// rows (its k), E of them.  A stage takes 64 rows and `blocks` blocks of 64
+// columns, each block to 8 KB of its own: with one load where the columns
+// are whole blocks, else one load for each.
+cudaError_t encode_mn(CUtensorMap *m, const void *base, int cols, int rows, int E, int blocks, int *whole)
+{
+    const uint64_t per = E > 1 ? (uint64_t)cols * rows : cols;  // unused for one
+    *whole = cols % 64 == 0;
+    if (*whole) {
+        const uint64_t d[4] = {64, (uint64_t)rows, (uint64_t)cols / 64, (uint64_t)E};
+        const uint64_t st[3] = {(uint64_t)cols, 64, per};
+        const uint32_t b[4] = {64, 64, (uint32_t)blocks, 1};
+        return encode(m, false, base, 4, d, st, b);
+    }
+    const uint64_t d[4] = {(uint64_t)cols, (uint64_t)rows, 1, (uint64_t)E}, st[3] = {(uint64_t)cols, per, per};
+    const uint32_t b[4] = {64, 64, 1, 1};
+    return encode(m, false, base, 4, d, st, b);
+}
+
 template <int CG, int BN, int MODE, bool FP8, bool SPLIT>
 cudaError_t launch(const Params &p, cudaStream_t s)
 {
@@ -980,8 +1024,8 @@ cudaError_t launch(const Params &p, cudaStream_t s)
     if (err != cudaSuccess) return err;
     // the most tiles that offsets over these rows can give
     const long long tm = (p.M + kTileM * CG - 1) / (kTileM * CG);
-    const long long tn = MODE == kWgrad ? (long long)p.E * ((p.N + BN - 1) / BN + 1)
-                                        : p.rows / BN + (p.rows < p.E ? p.rows : p.E);
+    const long long tn = MODE == kWgrad ? (long long)p.E * ((p.N + p.bn - 1) / p.bn + 1)
+                                            : p.rows / p.bn + (p.rows < p.E ? p.rows : p.E);
     const int cluster = SPLIT ? p.split : CG;
 
     cudaLaunchConfig_t cfg = {};
@@ -1017,43 +1061,51 @@ cudaError_t launch(const Params &p, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
-// How a product is cut: columns of n per tile (256: a pair of SMs and 256 of
-// m; else one SM and 128), and blocks that share a tile's k.
+// How a product is cut: SMs of a tile (2: a pair, 256 of m; 1: 128), columns
+// of n per tile, and blocks that share a tile's k.
 struct Cut {
-    int bn, split;
+    int cg, bn, split;
 };
 
 // The cut with the least time for tiles in whole waves over the SMs.  The
-// constants are cycles, measured: a stage of 64 (e4m3: 128) of k takes about
-// 550 for 256 and 128 columns (32 KB a block; the pair does four times the
-// work in it) and 350 for 32 (20 KB); after the last stage the accumulator
-// takes about 1000 per 32 columns and group, and a joint sum about 2500.
+// constants are cycles, measured: a stage of 64 (e4m3: 128) of k is bound by
+// its bytes, 16 KB of A and 128 per row of B in a block at about 61 a cycle,
+// or, for a pair with 256 columns, by the matrix instructions (545); after
+// the last stage the accumulator takes about 1000 per 32 columns and group,
+// and a joint sum about 2500.  Narrower tiles pay where they fill the last
+// wave: 5000 rows, 4096 -> 2048 (160 tiles of 256, 2.1 waves of 76 pairs)
+// take 63.6 us 256 wide and LATER 192 wide.
 // `live` experts have `n` of the ragged axis together (`each`: wgrad, whose n
 // is the same for every expert); their sizes are not known on the host, half
 // a tile each is taken for lost.
 Cut pick(int m, long long n, int live, bool each, long long k_stages, bool narrow)
 {
-    Cut best = {256, 1};
+    static const Cut cuts[] = {{2, 256, 1}, {2, 224, 1}, {2, 192, 1}, {2, 160, 1}, {2, 128, 1}, {1, 128, 8},
+                               {1, 96, 1},  {1, 64, 1},  {1, 32, 8}};
+    Cut best = cuts[0];
     double least = 0.0;
     const int sms = device_sm_count();
-    for (int bn = 256; bn >= (narrow ? 32 : 128); bn = bn == 256 ? 128 : 32) {
-        const int cg = bn == 256 ? 2 : 1;
-        const long long tm = (m + 128 * cg - 1) / (128 * cg);
-        long long tn = live == 1 || each ? (n + bn - 1) / bn * (each ? live : 1) : n / bn + (live + 1) / 2;
+    for (const Cut &c : cuts) {
+        if (!narrow && c.bn != 256 && c.bn != 128) continue;  // wgrad loads B by 64 columns
+        const long long tm = (m + 128 * c.cg - 1) / (128 * c.cg);
+        long long tn = live == 1 || each ? (n + c.bn - 1) / c.bn * (each ? live : 1) : n / c.bn + (live + 1) / 2;
         if (tn < live) tn = live;
-        for (int split = 1; split <= (cg == 2 ? 1 : 8); split *= 2) {
+        const double bytes = 270.0 + 2.1 * c.bn / c.cg, mma = 2.13 * c.bn;
+        const double stage = c.cg == 2 && mma > bytes ? mma : bytes;
+        for (int split = 1; split <= c.split; split *= 2) {
             if (split > 1 && k_stages < 4 * split) break;
             // clusters of 4 and 8 leave some SMs of a GPC over
-            const long long slots = split < 4 ? sms / (cg * split) : sms * 7 / 8 / split;
-            const long long waves = (tm * tn + slots - 1) / slots;
-            const double cycles = (double)waves * k_stages / split * (bn == 32 ? 350 : 550) +
-                                  1000.0 * ((bn / split + 63) / 64) + (split > 1 ? 2500.0 * waves : 0.0);
+            const long long slots = split < 4 ? sms / (c.cg * split) : sms * 7 / 8 / split;
+            // unknown sizes: 15 % more tiles, or a full last wave turns into two
+            const long long tiles = live == 1 || each ? tm * tn : tm * tn * 23 / 20;
+            const long long waves = (tiles + slots - 1) / slots;
+            const double cycles = (double)waves * k_stages / split * stage + 1000.0 * ((c.bn / split + 63) / 64) +
+                                  (split > 1 ? 2500.0 * waves : 0.0);
             if (least == 0.0 || cycles < least) {
                 least = cycles;
-                best = {bn, split};
+                best = {c.cg, c.bn, split};
             }
         }
-        if (bn == 32) break;
     }
     return best;
 }
@@ -1061,8 +1113,9 @@ Cut pick(int m, long long n, int live, bool each, long long k_stages, bool narro
 template <int MODE, bool FP8>
 cudaError_t launch_cut(Params &p, const Cut &c, cudaStream_t s)
 {
+    p.bn = c.bn;
     p.split = c.split;
-    if (c.bn == 256) return launch<2, 256, MODE, FP8, false>(p, s);
+    if (c.cg == 2) return launch<2, 256, MODE, FP8, false>(p, s);
     if constexpr (MODE != kWgrad)
         if (c.bn == 32)
             return c.split > 1 ? launch<1, 32, MODE, FP8, true>(p, s) : launch<1, 32, MODE, FP8, false>(p, s);
@@ -1100,7 +1153,7 @@ cudaError_t linear(const moe_rows *G, const void *x, const float *x_scales, int 
     const uint64_t st[3] = {n * K, (uint64_t)K, (uint64_t)N * K};
     const uint32_t b[4] = {(uint32_t)elems, (uint32_t)h, (uint32_t)(kTileM / h), 1};
     cudaError_t err = encode(&p.ma, FP8, w, 4, d, st, b);
-    if (err == cudaSuccess) err = encode_rows(&p.mb, FP8, x, K, G->rows, elems, cut.bn == 256 ? 128 : cut.bn);
+    if (err == cudaSuccess) err = encode_rows(&p.mb, FP8, x, K, G->rows, elems, cut.bn / cut.cg);
     if (err != cudaSuccess) return err;
     return launch_cut<kLinear, FP8>(p, cut, s);
 }
@@ -1122,11 +1175,8 @@ cudaError_t dgrad(const moe_rows *G, const void *dy, int N, const void *w, int K
     p.saved = static_cast<uint8_t *>(const_cast<void *>(saved));
     p.saved_scales = static_cast<uint8_t *>(const_cast<void *>(saved_scales));
     const Cut cut = pick(K, G->rows, G->rows < G->E ? G->rows : G->E, false, (N + 63) / 64, true);
-    const uint64_t d[4] = {(uint64_t)K, (uint64_t)N, (uint64_t)G->E, 1};
-    const uint64_t st[3] = {(uint64_t)K, (uint64_t)N * K, (uint64_t)N * K};
-    const uint32_t b[4] = {64, 64, 1, 1};
-    cudaError_t err = encode(&p.ma, false, w, 4, d, st, b);
-    if (err == cudaSuccess) err = encode_rows(&p.mb, false, dy, N, G->rows, 64, cut.bn == 256 ? 128 : cut.bn);
+    cudaError_t err = encode_mn(&p.ma, w, K, N, G->E, 2, &p.whole_a);
+    if (err == cudaSuccess) err = encode_rows(&p.mb, false, dy, N, G->rows, 64, cut.bn / cut.cg);
     if (err != cudaSuccess) return err;
     return launch_cut<MODE, false>(p, cut, s);
 }

@@ -21,10 +21,10 @@ cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const 
     p.fp32 = fp32;
     p.dw = dw;
     p.db = db;
-    cudaError_t err = encode_rows(&p.ma, false, dy, N, G->rows, 64, 64);
-    if (err == cudaSuccess) err = encode_rows(&p.mb, false, x, K, G->rows, 64, 64);
-    if (err != cudaSuccess) return err;
     const Cut cut = pick(N, K, G->E, true, (G->rows / G->E + 63) / 64, false);
+    cudaError_t err = encode_mn(&p.ma, dy, N, G->rows, 1, 2, &p.whole_a);
+    if (err == cudaSuccess) err = encode_mn(&p.mb, x, K, G->rows, 1, cut.bn / cut.cg / 64, &p.whole_b);
+    if (err != cudaSuccess) return err;
     return launch_cut<kWgrad, false>(p, cut, s);
 }
 
