@@ -89,6 +89,7 @@ struct Params {
     int K;         // linear, dgrad: extent of k, in bytes
     int act, glu;  // glu: A's rows alternate gate and up columns
     int fp32;
+    int sectors;   // bf16 dw: rows of whole 32-byte sectors
     int whole_a, whole_b;  // an MN-major operand whose columns are whole blocks of 64
     int bn;        // columns of n per tile, at most BN
     int split;     // blocks that share a tile's k (a cluster of 2, 4 or 8), or 1
@@ -509,9 +510,20 @@ __device__ __forceinline__ void store_row(const Params &p, size_t at, const uint
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.dw) + at;
+    // whole 32-byte sectors where rows and base allow: half the store instructions
+    if (p.sectors && n == 32) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(o + j * 16), "r"(w[8 * j]),
+                         "r"(w[8 * j + 1]), "r"(w[8 * j + 2]), "r"(w[8 * j + 3]), "r"(w[8 * j + 4]),
+                         "r"(w[8 * j + 5]), "r"(w[8 * j + 6]), "r"(w[8 * j + 7])
+                         : "memory");
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (j * 8 < n) *reinterpret_cast<uint4 *>(o + j * 8) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        if (j * 8 < n)
+            *reinterpret_cast<uint4 *>(o + j * 8) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
 // --------------------------------------------------------------------------

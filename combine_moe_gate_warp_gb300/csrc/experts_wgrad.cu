@@ -20,6 +20,7 @@ cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const 
     p.N = K;
     p.fp32 = fp32;
     p.dw = dw;
+    p.sectors = !fp32 && K % 16 == 0 && reinterpret_cast<uintptr_t>(dw) % 32 == 0;
     p.db = db;
     const Cut cut = pick(N, K, G->E, true, (G->rows / G->E + 63) / 64, false);
     cudaError_t err = encode_mn(&p.ma, dy, N, G->rows, 1, 2, &p.whole_a);
