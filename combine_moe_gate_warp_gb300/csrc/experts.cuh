@@ -80,7 +80,7 @@ __host__ __device__ constexpr int smem_bytes(int CG, int BN, int MODE, bool SPLI
 __host__ __device__ constexpr int tmem_cols(int BN) { return 2 * BN < 32 ? 32 : 2 * BN; }
 
 struct Params {
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, mb32;  // mb32: 32 rows of B at a time, for an expert's last tile
     const int32_t *offsets;
     void *ws;
     int E, rows;
@@ -669,7 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             const int m0 = t.m * kBM + (int)rank * kTileM;
             const int n0 = t.n * p.bn + (int)rank * (width(t) / CG);
             const bool no_b = is_bias(t);
-            const uint32_t bytes = no_b ? kStageA : load_bytes;
+            // a narrow last tile loads the rows it has, by 32
+            const int few = MODE == kWgrad ? 0 : (width(t) / CG + 31) / 32;
+            const bool some = few * 32 < p.bn / CG;
+            const uint32_t bytes = no_b ? kStageA : MODE != kWgrad && some ? kStageA + few * 4096 : load_bytes;
             for (int i = part.first; i < part.first + part.count; ++i) {
                 ok = ready || wait(&c->empty[s], ph, c, p.ws);
                 if (!ok) break;
@@ -710,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                         }
                     } else {
                         // the pair's first block expects the bytes of both
-                        if (CG == 1 || self == 0) mbar_arrive_expect_tx(&c->full[now], CG * load_bytes);
+                        if (CG == 1 || self == 0) mbar_arrive_expect_tx(&c->full[now], CG * bytes);
                         else bar = cluster_addr(&c->full[now], 0);
                         if constexpr (MODE == kLinear) {
                             tma_load_4d<CG>(sa, &p.ma, k0, 0, p.glu ? m0 / 2 : m0, t.e, bar);
@@ -720,7 +723,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                             for (int j = 0; j < 2; ++j)
                                 tma_load_4d<CG>(sa + j * 8192, &p.ma, m0 + 64 * j, k0, 0, t.e, bar);
                         }
-                        tma_load_2d<CG>(sb, &p.mb, k0, t.row0 + n0, bar);
+                        if (!some) {
+                            tma_load_2d<CG>(sb, &p.mb, k0, t.row0 + n0, bar);
+                        } else {
+                            for (int j = 0; j < few; ++j)
+                                tma_load_2d<CG>(sb + j * 4096, &p.mb32, k0, t.row0 + n0 + 32 * j, bar);
+                        }
                     }
                 }
                 __syncwarp();
@@ -1166,6 +1174,7 @@ cudaError_t linear(const moe_rows *G, const void *x, const float *x_scales, int 
     const uint32_t b[4] = {(uint32_t)elems, (uint32_t)h, (uint32_t)(kTileM / h), 1};
     cudaError_t err = encode(&p.ma, FP8, w, 4, d, st, b);
     if (err == cudaSuccess) err = encode_rows(&p.mb, FP8, x, K, G->rows, elems, cut.bn / cut.cg);
+    if (err == cudaSuccess && cut.bn > 32) err = encode_rows(&p.mb32, FP8, x, K, G->rows, elems, 32);
     if (err != cudaSuccess) return err;
     return launch_cut<kLinear, FP8>(p, cut, s);
 }
@@ -1189,6 +1198,7 @@ cudaError_t dgrad(const moe_rows *G, const void *dy, int N, const void *w, int K
     const Cut cut = pick(K, G->rows, G->rows < G->E ? G->rows : G->E, false, (N + 63) / 64, true);
     cudaError_t err = encode_mn(&p.ma, w, K, N, G->E, 2, &p.whole_a);
     if (err == cudaSuccess) err = encode_rows(&p.mb, false, dy, N, G->rows, 64, cut.bn / cut.cg);
+    if (err == cudaSuccess && cut.bn > 32) err = encode_rows(&p.mb32, false, dy, N, G->rows, 64, 32);
     if (err != cudaSuccess) return err;
     return launch_cut<MODE, false>(p, cut, s);
 }

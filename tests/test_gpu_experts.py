@@ -270,6 +270,25 @@ def test_wgrad_split(counts, N, K):
         check_wgrad(dw, db, dy, x, counts, dtype)
 
 
+@pytest.mark.parametrize("mean", [4, 900])
+def test_256_experts(mean):
+    """The largest number of experts, most with a few rows, some with none."""
+    counts = [(e * 37) % 11 if e % 3 else 0 for e in range(256)]
+    counts[200] = 400
+    R, K, N = sum(counts), 136, 64
+    rows = rows_for(counts, mean)
+    x, w, dy = normal(R, K, seed=71), normal(256, N, K, seed=72, std=K ** -0.5), normal(R, N, seed=73)
+    r = ExpertRows(offsets_of(counts), rows=rows)
+    y, dx = r.linear(padded(x, rows), w), r.dgrad(padded(dy, rows), w)
+    dw, db = r.wgrad(padded(dy, rows), padded(x, rows), bias=True)
+    assert r.status() == 0
+    u, e = linear64(x, w, counts)
+    assert_near(y[:R], u, e + BF16 * (u.abs() + e), "y")
+    d, e = linear64(dy, w.mT, counts)
+    assert_near(dx[:R], d, e + BF16 * (d.abs() + e), "dx")
+    check_wgrad(dw, db, dy, x, counts, torch.bfloat16)
+
+
 @pytest.mark.parametrize("mean", [8, 9000])
 def test_same_bits_twice(mean):
     """No result depends on timing."""
