@@ -748,8 +748,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         // ---- tails ---------------------------------------------------------
         // The last rows of an expert rarely fill 64 of k; the rows after them
         // are another expert's, or nobody's with any bits in them.  That
-        // stage lands on a barrier of its own, its rows past the end are
-        // zeroed in both tiles, and then it counts as full.
+        // stage lands on a barrier of its own, its rows past the end, up to
+        // the next 16 that a matrix instruction takes, are zeroed in both
+        // tiles, and then it counts as full.
         int s = 0;
         uint32_t phases = 0;  // of each stage's barrier
         bool ok = true;
@@ -764,12 +765,16 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             phases ^= 1u << at;
             // row k of a tile is the 128 bytes at 128 * k of each 8 KB
             unsigned char *sa = smem + at * kStage;
+            const int end = (keep + 15) / 16 * 16 * 128;
             for (int j = 0; j < (is_bias(t) ? 2 : 2 + chunks_b); ++j)
-                for (int o = keep * 128 + lane * 16; o < 8192; o += 512)
+                for (int o = keep * 128 + lane * 16; o < end; o += 512)
                     *reinterpret_cast<uint4 *>(sa + j * 8192 + o) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_release_cluster(cluster_addr(&c->full[at], lead));
+            if (lane == 0) {
+                if (self == lead) mbar_arrive(&c->full[at]);
+                else mbar_arrive_release_cluster(cluster_addr(&c->full[at], lead));
+            }
         }
     } else if (warp == 1 && rank == 0) {
         // ---- matrix instructions ------------------------------------------
@@ -797,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 const uint32_t idesc = mma_idesc(FP8, kMnA, kMnB, kBM, width(t));
                 const uint32_t d = tmem + acc * BN;
                 const bool bias = is_bias(t);
-                const bool tail = MODE == kWgrad && CG == 2 && (t.rows & 63);
+                const int last_steps = MODE == kWgrad && span(t).last ? ((t.rows & 63) + 15) / 16 : 0;
                 ok = wait(&c->acc_empty[acc], aph ^ 1, c, p.ws);
                 if (!ok) break;
                 tc_fence_after();
@@ -805,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     ok = ready || wait(&c->full[s], ph, c, p.ws);
                     if (!ok) break;
                     // the zeroed rows of a tail come from the peer's generic writes too
-                    if (tail && i == iters - 1) mbar_try_wait_acquire_cluster(&c->full[s], ph);
+                    if (CG == 2 && last_steps != 0 && i == iters - 1) mbar_try_wait_acquire_cluster(&c->full[s], ph);
                     tc_fence_after();
                     const int now = s;
                     if (++s == kStages) {
@@ -814,10 +819,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     }
                     const bool next = mbar_test_wait(&c->full[s], ph);
                     const uint64_t da = da0 + (uint64_t)(now * (kStage >> 4)), db = db0 + (uint64_t)(now * (kStage >> 4));
+                    // a tail's steps of 16 rows past its end are left out
+                    const int steps = MODE == kWgrad && last_steps != 0 && i == iters - 1 ? last_steps : 4;
                     if (one) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_ss<CG, FP8>(d, da + k * kStepA, bias ? ones : db + k * kStepB, idesc, (i | k) != 0);
+                            if (MODE != kWgrad || k < steps) mma_ss<CG, FP8>(d, da + k * kStepA, bias ? ones : db + k * kStepB, idesc, (i | k) != 0);
                         mma_commit<CG>(&c->empty[now]);
                     }
                     __syncwarp();
