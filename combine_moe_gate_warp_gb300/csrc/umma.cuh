@@ -55,26 +55,10 @@ __device__ __forceinline__ void cluster_sync_all()
 }
 
 // Arrivals on a barrier anywhere in the cluster (a shared::cluster address).
-// Releasing (and acquiring) at cluster scope is a fence; once per stage of a
-// ring it doubled the time of a product (645 us against 348 us for 57000 rows,
-// 2048 x 2048), so it is left to where memory that this thread wrote is handed
-// to the other CTA.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_acquire_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
+// None of them is a fence at cluster scope: once per stage of a ring such a
+// fence doubled the time of a product (645 us against 348 us for 57000 rows,
+// 2048 x 2048).  Where a thread's memory is handed to another CTA, fence_cluster
+// comes before.
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v)
 {
