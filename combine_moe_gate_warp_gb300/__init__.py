@@ -13,7 +13,7 @@ from .abi import (MOE_ACT_GELU, MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_SWIGLU, MOE_
                   alloc_workspace, moe_combine, moe_combine_backward, moe_combine_fp8, moe_dispatch,
                   moe_dispatch_backward, moe_dispatch_layout, moe_gate, moe_gate_backward, moe_get_status,
                   moe_quantize_rows, moe_route, moe_rows_max, moe_workspace_init, moe_workspace_size)
-from .experts import ExpertFFN, ExpertRows, FFNGrads, SavedLayer
+from .experts import ExpertFFN, ExpertRows, FFNGrads, SavedLayer, quantize_weights
 from .pipeline import RouteGraph, RoutePipeline, RoutePlan, RouteShape
 
 
@@ -23,7 +23,7 @@ def build(force: bool = False) -> str:
 
 
 __all__ = [
-    "build", "ExpertRows", "ExpertFFN", "FFNGrads", "SavedLayer", "MOE_ACT_NONE", "MOE_ACT_SILU", "MOE_ACT_GELU",
+    "build", "ExpertRows", "ExpertFFN", "FFNGrads", "SavedLayer", "quantize_weights", "MOE_ACT_NONE", "MOE_ACT_SILU", "MOE_ACT_GELU",
     "MOE_ACT_SWIGLU", "RoutePlan", "RoutePipeline", "RouteGraph", "RouteShape", "Layout", "MoeError", "alloc_workspace",
     "moe_gate", "moe_dispatch_layout", "moe_dispatch", "moe_combine", "moe_get_status", "moe_route",
     "moe_quantize_rows", "moe_combine_fp8", "moe_combine_backward", "moe_dispatch_backward",

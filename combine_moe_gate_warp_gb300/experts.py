@@ -69,9 +69,42 @@ def _check(t, dtype, shape, name, device):
     _refuse(t, dtype, shape, name, device)
 
 
+def _check_rows(t, dtype, rows, cols, name, device):
+    """A contiguous [at least `rows`, cols] tensor of this type and device; its address."""
+    try:
+        shape = t.shape
+        if (t.dtype is dtype and len(shape) == 2 and shape[0] >= rows and shape[1] == cols and t.device == device
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if isinstance(t, torch.Tensor) and (t.dim() != 2 or t.shape[1] != cols or t.shape[0] < rows):
+        raise ValueError(f"{name}: expected shape ({rows}, {cols}) or more rows, got {tuple(t.shape)}")
+    _refuse(t, dtype, getattr(t, "shape", None), name, device)
+
+
+def quantize_weights(w: torch.Tensor):
+    """Weights [E, N, K] (or [N, K]) in e4m3 for products with e4m3 rows, once
+    when a model is loaded: codes (uint8) and (scale, sum) [.., N, 2] fp32 with
+    scale = max |w| / 448 of each output column (1 for a column of zeros) and
+    sum the sum over k of scale * code."""
+    codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+    scales = torch.empty((*w.shape[:-1], 2), dtype=torch.float32, device=w.device)
+    for c, s, v in zip(codes.view(-1, *w.shape[-2:]), scales.view(-1, w.shape[-2], 2), w.view(-1, *w.shape[-2:])):
+        v = v.float()
+        top = v.abs().amax(1)
+        scale = torch.where(top > 0, top / 448.0, 1.0)
+        q = (v / scale[:, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+        c.copy_(q.view(torch.uint8))
+        s[:, 0] = scale
+        s[:, 1] = (q.double().sum(1) * scale.double()).float()
+    return codes, scales
+
+
 class ExpertRows:
     """The packed rows of a layout: expert e has rows offsets[e] ..
-    offsets[e+1]-1 of buffers that hold ``rows`` rows.
+    offsets[e+1]-1 of buffers that hold ``rows`` rows (or more: those past
+    ``rows`` are left alone).
 
     ``offsets`` is the layout's device tensor (int32 [E+1]); None makes all
     rows one group, for the shared experts' plain products (weights then
@@ -143,9 +176,15 @@ class ExpertRows:
             return t, t.data_ptr()
         return t, _check(t, dtype, shape, name, self.device)
 
+    def _out_rows(self, t, cols, name):
+        if t is None:
+            t = torch.empty((self.rows, cols), dtype=torch.bfloat16, device=self.device)
+            return t, t.data_ptr()
+        return t, _check_rows(t, torch.bfloat16, self.rows, cols, name, self.device)
+
     def _saved(self, saved, N):
-        return (_check(saved.codes, torch.uint8, (self.rows, N), "saved.codes", self.device),
-                _check(saved.scales, torch.uint8, (self.rows, N // SAVED_BLOCK), "saved.scales", self.device))
+        return (_check_rows(saved.codes, torch.uint8, self.rows, N, "saved.codes", self.device),
+                _check_rows(saved.scales, torch.uint8, self.rows, N // SAVED_BLOCK, "saved.scales", self.device))
 
     # ------------------------------------------------------------------
     def linear(self, x, w, *, bias=None, act: str = "none", residual=None, saved: SavedLayer | None = None,
@@ -164,22 +203,22 @@ class ExpertRows:
                 raise ValueError("x_scales and w_scales go together")
             dtype = torch.uint8
         N, K, wp = self._weights(w, dtype)
-        xp = _check(x, dtype, (rows, K), "x", dev)
+        xp = _check_rows(x, dtype, rows, K, "x", dev)
         if x_scales is not None:
-            xs = _check(x_scales, torch.float32, (rows, 2), "x_scales", dev)
+            xs = _check_rows(x_scales, torch.float32, rows, 2, "x_scales", dev)
             ws = _check(w_scales, torch.float32, self._per_expert(N, 2), "w_scales", dev)
         if bias is not None:
             bp = _check(bias, torch.bfloat16, self._per_expert(N), "bias", dev)
         cols = N // 2 if a == abi.MOE_ACT_SWIGLU else N
         if residual is not None:
-            rp = _check(residual, torch.bfloat16, (rows, cols), "residual", dev)
+            rp = _check_rows(residual, torch.bfloat16, rows, cols, "residual", dev)
         if saved is not None:
             sc, ss = self._saved(saved, N)
         if out is None:
             out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
             op = out.data_ptr()
         else:
-            op = _check(out, torch.bfloat16, (rows, cols), "out", dev)
+            op = _check_rows(out, torch.bfloat16, rows, cols, "out", dev)
         st = self._lib.moe_expert_linear(self._ref, xp, xs, K, wp, ws, N, bp, a, rp, op, sc, ss, self._stream())
         if st:
             abi._check(st, "moe_expert_linear")
@@ -197,13 +236,13 @@ class ExpertRows:
         if a is not None and saved is None:
             raise ValueError("a: only with a saved layer")
         cols = 2 * K if code == abi.MOE_ACT_SWIGLU else K
-        dp = _check(dy, torch.bfloat16, (self.rows, N), "dy", self.device)
+        dp = _check_rows(dy, torch.bfloat16, self.rows, N, "dy", self.device)
         sc = ss = ap = None
         if saved is not None:
             sc, ss = self._saved(saved, cols)
             if a is not None:
-                ap = _check(a, torch.bfloat16, (self.rows, K), "a", self.device)
-        out, op = self._out(out, torch.bfloat16, (self.rows, cols), "out")
+                ap = _check_rows(a, torch.bfloat16, self.rows, K, "a", self.device)
+        out, op = self._out_rows(out, cols, "out")
         st = self._lib.moe_expert_dgrad(self._ref, dp, N, wp, K, code, sc, ss, op, ap, self._stream())
         if st:
             abi._check(st, "moe_expert_dgrad")
@@ -218,8 +257,8 @@ class ExpertRows:
         if dy.dim() != 2 or x.dim() != 2:
             raise ValueError("dy and x: expected [rows, columns]")
         N, K = dy.shape[1], x.shape[1]
-        dp = _check(dy, torch.bfloat16, (self.rows, N), "dy", self.device)
-        xp = _check(x, torch.bfloat16, (self.rows, K), "x", self.device)
+        dp = _check_rows(dy, torch.bfloat16, self.rows, N, "dy", self.device)
+        xp = _check_rows(x, torch.bfloat16, self.rows, K, "x", self.device)
         out, op = self._out(out, dtype, self._per_expert(N, K), "out")
         bp = None
         if bias or out_bias is not None:
@@ -236,10 +275,10 @@ class ExpertRows:
             raise ValueError("act: 'none' has no backward pass")
         N = saved.codes.shape[-1]
         cols = N // 2 if code == abi.MOE_ACT_SWIGLU else N
-        dp = _check(dy, torch.bfloat16, (self.rows, cols), "dy", self.device)
+        dp = _check_rows(dy, torch.bfloat16, self.rows, cols, "dy", self.device)
         sc, ss = self._saved(saved, N)
-        ap = self._opt(a, torch.bfloat16, (self.rows, cols), "a")
-        out, op = self._out(out, torch.bfloat16, (self.rows, N), "out")
+        ap = None if a is None else _check_rows(a, torch.bfloat16, self.rows, cols, "a", self.device)
+        out, op = self._out_rows(out, N, "out")
         abi._check(self._lib.moe_act_backward(self._ref, dp, N, code, sc, ss, op, ap, self._stream()),
                    "moe_act_backward")
         return out

@@ -134,3 +134,20 @@ def test_binding_refusals(abi):
                        (lambda: ExpertRows(off, rows=8, device="cpu", ws=torch.zeros(100)), "workspace")):
         with pytest.raises(ValueError, match=what):
             call()
+
+
+def test_quantize_weights():
+    """e4m3 weights: the largest of a column is 448 * scale, every value is
+    within half a step (2^-4 of it, or 2^-10 of the scale), zeros stay zeros."""
+    from combine_moe_gate_warp_gb300 import quantize_weights
+    w = torch.randn(3, 24, 32, generator=torch.Generator().manual_seed(1)).bfloat16()
+    w[1, 5] = 0
+    codes, scales = quantize_weights(w)
+    assert codes.shape == w.shape and scales.shape == (3, 24, 2)
+    v = codes.view(torch.float8_e4m3fn).double() * scales[..., :1].double()
+    assert bool(((v - w.double()).abs() <= 2.0 ** -4 * w.double().abs() * (1 + 2.0 ** -20)
+                 + 2.0 ** -10 * scales[..., :1].double()).all())
+    assert bool((v[1, 5] == 0).all()) and scales[1, 5, 0] == 1 and scales[1, 5, 1] == 0
+    assert torch.allclose(scales[..., 1].double(), v.sum(2), rtol=2.0 ** -23, atol=0)
+    one, two = quantize_weights(w[0])
+    assert torch.equal(one, codes[0]) and torch.equal(two, scales[0])

@@ -5,7 +5,8 @@ gradients, rows outside the groups, and the FFN they make."""
 import pytest
 import torch
 
-from combine_moe_gate_warp_gb300 import ExpertFFN, ExpertRows, RoutePlan, RouteShape, SavedLayer, abi
+from combine_moe_gate_warp_gb300 import (ExpertFFN, ExpertRows, RoutePlan, RouteShape, SavedLayer, abi,
+                                         quantize_weights)
 from expert_util import (BF16, act64, act_error, assert_near, decode64, encode_saved, grad64, grad_error, linear64,
                          normal, offsets_of, spans, sum_error)
 
@@ -487,3 +488,28 @@ def test_ffn_between_dispatch_and_combine():
             # roundings to bf16: a, y
             size[at] += gates[at, j: j + 1] * (1.1 * a.abs() @ w2[e].double().abs().T + y.abs())
     assert_near(plan.y, want, BF16 * (1.05 * size + want.abs()), "y")
+
+
+@pytest.mark.parametrize("T", [0, 1, 77])
+def test_fp8_dispatch_into_the_experts(T):
+    """The FP8 dispatch's rows and scales go straight into a product: against
+    the same codes and scales in 64 bits; a batch without tokens is fine."""
+    H, E, k, N = 160, 8, 2, 96
+    plan = RoutePlan(RouteShape(T=T, H=H, E=E, k=k, P=4, fp8=abi.MOE_FP8_PER_TOKEN), "cuda")
+    plan.route(torch.randn(T, E, generator=torch.Generator().manual_seed(81)).cuda())
+    plan.dispatch(normal(T, H, seed=82))
+    codes, scales = quantize_weights(normal(E, N, H, seed=83, std=H ** -0.5))
+    y = ExpertRows.of(plan).linear(plan.packed, codes, x_scales=plan.scales, w_scales=scales)
+    assert plan.status() == 0 and y.shape == (T * k, N)
+    off = plan.layout.offsets.tolist() if T else [0] * (E + 1)
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        q, c = plan.packed[lo:hi].view(torch.float8_e4m3fn).double(), codes[e].view(torch.float8_e4m3fn).double()
+        s, z = plan.scales[lo:hi, :1].double(), plan.scales[lo:hi, 1:].double()
+        acc, mags = q @ c.T, q.abs() @ c.abs().T
+        ws, total = scales[e, :, 0].double(), scales[e, :, 1].double()
+        want = s * ws * acc + z * total
+        err = s * ws * sum_error(H, mags) + 2.0 ** -22 * ((s * ws * acc).abs() + (z * total).abs())
+        assert_near(y[lo:hi], want, err + BF16 * (want.abs() + err), "y")
+        # the sums the weights carry are their own
+        assert_near(total, ws * c.sum(1), 2.0 ** -23 * (ws * c.sum(1)).abs() + 1e-30, "sum")
