@@ -30,7 +30,12 @@ struct WsHeader {
     // is bumped by the block that draws the last tile id of a call
     unsigned long long tile_epoch;
     unsigned quant_ticket;         // grouped FP8 encode: finished blocks
-    unsigned pad0[25];
+    // Failure-injection hook for tests, written only from the host: when it
+    // is not zero, the first block of the next expert product leaves its
+    // first load out, so that its waits run out (MOE_ERR_TIMEOUT).  Cleared
+    // by the call that sees it.
+    unsigned inject_skip_load;
+    unsigned pad0[24];
     unsigned gate_counts[MOE_MAX_EXPERTS];  // gate: per-expert totals
     unsigned part_tok[MOE_MAX_EXPERTS];     // layout: per-partition token totals
     // grouped FP8 quantiser: per group (expert, or group 0 for global) the

@@ -117,6 +117,7 @@ struct Control {
     uint64_t full[12], empty[12], tail[12], acc_full[2], acc_empty[2], joined, taken;
     uint32_t tmem;
     int abort;
+    unsigned skip;  // the injected failure
     int part[12];
     int row0[MOE_MAX_EXPERTS], rows[MOE_MAX_EXPERTS];  // of each expert, checked
     int tile0[MOE_MAX_EXPERTS + 1];                    // its first tile
@@ -583,7 +584,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         lo = p.offsets ? p.offsets[tid] : 0;
         hi = p.offsets ? p.offsets[tid + 1] : p.rows;
     }
+    WsHeader *const header = static_cast<WsHeader *>(p.ws);
     if (tid == 0) {
+        const unsigned skip = blockIdx.x == 0 ? *(volatile unsigned *)&header->inject_skip_load : 0u;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&c->full[i], MODE == kWgrad ? CG : 1);
             mbar_init(&c->empty[i], 1);
@@ -596,6 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         mbar_init(&c->joined, 8 * split);
         mbar_init(&c->taken, 8 * split);
         c->abort = 0;
+        c->skip = skip;
+        if (skip) header->inject_skip_load = 0;
         mbar_fence_init();
         tmap_prefetch(&p.ma);
         tmap_prefetch(&p.mb);
@@ -688,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         const uint32_t load_bytes = kStageA + (MODE == kWgrad ? chunks_b * 8192 : p.bn / CG * 128);
         int s = 0;
         uint32_t ph = 1;
-        bool ok = true, ready = false;
+        bool ok = true, ready = false, skip = c->skip != 0;
         while (ok && walk.next(t)) {
             const Span part = span(t);
             const int m0 = t.m * kBM + (int)rank * kTileM;
@@ -707,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     ph ^= 1;
                 }
                 const bool next = mbar_test_wait(&c->empty[s], ph);
-                if (one) {
+                if (one && !skip) {
                     unsigned char *sa = smem + now * kStage, *sb = sa + kStageA;
                     const int k0 = i * kElems;
                     uint32_t bar = smem_addr(&c->full[now]);
@@ -756,6 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                         }
                     }
                 }
+                skip = false;
                 __syncwarp();
                 ready = __all_sync(0xFFFFFFFFu, next);
             }

@@ -513,3 +513,23 @@ def test_fp8_dispatch_into_the_experts(T):
         assert_near(y[lo:hi], want, err + BF16 * (want.abs() + err), "y")
         # the sums the weights carry are their own
         assert_near(total, ws * c.sum(1), 2.0 ** -23 * (ws * c.sum(1)).abs() + 1e-30, "sum")
+
+
+@pytest.mark.parametrize("T,K,N,call", [(40, 256, 256, "linear"), (40, 256, 256, "dgrad"), (300, 256, 128, "wgrad"),
+                                        (4, 2048, 256, "linear"), (6000, 256, 2048, "linear"),
+                                        (6000, 2048, 2048, "wgrad")])
+def test_waits_expire_with_timeout_status(T, K, N, call):
+    """The first load of a product is left out (a workspace hook, from the
+    host): its waits run out after their limit of 1 s, the call ends with
+    MOE_ERR_TIMEOUT, and the next one is right.  One SM, blocks that share k,
+    and pairs."""
+    x, w, dy = normal(T, K, seed=91), normal(N, K, seed=92, std=K ** -0.5), normal(T, N, seed=93)
+    r = ExpertRows(rows=T)
+    run = {"linear": lambda: r.linear(x, w), "dgrad": lambda: r.dgrad(dy, w), "wgrad": lambda: r.wgrad(dy, x)[0]}[call]
+    want = run()
+    assert r.status() == 0
+    r.ws.view(torch.int32)[7] = 1  # inject_skip_load (byte offset 28)
+    run()
+    assert r.status() == abi.MOE_ERR_TIMEOUT
+    assert int(r.ws.view(torch.int32)[7].item()) == 0  # the hook was consumed
+    assert torch.equal(run(), want) and r.status() == 0
