@@ -60,15 +60,17 @@ constexpr int kLinear = 0, kDgrad = 1, kWgrad = 2, kDgradSaved = 3;
 // accumulator columns (packed rows) that an epilogue group takes at a time
 __host__ __device__ constexpr int chunk(int MODE) { return MODE == kDgradSaved ? 16 : 32; }
 
-// Shared memory of one epilogue group (wgrad: of the bias sums' ones).  A row of 128 output columns is padded
+// Shared memory of one epilogue group.  A row of 128 output columns is padded
 // by 16 bytes (by 32 where it has 64, for swiglu), so that neighbouring rows
 // start in other banks.
 constexpr int kPitch = 272, kPitchGlu = 160, kPitchCode = 144;
 constexpr int kOutBytes = 32 * kPitch;
 constexpr int kCodeBytes = 32 * kPitchCode;
+constexpr int kOnes = 2048;          // wgrad: the bias sums' ones, then
+constexpr int kDwBytes = 32 * 32 * 2;  // for each epilogue warp 32 rows of 32 values of dw
 __host__ __device__ constexpr int group_bytes(int MODE)
 {
-    return MODE == kWgrad        ? 1024
+    return MODE == kWgrad        ? kOnes / 2 + 4 * kDwBytes
            : MODE == kDgradSaved ? 3 * 16 * kPitch + 2 * 16 * kPitchCode + 512
                                  : kOutBytes + kCodeBytes + 256 + 1024 + 512;
 }
@@ -93,7 +95,7 @@ __host__ __device__ constexpr int smem_bytes(int CG, int BN, int MODE, bool SPLI
 __host__ __device__ constexpr int tmem_cols(int BN) { return 2 * BN < 32 ? 32 : 2 * BN; }
 
 struct Params {
-    CUtensorMap ma, mb, mb32;  // mb32: 32 rows of B at a time, for an expert's last tile
+    CUtensorMap ma, mb, mb32, mo;  // mb32: 32 rows of B at a time, for an expert's last tile; mo: bf16 dw
     const int32_t *offsets;
     void *ws;
     int E, rows;
@@ -102,7 +104,6 @@ struct Params {
     int K;         // linear, dgrad: extent of k, in bytes
     int act, glu;  // glu: A's rows alternate gate and up columns
     int fp32;
-    int sectors;   // bf16 dw: rows of whole 32-byte sectors
     int whole_a, whole_b;  // an MN-major operand whose columns are whole blocks of 64
     int bn;        // columns of n per tile, at most BN
     int split;     // blocks that share a tile's k (a cluster of 2, 4 or 8), or 1
@@ -536,20 +537,35 @@ __device__ __forceinline__ void store_row(const Params &p, size_t at, const uint
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.dw) + at;
-    // whole 32-byte sectors where rows and base allow: half the store instructions
-    if (p.sectors && n == 32) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(o + j * 16), "r"(w[8 * j]),
-                         "r"(w[8 * j + 1]), "r"(w[8 * j + 2]), "r"(w[8 * j + 3]), "r"(w[8 * j + 4]),
-                         "r"(w[8 * j + 5]), "r"(w[8 * j + 6]), "r"(w[8 * j + 7])
-                         : "memory");
-        return;
-    }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         if (j * 8 < n)
             *reinterpret_cast<uint4 *>(o + j * 8) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+
+// The warp's 32 rows of 32 values as one tile copy: rows of 64 bytes in
+// shared memory (64-byte swizzle: no bank conflicts), written out by the copy
+// engine.  32 lanes' own stores to 32 rows cost the load/store unit four times
+// as much, which bounded experts with few rows.
+__device__ __forceinline__ void store_tile(const Params &p, unsigned char *buf, const uint32_t (&v)[32], int lane, int col,
+                                           int row, int e)
+{
+    if (lane == 0) bulk_wait_group_read<0>();  // the last tile has left the buffer
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = pack_bf16(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
+        *reinterpret_cast<uint4 *>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && row < p.M) {
+        tma_store_3d(&p.mo, buf, col, row, e);
+        bulk_commit_group();
+    }
 }
 
 // --------------------------------------------------------------------------
@@ -877,6 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         // Two groups of four warps take the chunks of a tile in turn.
         constexpr int kChunk = chunk(MODE);
         const int q = warp & 3, g = (warp - kEpiWarp) >> 2;  // q: the lanes of tensor memory a warp may read
+        unsigned char *const dw_tile = stg + kOnes + (warp - kEpiWarp) * kDwBytes;  // wgrad
         int acc = 0, turn = 0;
         uint32_t aph = 0;
         using Epilogue = std::conditional_t<MODE == kDgradSaved, SavedEpilogue, LinearEpilogue<FP8>>;
@@ -898,10 +915,14 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 const int m = m0 + q * 32 + lane;
                 const size_t r = (size_t)t.e * p.M + m;
                 if (m < p.M) {
-                    if (!is_bias(t)) store_row(p, r * p.N + n0 + c0, v, n);
-                    else if (p.fp32) static_cast<float *>(p.db)[r] = __uint_as_float(v[0]);
-                    else static_cast<__nv_bfloat16 *>(p.db)[r] = __float2bfloat16_rn(__uint_as_float(v[0]));
+                    if (is_bias(t)) {
+                        if (p.fp32) static_cast<float *>(p.db)[r] = __uint_as_float(v[0]);
+                        else static_cast<__nv_bfloat16 *>(p.db)[r] = __float2bfloat16_rn(__uint_as_float(v[0]));
+                    } else if (SPLIT || p.fp32) {
+                        store_row(p, r * p.N + n0 + c0, v, n);
+                    }
                 }
+                if (!SPLIT && !p.fp32 && !is_bias(t)) store_tile(p, dw_tile, v, lane, n0 + c0, m0 + q * 32, t.e);
                 __syncwarp();
             } else {
                 ep.finish(v, t.row0 + n0 + c0, n, next);
@@ -996,6 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 aph ^= acc == 0;
             }
         }
+        if (MODE == kWgrad && lane == 0) bulk_wait_group<0>();  // written, and out of shared memory
     }
     __syncwarp();
     if (*(volatile int *)&c->abort) {
@@ -1030,7 +1052,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 
 // A map of `rank` axes, innermost first; strides in values, of axes 1 and up.
 cudaError_t encode(CUtensorMap *m, bool fp8, const void *base, int rank, const uint64_t *dims,
-                   const uint64_t *strides, const uint32_t *box)
+                   const uint64_t *strides, const uint32_t *box,
+                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
 {
     const auto fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
@@ -1043,7 +1066,7 @@ cudaError_t encode(CUtensorMap *m, bool fp8, const void *base, int rank, const u
     }
     const CUresult r =
         fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
-           const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

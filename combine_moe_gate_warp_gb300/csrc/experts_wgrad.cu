@@ -20,11 +20,15 @@ cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const 
     p.N = K;
     p.fp32 = fp32;
     p.dw = dw;
-    p.sectors = !fp32 && K % 16 == 0 && reinterpret_cast<uintptr_t>(dw) % 32 == 0;
     p.db = db;
     const Cut cut = pick(N, K, G->E, true, (G->rows / G->E + 63) / 64, false);
     cudaError_t err = encode_mn(&p.ma, dy, N, G->rows, 1, 2, &p.whole_a);
     if (err == cudaSuccess) err = encode_mn(&p.mb, x, K, G->rows, 1, cut.bn / cut.cg / 64, &p.whole_b);
+    if (err == cudaSuccess && !fp32) {
+        const uint64_t d[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)G->E}, st[2] = {(uint64_t)K, (uint64_t)N * K};
+        const uint32_t b[3] = {32, 32, 1};
+        err = encode(&p.mo, false, dw, 3, d, st, b, CU_TENSOR_MAP_SWIZZLE_64B);
+    }
     if (err != cudaSuccess) return err;
     return launch_cut<kWgrad, false>(p, cut, s);
 }

@@ -115,6 +115,15 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *m, int
             : "memory");
 }
 
+// A tile from shared to global memory, in the issuing thread's bulk group;
+// what lies past the map's axes is not written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, const void *src, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(src))
+                 : "memory");
+}
+
 // Tensor memory: one warp allocates and frees; the address lands in shared memory.
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols)
