@@ -27,7 +27,7 @@
 //     pipe 86 % busy, 1.85 PFLOP/s: the matrix instructions.  Back to back for
 //     seconds the power limit lowers the clock: 306 us
 //   dgrad, 31903 rows, 16 experts, 5120 -> 2560               450 us, 87 %
-//   wgrad, the same                                           470 us, 78 %
+//   wgrad, the same                                           463 us
 //   linear, 128 rows, 32 experts, 2048 -> 2 x 1024            47 us, 5.7 TB/s:
 //     the weights' bytes (and 6 us to start and to finish)
 //   linear, 512 rows, 8 experts, 512 -> 2 x 256               6 us from the
