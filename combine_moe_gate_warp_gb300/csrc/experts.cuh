@@ -22,12 +22,12 @@
 // last row.  The blocks walk the tiles in a fixed order, derived from the
 // offsets on the device; no result depends on timing.
 //
-// What bounds it, on a GB300 (ncu, burst clocks):
-//   linear, 56851 rows, 32 experts, 2048 -> 2 x 1024 swiglu   257 us, tensor
-//     pipe 86 % busy, 1.85 PFLOP/s: the matrix instructions.  Back to back for
-//     seconds the power limit lowers the clock: 306 us
-//   dgrad, 31903 rows, 16 experts, 5120 -> 2560               450 us, 87 %
-//   wgrad, the same                                           463 us
+// What bounds it, on a GB300 (single launches; cards differ by up to 6 %):
+//   linear, 56902 rows, 32 experts, 2048 -> 2 x 1024 swiglu   257-267 us, tensor
+//     pipe 87 % busy, 1.8 PFLOP/s: the matrix instructions.  Back to back for
+//     seconds the power limit lowers the clock: 306 us and more
+//   dgrad, 31918 rows, 16 experts, 5120 -> 2560               450-475 us, 87 %
+//   wgrad, the same                                           463-469 us, 83 %
 //   linear, 128 rows, 32 experts, 2048 -> 2 x 1024            47 us, 5.7 TB/s:
 //     the weights' bytes (and 6 us to start and to finish)
 //   linear, 512 rows, 8 experts, 512 -> 2 x 256               6 us from the
