@@ -816,15 +816,16 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             for (int j = 0; j < (is_bias(t) ? 2 : 2 + chunks_b); ++j)
                 for (int o = keep * 128 + lane * 16; o < end; o += 512)
                     *reinterpret_cast<uint4 *>(sa + j * 8192 + o) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
+            // In a pair each SM holds half of B's columns and the tensor cores
+            // of both read both halves: the zeros go to the other SM too, so
+            // their arrival releases them to the cluster, and the thread that
+            // issues for the pair acquires at that scope.
+            if (CG == 2) fence_proxy_async_cluster();
+            else fence_proxy_async_smem();
             __syncwarp();
-            // The zeros are in this SM's shared memory once the fence is
-            // through, and only this SM's tensor cores read them: the arrival
-            // hands no memory to the other SM and needs no fence of its own
-            // (2900 cycles a tile).
             if (lane == 0) {
-                if (self == lead) mbar_arrive(&c->full[at]);
-                else mbar_arrive_remote(cluster_addr(&c->full[at], lead));
+                if (CG == 2) mbar_arrive_release_cluster(cluster_addr(&c->full[at], lead));
+                else mbar_arrive(&c->full[at]);
             }
         }
     } else if (warp == 1 && rank == 0) {
@@ -860,6 +861,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 for (int i = 0; i < iters; ++i) {
                     ok = ready || wait(&c->full[s], ph, c, p.ws);
                     if (!ok) break;
+                    // complete, so this answers at once: the tail's zeros, of both SMs
+                    if (MODE == kWgrad && CG == 2 && last_steps != 0 && i == iters - 1)
+                        mbar_test_wait_cluster(&c->full[s], ph);
                     tc_fence_after();
                     const int now = s;
                     if (++s == kStages) {
