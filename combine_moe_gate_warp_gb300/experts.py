@@ -5,10 +5,12 @@ layout's offsets and a workspace) and has the products as methods;
 ``ExpertFFN`` is the two-layer expert network made of them, with its hidden
 layer saved in 8 bits between the passes.  Every method checks its arguments
 on the host, allocates the outputs it is not given (through PyTorch) and
-enqueues the library's kernels on the current stream.
+enqueues the library's kernels on the handle's stream: the plan's for the rows
+of a plan, else the current one.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -110,9 +112,14 @@ class ExpertRows:
     rows one group, for the shared experts' plain products (weights then
     lack the expert axis: [N, K], bias [N]).  ``ws`` is a workspace whose
     status word takes device-detected problems; one is made if none is
-    given."""
+    given.
 
-    def __init__(self, offsets: torch.Tensor | None = None, *, rows: int, device="cuda", ws=None):
+    With a ``stream`` every call runs on it, whatever the current stream is,
+    as a RoutePlan's calls do, and the outputs that the handle allocates
+    belong to it: other streams that use them wait for it.  Without one a
+    call runs on the stream that is current then."""
+
+    def __init__(self, offsets: torch.Tensor | None = None, *, rows: int, device="cuda", ws=None, stream=None):
         if rows < 0:
             raise ValueError(f"rows: {rows}")
         self.device = torch.device(device)
@@ -127,8 +134,10 @@ class ExpertRows:
             self.E = offsets.numel() - 1
             _check(offsets, torch.int32, offsets.shape, "offsets", self.device)
         self.rows, self.offsets = rows, offsets
+        self.stream = stream
         if ws is None:
-            ws = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=self.device)
+            with self._owner():
+                ws = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=self.device)
         elif ws.numel() * ws.element_size() < _STATUS_BYTES or ws.device != self.device:
             raise ValueError(f"ws: a workspace of at least {_STATUS_BYTES} bytes on {self.device}")
         self.ws = ws
@@ -138,22 +147,40 @@ class ExpertRows:
 
     @staticmethod
     def of(plan) -> "ExpertRows":
-        """The packed rows of a RoutePlan; problems are recorded in its workspace."""
-        return ExpertRows(plan.layout.offsets, rows=plan.r_max, device=plan.layout.offsets.device, ws=plan.ws)
+        """The packed rows of a RoutePlan, on its stream, where its dispatch
+        writes them and its combine reads what the experts make of them;
+        problems are recorded in its workspace."""
+        return ExpertRows(plan.layout.offsets, rows=plan.r_max, device=plan.layout.offsets.device, ws=plan.ws,
+                          stream=plan.stream)
 
     def status(self) -> int:
         """Synchronise, return and clear the device status."""
-        return abi.moe_get_status(self.ws)
+        return abi.moe_get_status(self.ws, self.stream)
 
     def new_saved(self, N: int) -> SavedLayer:
-        return SavedLayer.empty(self.rows, N, self.device)
+        with self._owner():
+            return SavedLayer.empty(self.rows, N, self.device)
 
     # ------------------------------------------------------------------
     def _stream(self):
         if self.device.type != "cuda":
             raise ValueError(f"the rows are on {self.device}: a CUDA device is needed")
+        if self.stream is not None:
+            return self.stream.cuda_stream
         # the current stream's handle, without the Stream object around it
         return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def _owner(self):
+        """Where memory is allocated: on the handle's stream, which uses it."""
+        if self.stream is None or torch._C._cuda_getCurrentRawStream(self.device.index) == self.stream.cuda_stream:
+            return contextlib.nullcontext()
+        return torch.cuda.stream(self.stream)
+
+    def _new(self, shape, dtype=torch.bfloat16):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with self._owner():
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     def _weights(self, w, dtype):
         """(N, K, address) of weights [E, N, K], or [N, K] for one plain group."""
@@ -172,13 +199,13 @@ class ExpertRows:
 
     def _out(self, t, dtype, shape, name):
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=self.device)
+            t = self._new(shape, dtype)
             return t, t.data_ptr()
         return t, _check(t, dtype, shape, name, self.device)
 
     def _out_rows(self, t, cols, name):
         if t is None:
-            t = torch.empty((self.rows, cols), dtype=torch.bfloat16, device=self.device)
+            t = self._new((self.rows, cols))
             return t, t.data_ptr()
         return t, _check_rows(t, torch.bfloat16, self.rows, cols, name, self.device)
 
@@ -215,7 +242,7 @@ class ExpertRows:
         if saved is not None:
             sc, ss = self._saved(saved, N)
         if out is None:
-            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+            out = self._new((rows, cols))
             op = out.data_ptr()
         else:
             op = _check_rows(out, torch.bfloat16, rows, cols, "out", dev)
@@ -325,10 +352,9 @@ class ExpertFFN:
         if H2 != H or N != (2 * F if act == "swiglu" else F):
             raise ValueError(f"w1 {tuple(w1.shape)} and w2 {tuple(w2.shape)} do not fit together for act {act!r}")
         self.rows, self.w1, self.w2, self.b1, self.b2, self.act, self.dtype = rows, w1, w2, b1, b2, act, dtype
-        bf16 = dict(dtype=torch.bfloat16, device=rows.device)
         self.saved = rows.new_saved(N)
-        self.hidden = torch.empty((rows.rows, F), **bf16)   # act(u): forward, and again in the backward pass
-        self.y = torch.empty((rows.rows, H), **bf16)
+        self.hidden = rows._new((rows.rows, F))   # act(u): forward, and again in the backward pass
+        self.y = rows._new((rows.rows, H))
         self.grads = self._du = None
 
     def forward(self, x, *, residual=None, out=None):
@@ -341,10 +367,9 @@ class ExpertFFN:
         """Gradients of the last forward pass; x is its input."""
         r = self.rows
         if self.grads is None:
-            self._du = torch.empty(self.saved.codes.shape, dtype=torch.bfloat16, device=r.device)
-            like = lambda w: None if w is None else torch.empty_like(w, dtype=self.dtype)  # noqa: E731
-            self.grads = FFNGrads(torch.empty_like(self.y), like(self.w1), like(self.w2), like(self.b1),
-                                  like(self.b2))
+            self._du = r._new(self.saved.codes.shape)
+            like = lambda w: None if w is None else r._new(w.shape, self.dtype)  # noqa: E731
+            self.grads = FFNGrads(r._new(self.y.shape), like(self.w1), like(self.w2), like(self.b1), like(self.b2))
         g = self.grads
         du = r.dgrad(dy, self.w2, act=self.act, saved=self.saved, out=self._du, a=self.hidden)
         r.wgrad(dy, self.hidden, dtype=self.dtype, out=g.dw2, out_bias=g.db2)

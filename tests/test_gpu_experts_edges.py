@@ -4,7 +4,7 @@ and graphs, and the FFN's gradients element by element."""
 import pytest
 import torch
 
-from combine_moe_gate_warp_gb300 import ExpertRows
+from combine_moe_gate_warp_gb300 import ExpertFFN, ExpertRows, RoutePlan, RouteShape, abi
 from expert_util import BF16, assert_near, normal, offsets_of, spans, sum_error
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +55,58 @@ def test_wgrad_of_wide_layers(N, K, dtype):
         assert_near(dw[e], want, err + half * (want.abs() + err), f"dw[{e}]")
         want, err = d.sum(0), sum_error(hi - lo, d.abs().sum(0))
         assert_near(db[e], want, err + half * (want.abs() + err), f"db[{e}]")
+
+
+@pytest.mark.parametrize("own_stream", [True, False])
+def test_a_plan_on_a_stream_of_its_own(own_stream):
+    """route, dispatch, experts and combine follow each other on the plan's
+    stream, forward and backward, called while another stream is current and
+    the plan's is held up by work before them."""
+    T, H, E, k, F = 200, 128, 8, 2, 64
+    logits = torch.randn(T, E, generator=torch.Generator().manual_seed(111)).cuda()
+    x, dy = normal(T, H, seed=112), normal(T, H, seed=113)
+    w1, w2 = normal(E, 2 * F, H, seed=114, std=H ** -0.5), normal(E, H, F, seed=115, std=F ** -0.5)
+
+    def layer(plan, ffn):
+        plan.route(logits)
+        plan.dispatch(x)
+        plan.combine(ffn.forward(plan.packed))
+        plan.combine_backward(dy, ffn.y)
+        plan.dispatch_backward(ffn.backward(plan.d_expert_out, plan.packed).dx)
+
+    def parts(plan, ffn):
+        return [t.clone() for t in (plan.y, plan.dx, ffn.grads.dw1, ffn.grads.dw2)]
+
+    def build(stream=None):
+        plan = RoutePlan(RouteShape(T=T, H=H, E=E, k=k, P=4), "cuda", stream=stream)
+        return plan, ExpertFFN(ExpertRows.of(plan), w1, w2)
+
+    plan, ffn = build()
+    layer(plan, ffn)
+    assert plan.status() == 0
+    want = parts(plan, ffn)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if own_stream:   # the plan on a side stream, the caller on the default one
+        plan, ffn = build(side)
+        run, current = side, torch.cuda.current_stream()
+    else:            # the other way round
+        plan, ffn = build()
+        run, current = torch.cuda.current_stream(), side
+    torch.cuda.synchronize()
+    with torch.cuda.stream(current):
+        for _ in range(2):
+            for t in (plan.packed, plan.y, ffn.y, ffn.hidden):
+                t.fill_(float("nan"))
+            torch.cuda.synchronize()
+            with torch.cuda.stream(run):
+                torch.cuda._sleep(20_000_000)  # about 10 ms
+            layer(plan, ffn)
+            assert plan.status() == 0
+            torch.cuda.synchronize()
+            for got, w in zip(parts(plan, ffn), want):
+                assert torch.equal(got, w)
+            # outputs that the handle allocates are the stream's as well
+            r = ffn.rows
+            assert torch.equal(r.linear(plan.packed, w1, act="swiglu"), r.linear(plan.packed, w1, act="swiglu"))
+            assert r.status() == 0
