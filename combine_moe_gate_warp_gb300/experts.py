@@ -117,7 +117,8 @@ class ExpertRows:
     With a ``stream`` every call runs on it, whatever the current stream is,
     as a RoutePlan's calls do, and the outputs that the handle allocates
     belong to it: other streams that use them wait for it.  Without one a
-    call runs on the stream that is current then."""
+    call runs on the stream that is current then.  The rows' device is the
+    current one at every call."""
 
     def __init__(self, offsets: torch.Tensor | None = None, *, rows: int, device="cuda", ws=None, stream=None):
         if rows < 0:
@@ -155,6 +156,7 @@ class ExpertRows:
 
     def status(self) -> int:
         """Synchronise, return and clear the device status."""
+        self._stream()  # the device is the current one
         return abi.moe_get_status(self.ws, self.stream)
 
     def new_saved(self, N: int) -> SavedLayer:
@@ -165,6 +167,10 @@ class ExpertRows:
     def _stream(self):
         if self.device.type != "cuda":
             raise ValueError(f"the rows are on {self.device}: a CUDA device is needed")
+        # a launch goes to the current device, whatever the stream handle was asked of
+        if torch._C._cuda_getDevice() != self.device.index:
+            raise ValueError(f"the rows are on {self.device}, the current device is "
+                             f"cuda:{torch._C._cuda_getDevice()}: make theirs current (torch.cuda.device)")
         if self.stream is not None:
             return self.stream.cuda_stream
         # the current stream's handle, without the Stream object around it

@@ -14,10 +14,10 @@ def experts():
     return experts
 
 
-def on_gpu(monkeypatch, rows, index=0, current=0x111):
-    """The handle as it would be on cuda:`index`, with that current stream."""
+def on_gpu(monkeypatch, rows, index=0, current=0x111, device=0):
+    """The handle as it would be on cuda:`index`, with that current stream and device."""
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: current, raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: index, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: device, raising=False)
     rows.device = torch.device("cuda", index)
     return rows
 
@@ -33,3 +33,29 @@ def test_a_plans_rows_are_on_its_stream(experts, monkeypatch):
         assert on_gpu(monkeypatch, experts.ExpertRows.of(plan))._stream() == handle
     # without a stream of its own a handle follows the current one
     assert on_gpu(monkeypatch, experts.ExpertRows(off, rows=8, device="cpu"))._stream() == 0x111
+
+
+def test_another_current_device_is_refused(experts, monkeypatch):
+    """A launch goes to the current device: rows on another one are refused
+    before the library is called, by the products and by status()."""
+    def called(*args):
+        raise AssertionError("the library was called")
+
+    off = torch.tensor([0, 3, 8], dtype=torch.int32)
+    for stream in (None, SimpleNamespace(cuda_stream=0xABC)):
+        r = experts.ExpertRows(off, rows=8, device="cpu")
+        r._lib = SimpleNamespace(moe_expert_linear=called, moe_expert_dgrad=called, moe_expert_wgrad=called,
+                                 moe_act_backward=called)
+        r.stream = stream
+        on_gpu(monkeypatch, r, index=1, device=0)
+        monkeypatch.setattr(experts, "_check", lambda *a: 16)
+        monkeypatch.setattr(experts, "_check_rows", lambda *a: 16)
+        monkeypatch.setattr(experts.ExpertRows, "_new", lambda self, shape, dtype=None: torch.empty(0))
+        monkeypatch.setattr(experts.abi, "moe_get_status", called)
+        bf = dict(dtype=torch.bfloat16)
+        x, dy, w = torch.zeros(8, 32, **bf), torch.zeros(8, 64, **bf), torch.zeros(2, 64, 32, **bf)
+        saved = experts.SavedLayer.empty(8, 64, "cpu")
+        for call in (lambda: r.linear(x, w), lambda: r.dgrad(dy, w), lambda: r.wgrad(dy, x),
+                     lambda: r.act_backward(dy, act="gelu", saved=saved), r.status):
+            with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
+                call()
