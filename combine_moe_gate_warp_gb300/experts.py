@@ -22,6 +22,7 @@ ACTIVATIONS = {"none": abi.MOE_ACT_NONE, "silu": abi.MOE_ACT_SILU, "gelu": abi.M
                "swiglu": abi.MOE_ACT_SWIGLU}
 SAVED_BLOCK = 32  # columns that share one scale byte
 _STATUS_BYTES = 8192
+_INT_MAX = (1 << 31) - 1  # the library refuses what is too large for it; ctypes passes the low 32 bits of more
 
 
 @dataclass
@@ -46,6 +47,12 @@ def _act(name: str) -> int:
         return ACTIVATIONS[name]
     except KeyError:
         raise ValueError(f"act: one of {', '.join(ACTIVATIONS)}, got {name!r}") from None
+
+
+def _columns(n: int, name: str) -> int:
+    if n > _INT_MAX:
+        raise ValueError(f"{name}: {n} columns are too many")
+    return n
 
 
 def _refuse(t, dtype, shape, name, device):
@@ -121,7 +128,7 @@ class ExpertRows:
     current one at every call."""
 
     def __init__(self, offsets: torch.Tensor | None = None, *, rows: int, device="cuda", ws=None, stream=None):
-        if rows < 0:
+        if not 0 <= rows <= _INT_MAX:
             raise ValueError(f"rows: {rows}")
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
@@ -195,7 +202,7 @@ class ExpertRows:
             raise ValueError("w: expected a tensor of " + ("[E, N, K]" if self.grouped else "[N, K]"))
         if self.grouped and shape[0] != self.E:
             raise ValueError(f"w: {shape[0]} experts, the rows have {self.E}")
-        return shape[-2], shape[-1], _check(w, dtype, shape, "w", self.device)
+        return _columns(shape[-2], "w"), _columns(shape[-1], "w"), _check(w, dtype, shape, "w", self.device)
 
     def _per_expert(self, *shape):
         return (self.E, *shape) if self.grouped else shape
@@ -289,7 +296,7 @@ class ExpertRows:
             raise ValueError(f"dtype: bfloat16 or float32, got {dtype}")
         if dy.dim() != 2 or x.dim() != 2:
             raise ValueError("dy and x: expected [rows, columns]")
-        N, K = dy.shape[1], x.shape[1]
+        N, K = _columns(dy.shape[1], "dy"), _columns(x.shape[1], "x")
         dp = _check_rows(dy, torch.bfloat16, self.rows, N, "dy", self.device)
         xp = _check_rows(x, torch.bfloat16, self.rows, K, "x", self.device)
         out, op = self._out(out, dtype, self._per_expert(N, K), "out")
@@ -306,7 +313,7 @@ class ExpertRows:
         code = _act(act)
         if code == abi.MOE_ACT_NONE:
             raise ValueError("act: 'none' has no backward pass")
-        N = saved.codes.shape[-1]
+        N = _columns(saved.codes.shape[-1], "saved.codes")
         cols = N // 2 if code == abi.MOE_ACT_SWIGLU else N
         dp = _check_rows(dy, torch.bfloat16, self.rows, cols, "dy", self.device)
         sc, ss = self._saved(saved, N)

@@ -59,3 +59,25 @@ def test_another_current_device_is_refused(experts, monkeypatch):
                      lambda: r.act_backward(dy, act="gelu", saved=saved), r.status):
             with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
                 call()
+
+
+def test_sizes_past_32_bits_are_refused(experts):
+    """ctypes passes an integer's low 32 bits: sizes past them are refused
+    before they could be taken for small ones."""
+    off = torch.zeros(3, dtype=torch.int32)
+    for rows in ((1 << 32) + 8, 1 << 31, -1):
+        with pytest.raises(ValueError, match="rows"):
+            experts.ExpertRows(off, rows=rows, device="cpu")
+    assert experts.ExpertRows(off, rows=(1 << 31) - 1, device="cpu")._c.rows == (1 << 31) - 1
+    r = experts.ExpertRows(off, rows=0, device="cpu")
+    far, bf = (1 << 32) + 64, dict(dtype=torch.bfloat16)
+    wide, x = torch.empty(0, far, **bf), torch.empty(0, 64, **bf)
+    for w in (torch.empty(2, 0, far, **bf), torch.empty(2, far, 0, **bf)):
+        for call in (r.linear, r.dgrad):
+            with pytest.raises(ValueError, match="columns are too many"):
+                call(wide, w)
+    saved = experts.SavedLayer(torch.empty(0, far, dtype=torch.uint8), torch.empty(0, far // 32, dtype=torch.uint8))
+    for call in (lambda: r.wgrad(wide, x, out=x), lambda: r.wgrad(x, wide, out=x),
+                 lambda: r.act_backward(wide, act="silu", saved=saved, out=x)):
+        with pytest.raises(ValueError, match="columns are too many"):
+            call()
