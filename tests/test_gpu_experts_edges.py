@@ -1,11 +1,14 @@
 """The expert products where they are most easily wrong: cuts and tails that
 wide layers take, activations' far tails, offsets that do not rise, streams
 and graphs, and the FFN's gradients element by element."""
+import math
+
 import pytest
 import torch
 
-from combine_moe_gate_warp_gb300 import ExpertFFN, ExpertRows, RoutePlan, RouteShape, abi
-from expert_util import BF16, assert_near, normal, offsets_of, spans, sum_error
+from combine_moe_gate_warp_gb300 import ExpertFFN, ExpertRows, RoutePlan, RouteShape, SavedLayer, abi
+from expert_util import (BF16, act64, act_error, assert_near, decode64, encode_saved, grad64, grad_error, normal,
+                         offsets_of, spans, sum_error)
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +113,48 @@ def test_a_plan_on_a_stream_of_its_own(own_stream):
             r = ffn.rows
             assert torch.equal(r.linear(plan.packed, w1, act="swiglu"), r.linear(plan.packed, w1, act="swiglu"))
             assert r.status() == 0
+
+
+# Evaluated in fp32, relative to the value: exp's argument is rounded (2^-24 of
+# up to 85) and exp is off by 2 + 1.18 |argument| steps of 2^-23, which makes
+# 2^-15.6 at the far end; the rest (a fit, a division, a few products) stays
+# below 2^-18.
+FAR = 2.0 ** -15
+
+
+def phi64(u):
+    """The normal distribution function; 1 + erf has no digits left below -6."""
+    return torch.special.erfc(-u / math.sqrt(2)) / 2
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_keep_their_tails(act):
+    """Where u is far below zero the activation is small, but it is a number
+    with the digits of its type: half a step of bf16 relative to the value."""
+    lo = -12.5 if act == "gelu" else -70.0   # further out fp32's exponential ends
+    u = torch.linspace(lo, 8.0, 8 * 4096).bfloat16().reshape(-1, 8).cuda()
+    eye = torch.eye(8).bfloat16().cuda()
+    r = ExpertRows(rows=u.shape[0])
+    y = r.linear(u, eye, act=act)
+    assert r.status() == 0
+    u = u.double()
+    want = u * phi64(u) if act == "gelu" else act64(u, act)
+    assert_near(y, want, (BF16 * (1 + FAR) + FAR) * want.abs(), "y")
+
+
+def test_gelus_slope_keeps_its_tail():
+    """The slope Phi(u) + u phi(u), through a saved layer: its error is
+    relative to the two terms (they cancel near u = -0.75)."""
+    u = torch.linspace(-12.5, 8.0, 64 * 512).bfloat16().reshape(-1, 64)
+    u[:, 32:] = u[:, 32:].flip(0)  # the blocks of a row have other scales
+    codes, scales = encode_saved(u)
+    saved = SavedLayer(codes.cuda(), scales.cuda())
+    u = decode64(saved.codes, saved.scales)
+    rows = u.shape[0]
+    dy = torch.ones(rows, 64, dtype=torch.bfloat16, device="cuda")
+    r = ExpertRows(rows=rows)
+    du = r.act_backward(dy, act="gelu", saved=saved)
+    assert r.status() == 0
+    density = torch.exp(-u * u / 2) / math.sqrt(2 * math.pi)
+    want, size = phi64(u) + u * density, phi64(u) + u.abs() * density
+    assert_near(du, want, BF16 * want.abs() + 2 * FAR * size, "du")
