@@ -10,16 +10,44 @@ namespace moe {
 
 namespace {
 
-// Rows in use: offsets[E], checked against the buffers.
-__device__ __forceinline__ int rows_in_use(const int32_t *offsets, int E, int rows, void *ws)
+// The rows that belong to an expert, by the same rules as in the products.
+// Where the offsets rise and stay inside the buffers they are one span.
+// Where not, the experts that break a rule are empty, and a row is looked up
+// among the others.
+struct Members {
+    int lo[MOE_MAX_EXPERTS], hi[MOE_MAX_EXPERTS];
+};
+// First and last row to look at; true if every row between them is a member.
+// For the whole block of at least MOE_MAX_EXPERTS threads.
+__device__ __forceinline__ bool members(const int32_t *offsets, int E, int rows, void *ws, Members &m, int &first,
+                                        int &last)
 {
-    if (!offsets) return rows;
-    const int R = offsets[E];
-    if (R < 0 || R > rows) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) record_status(ws, MOE_ERR_DEVICE_DATA);
-        return 0;
+    first = 0;
+    last = rows;
+    if (!offsets) return true;
+    const int e = threadIdx.x;
+    int lo = 0, hi = 0;
+    if (e < E) {
+        lo = offsets[e];
+        hi = offsets[e + 1];
     }
-    return R;
+    if (__syncthreads_and(e >= E || (lo >= 0 && hi >= lo && hi <= rows))) {
+        first = offsets[0];
+        last = offsets[E];
+        return true;
+    }
+    if (e < E) {
+        int before = 0;  // rows below the largest offset so far are an earlier expert's
+        for (int i = 0; i <= e; ++i) before = max(before, offsets[i]);
+        if (lo < before || hi < lo || hi > rows) {
+            if (blockIdx.x == 0) record_status(ws, MOE_ERR_DEVICE_DATA);
+            lo = hi = 0;
+        }
+        m.lo[e] = lo;
+        m.hi[e] = hi;
+    }
+    __syncthreads();
+    return false;
 }
 
 __device__ __forceinline__ void unpack8(const uint4 &v, float *f)
@@ -45,14 +73,30 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const __nv_bfloat16 *
                                                            __nv_bfloat16 *du, __nv_bfloat16 *a,
                                                            const int32_t *offsets, int E, int rows, void *ws)
 {
-    const int R = rows_in_use(offsets, E, rows, ws);
+    static_assert(MOE_MAX_EXPERTS <= 256, "a thread looks at an expert");
+    __shared__ Members m;
+    int start, last;
+    const bool all = members(offsets, E, rows, ws, m, start, last);
     const bool glu = act == MOE_ACT_SWIGLU;
     const int vecs = out / 16, N = glu ? 2 * out : out;
     const long long step = (long long)gridDim.x * 256;
     const int drow = (int)(step / vecs), dcol = (int)(step % vecs);
     const long long first = (long long)blockIdx.x * 256 + threadIdx.x;
-    int row = (int)(first / vecs), col = (int)(first % vecs);
-    while (row < R) {
+    int row = start + (int)(first / vecs), col = (int)(first % vecs);
+    const auto advance = [&] {
+        row += drow;
+        col += dcol;
+        if (col >= vecs) {
+            col -= vecs;
+            ++row;
+        }
+    };
+    for (; row < last; advance()) {
+        if (!all) {
+            bool mine = false;
+            for (int e = 0; e < E; ++e) mine |= row >= m.lo[e] && row < m.hi[e];
+            if (!mine) continue;
+        }
         const size_t at = (size_t)row * out + col * 16, sat = (size_t)row * N + col * 16;
         const uint8_t *b = scales + (size_t)row * (N / 32) + col / 2;
         const uint4 d0 = *reinterpret_cast<const uint4 *>(dy + at), d1 = *reinterpret_cast<const uint4 *>(dy + at + 8);
@@ -92,12 +136,6 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const __nv_bfloat16 *
             }
             *reinterpret_cast<uint4 *>(du + sat + h * 8) = pack8(g);
             if (a) *reinterpret_cast<uint4 *>(a + at + h * 8) = pack8(v);
-        }
-        row += drow;
-        col += dcol;
-        if (col >= vecs) {
-            col -= vecs;
-            ++row;
         }
     }
 }

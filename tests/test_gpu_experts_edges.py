@@ -158,3 +158,56 @@ def test_gelus_slope_keeps_its_tail():
     density = torch.exp(-u * u / 2) / math.sqrt(2 * math.pi)
     want, size = phi64(u) + u * density, phi64(u) + u.abs() * density
     assert_near(du, want, BF16 * want.abs() + 2 * FAR * size, "du")
+
+
+@pytest.mark.parametrize("with_a", [False, True])
+@pytest.mark.parametrize("act", ["silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("out", [32, 160, 2080])
+def test_act_backward_of_ragged_rows(act, out, with_a):
+    """The activation's gradient alone: rows of several experts, the first of
+    them past the buffer's start, the last before its end."""
+    counts, first = [0, 3, 41, 0, 128, 1], 7
+    R, rows = sum(counts), first + sum(counts) + 20
+    N = 2 * out if act == "swiglu" else out
+    codes, scales = encode_saved(normal(rows, N, seed=121, std=1.5))
+    codes[:first], scales[:first], codes[first + R:], scales[first + R:] = 0x7F, 0xFF, 0x7F, 0xFF
+    saved, dy = SavedLayer(codes, scales), normal(rows, out, seed=122)
+    r = ExpertRows(offsets_of(counts) + first, rows=rows)
+    du = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    a = torch.full((rows, out), 7.0, dtype=torch.bfloat16, device="cuda") if with_a else None
+    assert r.act_backward(dy, act=act, saved=saved, out=du, a=a) is du
+    assert r.status() == 0
+    mine = slice(first, first + R)
+    u, d = decode64(codes[mine], scales[mine]), dy[mine].double()
+    want, err = grad64(u, d, act), grad_error(u, d, torch.zeros_like(d), act)
+    assert_near(du[mine], want, err + BF16 * (want.abs() + err), "du")
+    if with_a:
+        want, err = act64(u, act), act_error(u, torch.zeros_like(u), act)
+        assert_near(a[mine], want, err + BF16 * (want.abs() + err), "a")
+    for t in (du, a):
+        if t is not None:
+            assert bool((t[:first] == 7.0).all()) and bool((t[first + R:] == 7.0).all())
+
+
+@pytest.mark.parametrize("off", [[0, 40, 30, 100], [0, 40, 101, 100], [-1, 40, 70, 100], [0, 40, 70, 101],
+                                 [0, 40, 70, -5], [0, 90, 20, 80]])
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+def test_act_backward_takes_bad_offsets_for_empty(off, act):
+    """As the products do: an expert whose offsets are negative, pass the
+    rows, decrease or start below an earlier one is empty, and recorded."""
+    rows, out = 100, 64
+    N = 2 * out if act == "swiglu" else out
+    codes, scales = encode_saved(normal(rows, N, seed=123))
+    r = ExpertRows(torch.tensor(off, dtype=torch.int32, device="cuda"), rows=rows)
+    du = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    whole = torch.empty_like(du)
+    dy = normal(rows, out, seed=124)
+    r.act_backward(dy, act=act, saved=SavedLayer(codes, scales), out=du)
+    assert r.status() == abi.MOE_ERR_DEVICE_DATA and r.status() == 0
+    ExpertRows(rows=rows).act_backward(dy, act=act, saved=SavedLayer(codes, scales), out=whole)
+    good = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for e in range(3):
+        lo, hi = off[e], off[e + 1]
+        if lo >= max([0] + off[:e]) and lo <= hi <= rows:
+            good[lo:hi] = True
+    assert torch.equal(du[good], whole[good]) and bool((du[~good] == 7.0).all())
