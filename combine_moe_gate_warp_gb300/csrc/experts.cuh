@@ -119,13 +119,20 @@ struct Control {
     uint32_t tmem;
     int abort;
     unsigned skip;  // the injected failure
+    unsigned long long limit;  // of every wait, ns
     int part[12];
     int row0[MOE_MAX_EXPERTS], rows[MOE_MAX_EXPERTS];  // of each expert, checked
     int tile0[MOE_MAX_EXPERTS + 1];                    // its first tile
 };
 static_assert(sizeof(Control) <= kControl, "barriers and tile counts");
 
-// Wait for phase `parity`, at most kSpinLimitNs.  False once the limit has
+// A wait may have to outlast a whole tile: the epilogue's for the products, a
+// tail's for the rows before it, and what waits for those.  A stage takes 0.3
+// us on its SM, 1.1 us where every SM waits for HBM; 2^28 rows of one expert
+// are 4 million stages of one tile of wgrad.
+constexpr unsigned long long kStageLimitNs = 2000;
+
+// Wait for phase `parity`, at most the block's limit.  False once the limit has
 // passed or another role of the block has given up; then every role leaves
 // its loop.
 __device__ __forceinline__ bool poll(uint64_t *bar, uint32_t parity, Control *c, void *ws)
@@ -137,7 +144,7 @@ __device__ __forceinline__ bool poll(uint64_t *bar, uint32_t parity, Control *c,
         for (int i = 0; i < 16; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (*(volatile int *)&c->abort) return false;
-        if (global_timer_ns() - t0 > kSpinLimitNs) {
+        if (global_timer_ns() - t0 > c->limit) {
             *(volatile int *)&c->abort = 1;
             record_status(ws, MOE_ERR_TIMEOUT);
             return false;
@@ -615,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         mbar_init(&c->joined, 8 * split);
         mbar_init(&c->taken, 8 * split);
         c->abort = 0;
+        c->limit = kSpinLimitNs + (MODE == kWgrad ? p.rows / 64 : p.K / 128) * kStageLimitNs;
         c->skip = skip;
         if (skip) header->inject_skip_load = 0;
         mbar_fence_init();

@@ -211,3 +211,27 @@ def test_act_backward_takes_bad_offsets_for_empty(off, act):
         if lo >= max([0] + off[:e]) and lo <= hi <= rows:
             good[lo:hi] = True
     assert torch.equal(du[good], whole[good]) and bool((du[~good] == 7.0).all())
+
+
+def test_an_expert_with_very_many_rows():
+    """One expert of 152 has 2^28 rows: its weight gradient is one block's
+    tile, which takes longer than a wait's second.  Small whole numbers that
+    cancel, so that the sums are exact."""
+    rows, E, hot = (1 << 28) + 37, 152, 40
+    sign = 1 - 2 * (torch.arange(rows, device="cuda", dtype=torch.int32) & 1).to(torch.int8)
+    cols = torch.arange(1, 9, device="cuda", dtype=torch.bfloat16)
+    dy, x = torch.empty(rows, 8, dtype=torch.bfloat16, device="cuda"), cols.repeat(rows, 1)
+    torch.mul(sign[:, None], cols, out=dy)
+    del sign
+    out = rows // 3 * 2 + 1  # an odd row: what it would have taken off stays
+    x[out] = 0
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[hot + 1:] = rows
+    r = ExpertRows(off, rows=rows)
+    dw, db = r.wgrad(dy, x, bias=True, dtype=torch.float32)
+    assert r.status() == 0
+    c = cols.float()
+    # rows is odd: the last row's product is left over, and the missing odd row's
+    assert torch.equal(dw[hot], 2 * c[:, None] * c) and torch.equal(db[hot], c)
+    dw[hot], db[hot] = 0, 0
+    assert bool((dw == 0).all()) and bool((db == 0).all())
