@@ -1112,8 +1112,22 @@ cudaError_t encode_mn(CUtensorMap *m, const void *base, int cols, int rows, int 
 template <int CG, int BN, int MODE, bool FP8, bool SPLIT>
 cudaError_t launch(const Params &p, cudaStream_t s)
 {
-    // No programmatic dependent launch here: the kernel takes whole SMs and
-    // their tensor memory, so the next one has nowhere to start early.
+    // No programmatic dependent launch: do not add it.  With it (tensor memory
+    // allocated before the wait for the predecessor) a sequence of the
+    // elementwise gradient, dgrad, wgrad and a column sum stopped for good
+    // after some passes, outside every bounded wait, and the cause was not
+    // found.  Without it no block starts before the kernels ahead of it on
+    // its stream are complete, and the waits that have no limit end:
+    //   tcgen05.alloc: no other block of these kernels fits on the SM (below),
+    //     so its tensor memory is free, or held by a kernel of another stream
+    //     that gives it back without waiting for this one;
+    //   the cluster barriers: the first comes before any other wait; every
+    //     role's loop ends, by its tiles or by a limit, and meets the second;
+    //   an epilogue group's barriers: its four warps decide together (agree)
+    //     and walk the same chunks;
+    //   bulk_wait_group, tcgen05.wait::ld: copies and loads already issued,
+    //     which depend on nothing else.
+    static_assert(2 * (smem_bytes(CG, BN, MODE, SPLIT) + 1024) > 228 * 1024, "one block on an SM");
     const auto fn = experts_kernel<CG, BN, MODE, FP8, SPLIT>;
     cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes(CG, BN, MODE, SPLIT));
     if (err != cudaSuccess) return err;
