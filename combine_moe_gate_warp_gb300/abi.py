@@ -146,6 +146,8 @@ def lib():
     L.moe_expert_wgrad.restype = I
     L.moe_act_backward.argtypes = [G, P, I, I, P, P, P, P, P]
     L.moe_act_backward.restype = I
+    L.moe_expert_cut.argtypes = [I, I, I, I, I, I, ctypes.POINTER(ctypes.c_int32)]
+    L.moe_expert_cut.restype = I
     L.moe_get_status.argtypes = [P, P]
     L.moe_get_status.restype = I
     L.moe_status_string.argtypes = [I]

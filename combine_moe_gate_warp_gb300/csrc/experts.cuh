@@ -1170,55 +1170,6 @@ cudaError_t launch(const Params &p, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
-// How a product is cut: SMs of a tile (2: a pair, 256 of m; 1: 128), columns
-// of n per tile, and blocks that share a tile's k.
-struct Cut {
-    int cg, bn, split;
-};
-
-// The cut with the least time for tiles in whole waves over the SMs.  The
-// constants are cycles, measured: a stage of 64 (e4m3: 128) of k is bound by
-// its bytes, 16 KB of A and 128 per row of B in a block at about 61 a cycle,
-// or, for a pair with 256 columns, by the matrix instructions (545); after
-// the last stage the accumulator takes about 1000 per 32 columns and group,
-// and a joint sum about 2500.  Narrower tiles pay where they fill the last
-// wave: 5000 rows, 4096 -> 2048 (160 tiles of 256, 2.1 waves of 76 pairs)
-// take 63.6 us 256 wide and 55.6 us 192 wide.
-// `live` experts have `n` of the ragged axis together (`each`: wgrad, whose n
-// is the same for every expert); their sizes are not known on the host, half
-// a tile each is taken for lost.
-Cut pick(int m, long long n, int live, bool each, long long k_stages, bool narrow)
-{
-    static const Cut cuts[] = {{2, 256, 1}, {2, 224, 1}, {2, 192, 1}, {2, 160, 1}, {2, 128, 1}, {1, 128, 8},
-                               {1, 96, 1},  {1, 64, 1},  {1, 32, 8}};
-    Cut best = cuts[0];
-    double least = 0.0;
-    const int sms = device_sm_count();
-    for (const Cut &c : cuts) {
-        if (!narrow && c.bn != 256 && c.bn != 128) continue;  // wgrad loads B by 64 columns
-        const long long tm = (m + 128 * c.cg - 1) / (128 * c.cg);
-        long long tn = live == 1 || each ? (n + c.bn - 1) / c.bn * (each ? live : 1) : n / c.bn + (live + 1) / 2;
-        if (tn < live) tn = live;
-        const double bytes = 270.0 + 2.1 * c.bn / c.cg, mma = 2.13 * c.bn;
-        const double stage = c.cg == 2 && mma > bytes ? mma : bytes;
-        for (int split = 1; split <= c.split; split *= 2) {
-            if (split > 1 && k_stages < 4 * split) break;
-            // clusters of 4 and 8 leave some SMs of a GPC over
-            const long long slots = split < 4 ? sms / (c.cg * split) : sms * 7 / 8 / split;
-            // unknown sizes: 15 % more tiles, or a full last wave turns into two
-            const long long tiles = live == 1 || each ? tm * tn : tm * tn * 23 / 20;
-            const long long waves = (tiles + slots - 1) / slots;
-            const double cycles = (double)waves * k_stages / split * stage + 1000.0 * ((c.bn / split + 63) / 64) +
-                                  (split > 1 ? 2500.0 * waves : 0.0);
-            if (least == 0.0 || cycles < least) {
-                least = cycles;
-                best = {c.cg, c.bn, split};
-            }
-        }
-    }
-    return best;
-}
-
 template <int MODE, bool FP8>
 cudaError_t launch_cut(Params &p, const Cut &c, cudaStream_t s)
 {
@@ -1230,7 +1181,6 @@ cudaError_t launch_cut(Params &p, const Cut &c, cudaStream_t s)
             return c.split > 1 ? launch<1, 32, MODE, FP8, true>(p, s) : launch<1, 32, MODE, FP8, false>(p, s);
     return c.split > 1 ? launch<1, 128, MODE, FP8, true>(p, s) : launch<1, 128, MODE, FP8, false>(p, s);
 }
-
 
 template <bool FP8>
 cudaError_t linear(const moe_rows *G, const void *x, const float *x_scales, int K, const void *w,
@@ -1254,7 +1204,7 @@ cudaError_t linear(const moe_rows *G, const void *x, const float *x_scales, int 
     p.saved = static_cast<uint8_t *>(saved);
     p.saved_scales = static_cast<uint8_t *>(saved_scales);
     const int elems = FP8 ? 128 : 64;
-    const Cut cut = pick(N, G->rows, G->rows < G->E ? G->rows : G->E, false, (K + elems - 1) / elems, true);
+    const Cut cut = rows_cut(N, G->rows, G->E, (K + elems - 1) / elems);
     // w as [E][N/halves][halves][K] with the halves inside: one load brings
     // gate and up rows alternating, so that a pair of them ends in one lane
     const uint64_t h = p.glu ? 2 : 1, n = (uint64_t)N / h;
@@ -1284,7 +1234,7 @@ cudaError_t dgrad(const moe_rows *G, const void *dy, int N, const void *w, int K
     p.a = static_cast<__nv_bfloat16 *>(a);
     p.saved = static_cast<uint8_t *>(const_cast<void *>(saved));
     p.saved_scales = static_cast<uint8_t *>(const_cast<void *>(saved_scales));
-    const Cut cut = pick(K, G->rows, G->rows < G->E ? G->rows : G->E, false, (N + 63) / 64, true);
+    const Cut cut = rows_cut(K, G->rows, G->E, (N + 63) / 64);
     cudaError_t err = encode_mn(&p.ma, w, K, N, G->E, 2, &p.whole_a);
     if (err == cudaSuccess) err = encode_rows(&p.mb, false, dy, N, G->rows, 64, cut.bn / cut.cg);
     if (err == cudaSuccess && cut.bn > 32) err = encode_rows(&p.mb32, false, dy, N, G->rows, 64, 32);

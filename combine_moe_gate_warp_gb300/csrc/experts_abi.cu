@@ -106,4 +106,22 @@ moe_status moe_act_backward(const moe_rows *G, const void *dy, int N, int act, c
     return from_cuda(moe::launch_act_backward(G, dy, N, act, saved, saved_scales, du, a, stream_of(stream)));
 }
 
+moe_status moe_expert_cut(int product, int e4m3, int rows, int E, int K, int N, int32_t *cut)
+{
+    if (!cut || rows < 0 || product < MOE_EXPERT_LINEAR || product > MOE_EXPERT_WGRAD) return MOE_ERR_INVALID_ARG;
+    if (e4m3 && product != MOE_EXPERT_LINEAR) return MOE_ERR_INVALID_ARG;
+    if (E < 1 || E > MOE_MAX_EXPERTS || rows >= (1 << 30) || !cols_ok(K, 8) || !cols_ok(N, 8))
+        return MOE_ERR_UNSUPPORTED;
+    cut[0] = cut[1] = cut[2] = 0;
+    if (rows == 0) return MOE_OK;  // nothing is cut
+    const int elems = e4m3 ? 128 : 64;
+    const moe::Cut c = product == MOE_EXPERT_LINEAR  ? moe::rows_cut(N, rows, E, (K + elems - 1) / elems)
+                       : product == MOE_EXPERT_DGRAD ? moe::rows_cut(K, rows, E, (N + 63) / 64)
+                                                     : moe::wgrad_cut(N, K, rows, E);
+    cut[0] = c.cg;
+    cut[1] = c.bn;
+    cut[2] = c.split;
+    return MOE_OK;
+}
+
 }  // extern "C"

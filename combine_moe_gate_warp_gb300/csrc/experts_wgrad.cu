@@ -21,7 +21,7 @@ cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const 
     p.fp32 = fp32;
     p.dw = dw;
     p.db = db;
-    const Cut cut = pick(N, K, G->E, true, (G->rows / G->E + 63) / 64, false);
+    const Cut cut = wgrad_cut(N, K, G->rows, G->E);
     cudaError_t err = encode_mn(&p.ma, dy, N, G->rows, 1, 2, &p.whole_a);
     if (err == cudaSuccess) err = encode_mn(&p.mb, x, K, G->rows, 1, cut.bn / cut.cg / 64, &p.whole_b);
     if (err == cudaSuccess && !fp32) {

@@ -166,6 +166,15 @@ class ExpertRows:
         self._stream()  # the device is the current one
         return abi.moe_get_status(self.ws, self.stream)
 
+    def cut(self, product: str, N: int, K: int, e4m3: bool = False):
+        """(SMs of a tile, rows per tile, blocks that share its sums) of
+        "linear", "dgrad" or "wgrad" with weights [N, K] on the current
+        device, for tests and tuning."""
+        c = (ctypes.c_int32 * 3)()
+        abi._check(self._lib.moe_expert_cut(("linear", "dgrad", "wgrad").index(product), int(e4m3), self.rows, self.E,
+                                            _columns(K, "w"), _columns(N, "w"), c), "moe_expert_cut")
+        return tuple(c)
+
     def new_saved(self, N: int) -> SavedLayer:
         with self._owner():
             return SavedLayer.empty(self.rows, N, self.device)

@@ -110,6 +110,18 @@ moe_status moe_expert_wgrad(const moe_rows *G, const void *dy, int N, const void
 moe_status moe_act_backward(const moe_rows *G, const void *dy, int N, int act, const void *saved,
                             const void *saved_scales, void *du, void *a, moe_stream_t stream);
 
+/*
+ * moe_expert_cut -- how the product of these sizes is cut on the current
+ * device, for tests and for tuning; nothing is launched.
+ *   cut  out [3], on the host: SMs of a tile (2: a pair), packed rows per
+ *        tile (wgrad: columns of x), blocks that share a tile's sums; zeros
+ *        without rows.
+ */
+#define MOE_EXPERT_LINEAR 0
+#define MOE_EXPERT_DGRAD 1
+#define MOE_EXPERT_WGRAD 2
+moe_status moe_expert_cut(int product, int e4m3, int rows, int E, int K, int N, int32_t *cut);
+
 #ifdef __cplusplus
 }
 #endif

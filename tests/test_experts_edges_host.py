@@ -81,3 +81,20 @@ def test_sizes_past_32_bits_are_refused(experts):
                  lambda: r.act_backward(wide, act="silu", saved=saved, out=x)):
         with pytest.raises(ValueError, match="columns are too many"):
             call()
+
+
+def test_cut_refusals(experts):
+    L, abi = experts.abi.lib(), experts.abi
+    import ctypes
+    out = (ctypes.c_int32 * 3)(9, 9, 9)
+    bad, uns = abi.MOE_ERR_INVALID_ARG, abi.MOE_ERR_UNSUPPORTED
+    for args, want in (((3, 0, 8, 1, 64, 64, out), bad), ((-1, 0, 8, 1, 64, 64, out), bad),
+                       ((0, 0, -1, 1, 64, 64, out), bad), ((0, 0, 8, 1, 64, 64, None), bad),
+                       ((1, 1, 8, 1, 64, 64, out), bad), ((0, 0, 8, 0, 64, 64, out), uns),
+                       ((0, 0, 8, 257, 64, 64, out), uns), ((2, 0, 1 << 30, 1, 64, 64, out), uns),
+                       ((0, 0, 8, 1, 60, 64, out), uns), ((0, 0, 8, 1, 64, (1 << 20) + 8, out), uns)):
+        assert L.moe_expert_cut(*args) == want, args
+    r = experts.ExpertRows(torch.zeros(3, dtype=torch.int32), rows=0, device="cpu")
+    assert r.cut("linear", 64, 64) == (0, 0, 0)  # nothing to cut
+    with pytest.raises(ValueError):
+        r.cut("product", 64, 64)

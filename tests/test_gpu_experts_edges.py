@@ -7,8 +7,8 @@ import pytest
 import torch
 
 from combine_moe_gate_warp_gb300 import ExpertFFN, ExpertRows, RoutePlan, RouteShape, SavedLayer, abi
-from expert_util import (BF16, act64, act_error, assert_near, decode64, encode_saved, grad64, grad_error, normal,
-                         offsets_of, spans, sum_error)
+from expert_util import (BF16, act64, act_error, assert_near, decode64, encode_saved, grad64, grad_error, linear64,
+                         normal, offsets_of, spans, sum_error)
 
 pytestmark = pytest.mark.gpu
 
@@ -17,6 +17,118 @@ pytestmark = pytest.mark.gpu
 def _built():
     import combine_moe_gate_warp_gb300 as pkg
     pkg.build()
+
+
+def ragged(rows, E):
+    """Counts that leave experts empty, fill no tile and not all rows."""
+    share = [(7 * e * e + 3 * e) % 11 for e in range(E)]
+    counts = [(rows - 2) * v // max(sum(share), 1) for v in share]
+    assert 0 in counts and 0 < sum(counts) < rows
+    return counts
+
+
+def fill(t, rows, value=float("nan")):
+    out = torch.full((rows, *t.shape[1:]), value, dtype=t.dtype, device=t.device)
+    out[:t.shape[0]] = t
+    return out
+
+
+# SMs of a tile, rows per tile, blocks that share its sums; rows, experts, output columns, k
+CUTS = [((1, 32, 1), 7, 3, 96, 64), ((1, 32, 2), 7, 3, 1184, 1040), ((1, 32, 4), 7, 3, 96, 1040),
+        ((1, 32, 8), 7, 3, 96, 2064), ((1, 64, 1), 2001, 9, 160, 64), ((1, 96, 1), 4001, 5, 288, 144),
+        ((1, 128, 1), 4001, 7, 288, 272), ((1, 128, 2), 2001, 9, 160, 1168), ((1, 128, 4), 450, 3, 160, 1040),
+        ((1, 128, 8), 130, 7, 160, 2064), ((2, 128, 1), 5001, 3, 160, 144), ((2, 160, 1), 1501, 7, 1184, 144),
+        ((2, 192, 1), 6001, 3, 288, 144), ((2, 224, 1), 6001, 5, 288, 528), ((2, 256, 1), 450, 3, 4128, 528)]
+
+
+@pytest.mark.parametrize("cut,rows,E,m,k", CUTS)
+def test_every_cut_of_linear_and_dgrad(cut, rows, E, m, k):
+    """Each way in which the rows' products are cut, forward with everything
+    in the epilogue, and the rows' gradient, plain and through a saved layer."""
+    counts = ragged(rows, E)
+    R = sum(counts)
+    r = ExpertRows(offsets_of(counts), rows=rows)
+    assert r.cut("linear", m, k) == cut and r.cut("dgrad", k, m) == cut
+    x, w = normal(R, k, seed=131), normal(E, m, k, seed=132, std=k ** -0.5)
+    b, res = normal(E, m, seed=133), normal(R, m, seed=134)
+    xp, saved = fill(x, rows), r.new_saved(m)
+    y = r.linear(xp, w, bias=b, act="silu", residual=fill(res, rows), saved=saved)
+    assert r.status() == 0
+    u, e = linear64(x, w, counts, b)
+    want, err = act64(u, "silu") + res.double(), act_error(u, e, "silu")
+    err = err + 2.0 ** -23 * want.abs()
+    assert_near(y[:R], want, err + BF16 * (want.abs() + err), "y")
+    # half a step of a code is 2^-4 of the value or 2^-10 of the scale
+    kept, scale = decode64(saved.codes[:R], saved.scales[:R]), torch.pow(2.0, saved.scales[:R].double() - 127)
+    assert_near(kept, u, 2.0 ** -4 * (u.abs() + e) + 2.0 ** -10 * scale.repeat_interleave(32, -1) + e, "saved")
+    wt = w.mT.contiguous()  # its product's k is the forward's
+    dx = r.dgrad(xp, wt)
+    d, e = linear64(x, w, counts)
+    assert r.status() == 0
+    assert_near(dx[:R], d, e + BF16 * (d.abs() + e), "dx")
+    codes, scales = encode_saved(normal(R, m, seed=135, std=1.5))
+    a = torch.full((rows, m), 7.0, dtype=torch.bfloat16, device="cuda")
+    du = r.dgrad(xp, wt, act="gelu", saved=SavedLayer(fill(codes, rows, 0x7F), fill(scales, rows, 0xFF)), a=a)
+    assert r.status() == 0
+    u = decode64(codes, scales)
+    want, err = grad64(u, d, "gelu"), grad_error(u, d, e, "gelu")
+    assert_near(du[:R], want, err + BF16 * (want.abs() + err), "du")
+    want, err = act64(u, "gelu"), act_error(u, torch.zeros_like(u), "gelu")
+    assert_near(a[:R], want, err + BF16 * (want.abs() + err), "a")
+    assert bool((a[R:] == 7.0).all())
+
+
+CUTS_E4M3 = [((1, 32, 1), 7, 3, 96, 64), ((1, 32, 2), 7, 3, 1184, 2064), ((1, 32, 4), 7, 3, 96, 2064),
+             ((1, 32, 8), 7, 3, 96, 4112), ((1, 64, 1), 2001, 9, 160, 64), ((1, 96, 1), 4001, 5, 288, 272),
+             ((1, 128, 1), 611, 7, 4128, 144), ((1, 128, 2), 2001, 9, 160, 4112), ((1, 128, 4), 450, 3, 160, 2064),
+             ((1, 128, 8), 130, 7, 160, 4112), ((2, 128, 1), 5001, 3, 160, 272), ((2, 160, 1), 1501, 7, 1184, 272),
+             ((2, 192, 1), 6001, 3, 288, 272), ((2, 224, 1), 6001, 5, 288, 1040), ((2, 256, 1), 450, 3, 4128, 1040)]
+
+
+@pytest.mark.parametrize("cut,rows,E,m,k", CUTS_E4M3)
+def test_every_cut_of_e4m3_rows(cut, rows, E, m, k):
+    """x = zero + scale * code, w = scale * code, from the codes in 64 bits.
+    The sums are fp32 (products of codes, then three fp32 steps)."""
+    counts = ragged(rows, E)
+    R = sum(counts)
+    r = ExpertRows(offsets_of(counts), rows=rows)
+    assert r.cut("linear", m, k, e4m3=True) == cut
+    g = torch.Generator().manual_seed(141)
+    xq, wq = ((torch.randn(*s, generator=g) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).cuda()
+              for s in ((R, k), (E, m, k)))
+    xs = (torch.rand(R, 2, generator=g) * 0.02 + 0.001).cuda()
+    ws = torch.empty(E, m, 2, device="cuda")
+    ws[..., 0] = (torch.rand(E, m, generator=g) * 1e-3 + 1e-4).cuda()
+    ws[..., 1] = (wq.double().sum(2) * ws[..., 0].double()).float()
+    y = r.linear(fill(xq.view(torch.uint8), rows, 0x7F), wq.view(torch.uint8), x_scales=fill(xs, rows), w_scales=ws)
+    assert r.status() == 0
+    for e, lo, hi in spans(counts):
+        a, b = xq[lo:hi].double(), wq[e].double()
+        s, z = xs[lo:hi, :1].double() * ws[e, :, 0].double(), xs[lo:hi, 1:].double() * ws[e, :, 1].double()
+        acc = a @ b.T
+        want = s * acc + z
+        err = s * sum_error(k, a.abs() @ b.abs().T) + 2.0 ** -22 * ((s * acc).abs() + z.abs())
+        assert_near(y[lo:hi], want, err + BF16 * (want.abs() + err), f"y of expert {e}")
+
+
+@pytest.mark.parametrize("cut,rows,E,m,k", [
+    ((1, 128, 1), 20, 9, 96, 1040), ((1, 128, 2), 2500, 3, 96, 64), ((1, 128, 4), 3001, 3, 96, 64),
+    ((1, 128, 8), 6001, 3, 96, 64), ((2, 128, 1), 2001, 9, 520, 392), ((2, 128, 1), 4001, 7, 288, 528),
+    ((2, 256, 1), 7, 7, 1056, 4112), ((2, 256, 1), 6001, 5, 1032, 520)])
+def test_every_cut_of_wgrad(cut, rows, E, m, k):
+    counts = ragged(rows, E)
+    R = sum(counts)
+    r = ExpertRows(offsets_of(counts), rows=rows)
+    assert r.cut("wgrad", m, k) == cut
+    dy, x = normal(R, m, seed=151), normal(R, k, seed=152)
+    dw, db = r.wgrad(fill(dy, rows), fill(x, rows), bias=True)
+    assert r.status() == 0
+    for e, lo, hi in spans(counts):
+        d, v = dy[lo:hi].double(), x[lo:hi].double()
+        want, err = d.T @ v, sum_error(hi - lo, d.abs().T @ v.abs())
+        assert_near(dw[e], want, err + BF16 * (want.abs() + err), f"dw[{e}]")
+        want, err = d.sum(0), sum_error(hi - lo, d.abs().sum(0))
+        assert_near(db[e], want, err + BF16 * (want.abs() + err), f"db[{e}]")
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -37,6 +149,7 @@ def test_wgrad_of_wide_layers(N, K, dtype):
     xp = torch.full((rows, K), float("nan"), dtype=torch.bfloat16, device="cuda")
     dp[:R], xp[:R] = dy, x
     r = ExpertRows(offsets_of(counts), rows=rows)
+    assert r.cut("wgrad", N, K) == (2, 256, 1)
     half = BF16 if dtype == torch.bfloat16 else 2.0 ** -24
     first = None
     for _ in range(4):
