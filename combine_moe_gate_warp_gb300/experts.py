@@ -211,7 +211,10 @@ class ExpertRows:
             raise ValueError("w: expected a tensor of " + ("[E, N, K]" if self.grouped else "[N, K]"))
         if self.grouped and shape[0] != self.E:
             raise ValueError(f"w: {shape[0]} experts, the rows have {self.E}")
-        return _columns(shape[-2], "w"), _columns(shape[-1], "w"), _check(w, dtype, shape, "w", self.device)
+        N, K = shape[-2:]
+        if N > _INT_MAX or K > _INT_MAX:
+            raise ValueError(f"w: {max(N, K)} columns are too many")
+        return N, K, _check(w, dtype, shape, "w", self.device)
 
     def _per_expert(self, *shape):
         return (self.E, *shape) if self.grouped else shape
