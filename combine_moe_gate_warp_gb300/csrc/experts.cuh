@@ -17,9 +17,8 @@
 //
 // A block is persistent: warp 0 loads tiles of 128 bytes of k with TMA into
 // a ring of stages, warp 1 issues the matrix instructions into one of two
-// accumulators in tensor memory, two groups of four warps (4-11) drain the
-// other one, and in wgrad warp 3 clears what a stage holds past an expert's
-// last row.  The blocks walk the tiles in a fixed order, derived from the
+// accumulators in tensor memory, and two groups of four warps (4-11) drain the
+// other one.  The blocks walk the tiles in a fixed order, derived from the
 // offsets on the device; no result depends on timing.
 //
 // What bounds it, on a GB300 (single launches; cards differ by up to 6 %):
@@ -115,7 +114,7 @@ struct Params {
 };
 
 struct Control {
-    uint64_t full[12], empty[12], tail[12], acc_full[2], acc_empty[2], joined, taken;
+    uint64_t full[12], empty[12], acc_full[2], acc_empty[2], joined, taken;
     uint32_t tmem;
     int abort;
     unsigned skip;  // the injected failure
@@ -126,8 +125,8 @@ struct Control {
 };
 static_assert(sizeof(Control) <= kControl, "barriers and tile counts");
 
-// A wait may have to outlast a whole tile: the epilogue's for the products, a
-// tail's for the rows before it, and what waits for those.  A stage takes 0.3
+// A wait may have to outlast a whole tile: the epilogue's for the products, and
+// what waits for it.  A stage takes 0.3
 // us on its SM, 1.1 us where every SM waits for HBM; 2^28 rows of one expert
 // are 4 million stages of one tile of wgrad.
 constexpr unsigned long long kStageLimitNs = 2000;
@@ -611,9 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     if (tid == 0) {
         const unsigned skip = blockIdx.x == 0 ? *(volatile unsigned *)&header->inject_skip_load : 0u;
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&c->full[i], MODE == kWgrad ? CG : 1);
+            mbar_init(&c->full[i], 1);
             mbar_init(&c->empty[i], 1);
-            mbar_init(&c->tail[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->acc_full[i], 1);
@@ -740,35 +738,31 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     unsigned char *sa = smem + now * kStage, *sb = sa + kStageA;
                     const int k0 = i * kElems;
                     uint32_t bar = smem_addr(&c->full[now]);
+                    // the pair's first block expects the bytes of both
+                    if (CG == 1 || self == 0) mbar_arrive_expect_tx(&c->full[now], CG * bytes);
+                    else bar = cluster_addr(&c->full[now], 0);
                     if constexpr (MODE == kWgrad) {
-                        if (t.rows - k0 < 64) {  // a tail: see warp 3
-                            bar = smem_addr(&c->tail[now]);
-                            mbar_arrive_expect_tx(&c->tail[now], bytes);
-                        } else if (CG == 1 || self == 0) {
-                            mbar_arrive_expect_tx(&c->full[now], bytes);
-                        } else {
-                            bar = cluster_addr(&c->full[now], 0);
-                            mbar_arrive_expect_tx_remote(bar, bytes);
-                        }
-                        const int row = t.row0 + k0;
+                        // The last rows of an expert rarely fill 64 of k; the
+                        // rows after them are another expert's, or nobody's
+                        // with any bits in them.  The window of a tail starts
+                        // before its first row: zeros come first, the tail's
+                        // rows last (encode_window).
+                        const int row = t.row0 + k0, from = min(t.rows - k0 - 64, 0);
                         if (p.whole_a) {
-                            tma_load_4d<CG>(sa, &p.ma, 0, row, m0 / 64, 0, bar);
+                            tma_load_4d<CG>(sa, &p.ma, 0, from, row, m0 / 64, bar);
                         } else {
                             for (int j = 0; j < 2; ++j)
-                                tma_load_4d<CG>(sa + j * 8192, &p.ma, m0 + 64 * j, row, 0, 0, bar);
+                                tma_load_4d<CG>(sa + j * 8192, &p.ma, m0 + 64 * j, from, row, 0, bar);
                         }
                         if (!no_b) {
                             if (p.whole_b) {
-                                tma_load_4d<CG>(sb, &p.mb, 0, row, n0 / 64, 0, bar);
+                                tma_load_4d<CG>(sb, &p.mb, 0, from, row, n0 / 64, bar);
                             } else {
                                 for (int j = 0; j < chunks_b; ++j)
-                                    tma_load_4d<CG>(sb + j * 8192, &p.mb, n0 + 64 * j, row, 0, 0, bar);
+                                    tma_load_4d<CG>(sb + j * 8192, &p.mb, n0 + 64 * j, from, row, 0, bar);
                             }
                         }
                     } else {
-                        // the pair's first block expects the bytes of both
-                        if (CG == 1 || self == 0) mbar_arrive_expect_tx(&c->full[now], CG * bytes);
-                        else bar = cluster_addr(&c->full[now], 0);
                         if constexpr (MODE == kLinear) {
                             tma_load_4d<CG>(sa, &p.ma, k0, 0, p.glu ? m0 / 2 : m0, t.e, bar);
                         } else if (p.whole_a) {
@@ -799,43 +793,6 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 ph ^= 1;
             }
         }
-    } else if (MODE == kWgrad && warp == 3) {
-        // ---- tails ---------------------------------------------------------
-        // The last rows of an expert rarely fill 64 of k; the rows after them
-        // are another expert's, or nobody's with any bits in them.  That
-        // stage lands on a barrier of its own, its rows past the end, up to
-        // the next 16 that a matrix instruction takes, are zeroed in both
-        // tiles, and then it counts as full.
-        int s = 0;
-        uint32_t phases = 0;  // of each stage's barrier
-        bool ok = true;
-        while (ok && walk.next(t)) {
-            const Span part = span(t);
-            const int keep = t.rows & 63;
-            s = (s + part.count) % kStages;
-            if (keep == 0 || !part.last || part.count == 0) continue;
-            const int at = s == 0 ? kStages - 1 : s - 1;  // the tile's last stage
-            ok = wait(&c->tail[at], (phases >> at) & 1, c, p.ws);
-            if (!ok) break;
-            phases ^= 1u << at;
-            // row k of a tile is the 128 bytes at 128 * k of each 8 KB
-            unsigned char *sa = smem + at * kStage;
-            const int end = (keep + 15) / 16 * 16 * 128;
-            for (int j = 0; j < (is_bias(t) ? 2 : 2 + chunks_b); ++j)
-                for (int o = keep * 128 + lane * 16; o < end; o += 512)
-                    *reinterpret_cast<uint4 *>(sa + j * 8192 + o) = make_uint4(0, 0, 0, 0);
-            // In a pair each SM holds half of B's columns and the tensor cores
-            // of both read both halves: the zeros go to the other SM too, so
-            // their arrival releases them to the cluster, and the thread that
-            // issues for the pair acquires at that scope.
-            if (CG == 2) fence_proxy_async_cluster();
-            else fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2) mbar_arrive_release_cluster(cluster_addr(&c->full[at], lead));
-                else mbar_arrive(&c->full[at]);
-            }
-        }
     } else if (warp == 1 && rank == 0) {
         // ---- matrix instructions ------------------------------------------
         // One elected thread issues; the warp walks the loop together, so that
@@ -862,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 const uint32_t idesc = mma_idesc(FP8, kMnA, kMnB, kBM, width(t));
                 const uint32_t d = tmem + acc * BN;
                 const bool bias = is_bias(t);
+                // the steps of 16 rows that a tail fills, the stage's last
                 const int last_steps = MODE == kWgrad && span(t).last ? ((t.rows & 63) + 15) / 16 : 0;
                 ok = wait(&c->acc_empty[acc], aph ^ 1, c, p.ws);
                 if (!ok) break;
@@ -869,9 +827,6 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 for (int i = 0; i < iters; ++i) {
                     ok = ready || wait(&c->full[s], ph, c, p.ws);
                     if (!ok) break;
-                    // complete, so this answers at once: the tail's zeros, of both SMs
-                    if (MODE == kWgrad && CG == 2 && last_steps != 0 && i == iters - 1)
-                        mbar_test_wait_cluster(&c->full[s], ph);
                     tc_fence_after();
                     const int now = s;
                     if (++s == kStages) {
@@ -880,12 +835,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     }
                     const bool next = mbar_test_wait(&c->full[s], ph);
                     const uint64_t da = da0 + (uint64_t)(now * (kStage >> 4)), db = db0 + (uint64_t)(now * (kStage >> 4));
-                    // a tail's steps of 16 rows past its end are left out
-                    const int steps = MODE == kWgrad && last_steps != 0 && i == iters - 1 ? last_steps : 4;
+                    const int from = MODE == kWgrad && last_steps != 0 && i == iters - 1 ? 4 - last_steps : 0;
                     if (one) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (MODE != kWgrad || k < steps) mma_ss<CG, FP8>(d, da + k * kStepA, bias ? ones : db + k * kStepB, idesc, (i | k) != 0);
+                            if (MODE != kWgrad || k >= from)
+                                mma_ss<CG, FP8>(d, da + k * kStepA, bias ? ones : db + k * kStepB, idesc, i != 0 || k != from);
                         mma_commit<CG>(&c->empty[now]);
                     }
                     __syncwarp();
@@ -1105,6 +1060,25 @@ cudaError_t encode_mn(CUtensorMap *m, const void *base, int cols, int rows, int 
         return encode(m, false, base, 4, d, st, b);
     }
     const uint64_t d[4] = {(uint64_t)cols, (uint64_t)rows, 1, (uint64_t)E}, st[3] = {(uint64_t)cols, per, per};
+    const uint32_t b[4] = {64, 64, 1, 1};
+    return encode(m, false, base, 4, d, st, b);
+}
+
+// The same for wgrad, whose k are packed rows: the window axis before the rows
+// slides over them (both have the row's stride), so that value (c, i, r) is
+// column c of row r + i for 0 <= i < 64.  A load that starts at i = -z gets z
+// rows of zeros and then rows r .. r + 63 - z, whatever follows those.  Only
+// rows that the load asks for are read: r + i stays below `rows`.
+cudaError_t encode_window(CUtensorMap *m, const void *base, int cols, int rows, int blocks, int *whole)
+{
+    const uint64_t pitch = (uint64_t)cols, r = (uint64_t)rows;
+    *whole = cols % 64 == 0;
+    if (*whole) {
+        const uint64_t d[4] = {64, 64, r, pitch / 64}, st[3] = {pitch, pitch, 64};
+        const uint32_t b[4] = {64, 64, 1, (uint32_t)blocks};
+        return encode(m, false, base, 4, d, st, b);
+    }
+    const uint64_t d[4] = {pitch, 64, r, 1}, st[3] = {pitch, pitch, pitch};
     const uint32_t b[4] = {64, 64, 1, 1};
     return encode(m, false, base, 4, d, st, b);
 }

@@ -22,8 +22,8 @@ cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const 
     p.dw = dw;
     p.db = db;
     const Cut cut = wgrad_cut(N, K, G->rows, G->E);
-    cudaError_t err = encode_mn(&p.ma, dy, N, G->rows, 1, 2, &p.whole_a);
-    if (err == cudaSuccess) err = encode_mn(&p.mb, x, K, G->rows, 1, cut.bn / cut.cg / 64, &p.whole_b);
+    cudaError_t err = encode_window(&p.ma, dy, N, G->rows, 2, &p.whole_a);
+    if (err == cudaSuccess) err = encode_window(&p.mb, x, K, G->rows, cut.bn / cut.cg / 64, &p.whole_b);
     if (err == cudaSuccess && !fp32) {
         const uint64_t d[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)G->E}, st[2] = {(uint64_t)K, (uint64_t)N * K};
         const uint32_t b[3] = {32, 32, 1};

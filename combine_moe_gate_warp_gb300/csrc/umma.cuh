@@ -40,21 +40,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
     return done != 0;
 }
 
-// The same, and what the arriving threads of any CTA in the cluster wrote
-// before mbar_arrive_release_cluster is seen after it.
-__device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -70,10 +55,10 @@ __device__ __forceinline__ void cluster_sync_all()
 }
 
 // Arrivals on a barrier anywhere in the cluster (a shared::cluster address).
-// Plain ones are no fence at cluster scope: once per stage of a ring such a
+// None of them is a fence at cluster scope: once per stage of a ring such a
 // fence doubled the time of a product (645 us against 348 us for 57000 rows,
 // 2048 x 2048).  Where a thread's memory is handed to another CTA, fence_cluster
-// comes before, or the arrival is the releasing one.
+// comes before.
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v)
 {
@@ -82,22 +67,6 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v)
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Generic accesses of shared memory before this point are ordered before
-// later accesses by the async proxy (TMA, matrix instructions) of any CTA in
-// the cluster.
-__device__ __forceinline__ void fence_proxy_async_cluster()
-{
-    asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect_tx_remote(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
 }
 
 __device__ __forceinline__ void tmap_prefetch(const CUtensorMap *m)
