@@ -25,8 +25,8 @@
 //   linear, 56902 rows, 32 experts, 2048 -> 2 x 1024 swiglu   257-267 us, tensor
 //     pipe 87 % busy, 1.8 PFLOP/s: the matrix instructions.  Back to back for
 //     seconds the power limit lowers the clock: 306 us and more
-//   dgrad, 31918 rows, 16 experts, 5120 -> 2560               450-475 us, 87 %
-//   wgrad, the same                                           463-469 us, 83 %
+//   dgrad, 31918 rows, 16 experts, 5120 -> 2560               450-477 us, 86 %
+//   wgrad, the same                                           460 us, 85 %
 //   linear, 128 rows, 32 experts, 2048 -> 2 x 1024            47 us, 5.7 TB/s:
 //     the weights' bytes (and 6 us to start and to finish)
 //   linear, 512 rows, 8 experts, 512 -> 2 x 256               6 us from the
@@ -126,9 +126,9 @@ struct Control {
 static_assert(sizeof(Control) <= kControl, "barriers and tile counts");
 
 // A wait may have to outlast a whole tile: the epilogue's for the products, and
-// what waits for it.  A stage takes 0.3
-// us on its SM, 1.1 us where every SM waits for HBM; 2^28 rows of one expert
-// are 4 million stages of one tile of wgrad.
+// what waits for it.  A stage takes 0.3 us on its SM, and 48 KB for each of
+// 152 SMs are 1.1 us of HBM's time; 2^28 rows of one expert are 4 million
+// stages of one tile of wgrad.
 constexpr unsigned long long kStageLimitNs = 2000;
 
 // Wait for phase `parity`, at most the block's limit.  False once the limit has
