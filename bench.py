@@ -520,22 +520,53 @@ def run_ours(args):
     if sampler:
         sampler.stop()
     if rank == 0:
-        line = dict(entries[headline])
-        if len(names) > 1:
-            line["headline_workload"] = (f"{headline}: the largest of the workloads timed here (the metric names "
-                                         "no workload); every workload's full entry is under 'workloads'")
-            line["workloads"] = {n: {k2: v for k2, v in e.items() if k2 not in LINE_ONLY_KEYS}
-                                 for n, e in entries.items()}
-        print(json.dumps(line), flush=True)
+        for name, e in entries.items():
+            print("workload " + name + ": " + json.dumps(e), file=sys.stderr, flush=True)
+        print(json.dumps(contract_line(entries, headline)), flush=True)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
     return 0
 
 
-# keys of the contract line that a per-workload entry does not repeat
-LINE_ONLY_KEYS = ("metric", "unit", "n_gpus", "steps", "warmup", "higher_is_better", "scaling", "vs_baseline",
-                  "data")
+# what the line says of each workload: of a nested entry these of its keys.
+# The complete entries, with the notes on how each number was taken, go to
+# standard error: a line of all of them is 29 KB, more than its readers keep.
+SHORT = {"value": (), "ms_per_step": (), "hbm_frac": (), "unpipelined": ("ms_per_step", "hbm_frac"),
+         "graph": ("ms_per_step", "hbm_frac"), "roofline": ("kernel", "frac"),
+         "e2e": ("value", "h2d_bytes_per_step", "d2h_bytes_per_step"), "cpu_baseline": ("value",),
+         "combine_ulp": ("beyond_1ulp", "outside_bound"), "clocks": ("sm_mhz", "reasons"),
+         "backward": ("ms_per_pass",), "dedup": ("send_over_packed", "dispatch_frac")}
+
+
+def _short(v):
+    if isinstance(v, float):
+        return float(f"{v:.5g}")
+    return {k: _short(x) for k, x in v.items()} if isinstance(v, dict) else v
+
+
+def short_entry(e):
+    out = {}
+    for key, inner in SHORT.items():
+        if key in e:
+            v = e[key]
+            out[key] = _short({k: v[k] for k in inner if k in v} if inner and isinstance(v, dict) else v)
+    return out
+
+
+def contract_line(entries, headline):
+    """The line of a run: the headline's entry, and with several workloads
+    the short entry of each."""
+    line = dict(entries[headline])
+    if len(entries) > 1:
+        for key in ("backward", "dedup"):
+            if key in line:
+                line[key] = short_entry(line)[key]
+        line["headline_workload"] = (f"{headline}: the largest of the workloads timed here (the metric names "
+                                     "no workload); every workload's numbers are under 'workloads', its full entry "
+                                     "on standard error")
+        line["workloads"] = {n: short_entry(e) for n, e in entries.items()}
+    return line
 
 
 def measure_workload(args, world, rank, dev, sampler, cpu_seconds):
