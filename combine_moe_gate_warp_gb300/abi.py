@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from dataclasses import dataclass
 
 import torch
 
@@ -30,6 +31,9 @@ MOE_SOFTMAX_TOPK = 1
 MOE_FP8_PER_TOKEN = 1
 MOE_FP8_PER_EXPERT = 2
 MOE_FP8_GLOBAL = 3
+
+MOE_SCORE_SIGMOID = 0
+MOE_SCORE_SOFTMAX = 1
 
 MOE_ACT_NONE = 0
 MOE_ACT_SILU = 1
@@ -62,6 +66,15 @@ class moe_layout(ctypes.Structure):
         ("part_tokens", ctypes.c_void_p), ("src_pos", ctypes.c_void_p),
         ("dst_row", ctypes.c_void_p), ("capacity_mask", ctypes.c_void_p),
         ("dropped", ctypes.c_void_p),
+    ]
+
+
+class moe_scoring(ctypes.Structure):
+    """Mirror of ``struct moe_scoring``."""
+    _fields_ = [
+        ("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("bias_rate", ctypes.c_float), ("bias", ctypes.c_void_p), ("bias_next", ctypes.c_void_p),
     ]
 
 
@@ -148,6 +161,17 @@ def lib():
     L.moe_act_backward.restype = I
     L.moe_expert_cut.argtypes = [I, I, I, I, I, I, ctypes.POINTER(ctypes.c_int32)]
     L.moe_expert_cut.restype = I
+    S = ctypes.POINTER(moe_scoring)
+    L.moe_gate_scored.argtypes = [P, I, I, I, S, P, P, P, P, P, P, SZ, P]
+    L.moe_gate_scored.restype = I
+    L.moe_gate_scored_backward.argtypes = [P, P, P, I, I, I, S, P, P, SZ, P]
+    L.moe_gate_scored_backward.restype = I
+    L.moe_dispatch_fp4.argtypes = [P, I, I, ctypes.POINTER(moe_layout), P, P, P]
+    L.moe_dispatch_fp4.restype = I
+    L.moe_quantize_fp4.argtypes = [G, P, I, P, P, P]
+    L.moe_quantize_fp4.restype = I
+    L.moe_dequantize_fp4.argtypes = [G, P, P, I, P, P]
+    L.moe_dequantize_fp4.restype = I
     L.moe_get_status.argtypes = [P, P]
     L.moe_get_status.restype = I
     L.moe_status_string.argtypes = [I]
@@ -238,6 +262,112 @@ def moe_route_launches(T: int, E: int, k: int, mode: int, P: int) -> int:
     """Kernel launches moe_route takes for these sizes on the current device
     (1 fused, 2 gate + layout, 0 unsupported)."""
     return int(lib().moe_route_launches(T, E, k, mode, P))
+
+
+@dataclass(frozen=True)
+class Scoring:
+    """Routing by scores (``moe_gate_scored``): the score of an expert, the
+    groups that the selection goes through, and what becomes of the selected
+    scores.  ``groups = 1`` selects among all experts."""
+    score: str = "sigmoid"   # or "softmax"
+    groups: int = 1
+    top_groups: int = 1
+    group_top: int = 1       # a group's value: the sum of its 1 or 2 best
+    renorm: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in ("sigmoid", "softmax"):
+            raise ValueError(f"score: sigmoid or softmax, got {self.score!r}")
+
+    def c(self, bias=None, bias_next=None, bias_rate: float = 0.0) -> moe_scoring:
+        return moe_scoring(MOE_SCORE_SOFTMAX if self.score == "softmax" else MOE_SCORE_SIGMOID, self.groups,
+                           self.top_groups, self.group_top, int(self.renorm), self.scale, bias_rate, bias, bias_next)
+
+
+def _sized(t, dtype, numel: int, name: str, device):
+    """The address of a contiguous tensor of at least `numel` values of this
+    type on `device`; None for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} values, needs {numel}")
+    return t.data_ptr()
+
+
+def _here(t, name: str):
+    """The current CUDA device, where `t` has to be: a launch goes there."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if torch._C._cuda_getDevice() != t.device.index:
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}: make its "
+                         "current (torch.cuda.device)")
+    return t.device
+
+
+def moe_gate_scored(logits, k: int, scoring: Scoring, bias, topk_idx, gates, expert_counts, aux_loss, entropy, ws, *,
+                    bias_next=None, bias_rate: float = 0.0, stream=None) -> None:
+    """Routing by scores; ``aux_loss``, ``entropy`` and ``bias`` may be None.
+    ``bias_next`` [E] (or ``bias`` itself) receives the bias moved by
+    ``bias_rate`` towards balance."""
+    dev = _here(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits: expected [T, E], got {tuple(logits.shape)}")
+    T, E = logits.shape
+    f32 = torch.float32
+    for t, name in ((bias, "bias"), (bias_next, "bias_next")):
+        if t is not None and t.numel() != E:
+            raise ValueError(f"{name}: {t.numel()} values for {E} experts")
+    c = scoring.c(_sized(bias, f32, E, "bias", dev), _sized(bias_next, f32, E, "bias_next", dev), bias_rate)
+    _check(lib().moe_gate_scored(_sized(logits, f32, T * E, "logits", dev), T, E, k, c,
+                                 _sized(topk_idx, torch.int32, T * k, "topk_idx", dev),
+                                 _sized(gates, f32, T * k, "gates", dev),
+                                 _sized(expert_counts, torch.int32, E, "expert_counts", dev),
+                                 _sized(aux_loss, torch.float64, 1, "aux_loss", dev),
+                                 _sized(entropy, torch.float64, 1, "entropy", dev),
+                                 _sized(ws, torch.uint8, 1, "ws", dev), ws.numel(), _stream(stream)),
+           "moe_gate_scored")
+
+
+def moe_gate_scored_backward(logits, topk_idx, d_gates, scoring: Scoring, d_logits, ws, stream=None) -> None:
+    """The gradient of ``moe_gate_scored``'s gates with respect to the logits."""
+    dev = _here(logits, "logits")
+    if logits.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("logits and topk_idx: expected [T, E] and [T, k]")
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    _check(lib().moe_gate_scored_backward(_sized(logits, torch.float32, T * E, "logits", dev),
+                                          _sized(topk_idx, torch.int32, T * k, "topk_idx", dev),
+                                          _sized(d_gates, torch.float32, T * k, "d_gates", dev), T, E, k, scoring.c(),
+                                          _sized(d_logits, torch.float32, T * E, "d_logits", dev),
+                                          _sized(ws, torch.uint8, 1, "ws", dev), ws.numel(), _stream(stream)),
+           "moe_gate_scored_backward")
+
+
+def fp4_pitch(K: int) -> int:
+    """Scale bytes of a row of K values in 4 bits (MOE_FP4_PITCH)."""
+    return (K + 511) // 512 * 16
+
+
+def moe_dispatch_fp4(x, T: int, H: int, layout: "Layout", codes, scales, stream=None) -> None:
+    """moe_dispatch with the packed rows in 4 bits: ``codes`` [r_max, H/2] and
+    ``scales`` [r_max, fp4_pitch(H)], both uint8."""
+    dev = _here(x, "x")
+    r = layout.c.r_max
+    _check(lib().moe_dispatch_fp4(_sized(x, torch.bfloat16, T * H, "x", dev), T, H, ctypes.byref(layout.c),
+                                  _sized(codes, torch.uint8, r * (H // 2), "codes", dev),
+                                  _sized(scales, torch.uint8, r * fp4_pitch(H), "scales", dev), _stream(stream)),
+           "moe_dispatch_fp4")
 
 
 def _check_layout_fits(layout: "Layout", T: int, E: int, k: int, P: int, capacity: int, where: str):

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -91,6 +92,18 @@ inline moe_status check_gate_sizes(int T, int E, int k)
     return k > E ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
+inline moe_status check_scoring(const moe_scoring *S, int E, int k)
+{
+    if (!S || (S->score != MOE_SCORE_SIGMOID && S->score != MOE_SCORE_SOFTMAX)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(S->bias) || !aligned16(S->bias_next)) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(S->scale) || !std::isfinite(S->bias_rate)) return MOE_ERR_INVALID_ARG;
+    if (S->groups < 1 || S->groups > E || E % S->groups != 0) return MOE_ERR_UNSUPPORTED;
+    const int per = E / S->groups;
+    if (S->top_groups < 1 || S->top_groups > S->groups || k > S->top_groups * per) return MOE_ERR_UNSUPPORTED;
+    if (S->group_top < 1 || S->group_top > 2 || S->group_top > per) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
 inline moe_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 }  // namespace
@@ -135,6 +148,38 @@ moe_status moe_gate(const float *logits, int T, int E, int k, int mode, int32_t 
     if (ws_bytes < moe::kWsHeaderBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
     return from_cuda(moe::launch_gate(logits, T, E, k, mode, topk_idx, gates, expert_counts, aux_loss,
                                       entropy, ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_gate_scored(const float *logits, int T, int E, int k, const moe_scoring *S, int32_t *topk_idx,
+                           float *gates, int32_t *expert_counts, double *aux_loss, double *entropy, void *ws,
+                           size_t ws_bytes, moe_stream_t stream)
+{
+    moe_status st = check_gate_sizes(T, E, k);
+    if (st == MOE_OK) st = check_scoring(S, E, k);
+    if (st != MOE_OK) return st;
+    if (!expert_counts || !ws) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!logits || !topk_idx || !gates)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(gates) || !aligned16(ws))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < moe::kWsHeaderBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    return from_cuda(moe::launch_gate_scored(logits, T, E, k, S, topk_idx, gates, expert_counts, aux_loss, entropy, ws,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_gate_scored_backward(const float *logits, const int32_t *topk_idx, const float *d_gates, int T, int E,
+                                    int k, const moe_scoring *S, float *d_logits, void *ws, size_t ws_bytes,
+                                    moe_stream_t stream)
+{
+    moe_status st = check_gate_sizes(T, E, k);
+    if (st == MOE_OK) st = check_scoring(S, E, k);
+    if (st != MOE_OK) return st;
+    if (!ws) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!logits || !topk_idx || !d_gates || !d_logits)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(d_gates) || !aligned16(d_logits) || !aligned16(ws))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < moe::kWsHeaderBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    return from_cuda(moe::launch_gate_scored_backward(logits, topk_idx, d_gates, T, E, k, S, d_logits, ws,
+                                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
 static moe_status dispatch_layout_impl(const int32_t *topk_idx, const int32_t *expert_counts, int T, int E,
@@ -248,6 +293,17 @@ moe_status moe_dispatch(const void *x, int T, int H, const moe_layout *L, int fp
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (fp8 != 0) return from_cuda(moe::launch_dispatch_fp8_grouped(x, T, H, L, fp8, packed, scales, s));
     return from_cuda(moe::launch_dispatch_bf16(x, T, H, L, packed, s));
+}
+
+moe_status moe_dispatch_fp4(const void *x, int T, int H, const moe_layout *L, void *codes, void *scales,
+                            moe_stream_t stream)
+{
+    moe_status st = check_layout(L, T);
+    if (st != MOE_OK) return st;
+    if (H < 32 || H % 32 != 0 || H > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (T > 0 && (!x || !codes || !scales)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_dispatch_fp4(x, T, H, L, codes, scales, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_combine(const void *expert_out, const moe_layout *L, const float *gates,

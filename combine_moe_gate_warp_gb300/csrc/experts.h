@@ -28,4 +28,7 @@ cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const 
                                 int fp32, cudaStream_t s);
 cudaError_t launch_act_backward(const moe_rows *G, const void *dy, int N, int act, const void *saved,
                                 const void *saved_scales, void *du, void *a, cudaStream_t s);
+cudaError_t launch_quantize_fp4(const moe_rows *G, const void *rows, int K, void *codes, void *scales, cudaStream_t s);
+cudaError_t launch_dequantize_fp4(const moe_rows *G, const void *codes, const void *scales, int K, void *rows,
+                                  cudaStream_t s);
 }  // namespace moe

@@ -106,6 +106,28 @@ moe_status moe_act_backward(const moe_rows *G, const void *dy, int N, int act, c
     return from_cuda(moe::launch_act_backward(G, dy, N, act, saved, saved_scales, du, a, stream_of(stream)));
 }
 
+moe_status moe_quantize_fp4(const moe_rows *G, const void *rows, int K, void *codes, void *scales,
+                            moe_stream_t stream)
+{
+    moe_status st = check_rows(G);
+    if (st != MOE_OK) return st;
+    if (!cols_ok(K, 32)) return MOE_ERR_UNSUPPORTED;
+    if (G->rows > 0 && (!rows || !codes || !scales)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(rows) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_quantize_fp4(G, rows, K, codes, scales, stream_of(stream)));
+}
+
+moe_status moe_dequantize_fp4(const moe_rows *G, const void *codes, const void *scales, int K, void *rows,
+                              moe_stream_t stream)
+{
+    moe_status st = check_rows(G);
+    if (st != MOE_OK) return st;
+    if (!cols_ok(K, 32)) return MOE_ERR_UNSUPPORTED;
+    if (G->rows > 0 && (!rows || !codes || !scales)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(rows) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_dequantize_fp4(G, codes, scales, K, rows, stream_of(stream)));
+}
+
 moe_status moe_expert_cut(int product, int e4m3, int rows, int E, int K, int N, int32_t *cut)
 {
     if (!cut || rows < 0 || product < MOE_EXPERT_LINEAR || product > MOE_EXPERT_WGRAD) return MOE_ERR_INVALID_ARG;

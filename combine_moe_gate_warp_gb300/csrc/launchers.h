@@ -11,6 +11,10 @@ namespace moe {
 cudaError_t launch_gate(const float *logits, int T, int E, int k, int mode, int32_t *topk_idx,
                         float *gates, int32_t *expert_counts, double *aux, double *entropy,
                         void *ws, cudaStream_t s);
+cudaError_t launch_gate_scored(const float *logits, int T, int E, int k, const moe_scoring *S, int32_t *idx,
+                               float *gates, int32_t *counts, double *aux, double *ent, void *ws, cudaStream_t s);
+cudaError_t launch_gate_scored_backward(const float *logits, const int32_t *idx, const float *d_gates, int T, int E,
+                                        int k, const moe_scoring *S, float *d_logits, void *ws, cudaStream_t s);
 // gate + dropping layout in one launch; *too_large = 1 (nothing enqueued)
 // when the batch does not fit the fused kernel's grid; with dry_run only
 // that decision is made (nothing is read or launched)
@@ -22,6 +26,8 @@ cudaError_t launch_layout(const int32_t *topk_idx, const int32_t *counts_in, int
                           cudaStream_t s, int reassign = 0);
 cudaError_t launch_dispatch_bf16(const void *x, int T, int H, const moe_layout *L, void *packed,
                                  cudaStream_t s);
+cudaError_t launch_dispatch_fp4(const void *x, int T, int H, const moe_layout *L, void *codes, void *scales,
+                                cudaStream_t s);
 cudaError_t launch_combine(const void *eo, const moe_layout *L, const float *gates,
                            const void *shared, int Ks, int T, int H, void *y, cudaStream_t s);
 cudaError_t launch_dispatch_fp8_grouped(const void *x, int T, int H, const moe_layout *L, int mode, void *packed,

@@ -42,6 +42,21 @@ class SavedLayer:
                           torch.empty((rows, N // SAVED_BLOCK), dtype=torch.uint8, device=device))
 
 
+FP4_BLOCK = 32  # columns that share one scale byte
+
+
+@dataclass
+class Fp4Rows:
+    """Rows [.., K] of values in 4 bits: e2m1 ``codes`` [.., K / 2], two to a
+    byte, the even column in the low half, and one scale byte per 32 columns,
+    ``scales`` [.., fp4_pitch(K)]; a value is e2m1(code) * 2^(byte - 127).
+    Byte 255 marks a block that held a NaN or an infinity.  ``packed`` and
+    ``scales`` of a RoutePlan with ``fp4`` are such rows; weights [E, N, K]
+    come from ``quantize_weights_fp4``."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
 def _act(name: str) -> int:
     try:
         return ACTIVATIONS[name]
@@ -108,6 +123,16 @@ def quantize_weights(w: torch.Tensor):
         s[:, 0] = scale
         s[:, 1] = (q.double().sum(1) * scale.double()).float()
     return codes, scales
+
+
+def quantize_weights_fp4(w: torch.Tensor) -> Fp4Rows:
+    """bf16 weights [E, N, K] (or [N, K]) in 4 bits for products with rows in
+    4 bits, once when a model is loaded."""
+    if w.dim() not in (2, 3):
+        raise ValueError("w: expected a tensor of [E, N, K] or [N, K]")
+    flat = w.reshape(-1, w.shape[-1])
+    q = ExpertRows(rows=flat.shape[0], device=w.device).quantize_fp4(flat)
+    return Fp4Rows(q.codes.view(*w.shape[:-1], -1), q.scales.view(*w.shape[:-1], -1))
 
 
 class ExpertRows:
@@ -333,6 +358,41 @@ class ExpertRows:
         out, op = self._out_rows(out, N, "out")
         abi._check(self._lib.moe_act_backward(self._ref, dp, N, code, sc, ss, op, ap, self._stream()),
                    "moe_act_backward")
+        return out
+
+    # ------------------------------------------------------------------
+    def _fp4(self, q, K, name):
+        if not isinstance(q, Fp4Rows):
+            raise TypeError(f"{name}: expected Fp4Rows")
+        return (_check_rows(q.codes, torch.uint8, self.rows, K // 2, f"{name}.codes", self.device),
+                _check_rows(q.scales, torch.uint8, self.rows, abi.fp4_pitch(K), f"{name}.scales", self.device))
+
+    def new_fp4(self, K: int) -> Fp4Rows:
+        if K < FP4_BLOCK or K % FP4_BLOCK:
+            raise ValueError(f"columns in 4 bits are a multiple of {FP4_BLOCK}, got {K}")
+        return Fp4Rows(self._new((self.rows, K // 2), torch.uint8),
+                       self._new((self.rows, abi.fp4_pitch(K)), torch.uint8))
+
+    def quantize_fp4(self, x, *, out: Fp4Rows | None = None) -> Fp4Rows:
+        """The rows x [rows, K] bf16 in 4 bits, as the dispatch in 4 bits
+        packs them."""
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x: expected a tensor of [rows, K]")
+        K = _columns(x.shape[1], "x")
+        xp = _check_rows(x, torch.bfloat16, self.rows, K, "x", self.device)
+        if out is None:
+            out = self.new_fp4(K)
+        cp, sp = self._fp4(out, K, "out")
+        abi._check(self._lib.moe_quantize_fp4(self._ref, xp, K, cp, sp, self._stream()), "moe_quantize_fp4")
+        return out
+
+    def dequantize_fp4(self, x: Fp4Rows, *, out=None):
+        """Rows in 4 bits as bf16 [rows, K], which holds every value exactly:
+        for a weight gradient, or any product that takes bf16."""
+        K = 2 * _columns(x.codes.shape[-1], "x.codes")
+        cp, sp = self._fp4(x, K, "x")
+        out, op = self._out_rows(out, K, "out")
+        abi._check(self._lib.moe_dequantize_fp4(self._ref, cp, sp, K, op, self._stream()), "moe_dequantize_fp4")
         return out
 
     def linear_backward(self, dy, x, w, *, act: str = "none", saved: SavedLayer | None = None, bias: bool = False,

@@ -27,6 +27,8 @@ class RouteShape:
     capacity: int = 0
     fp8_combine: int = 0  # expert outputs: 0 bf16, else quantised with this MOE_FP8_* mode
     reassign: bool = False  # capacity overflow re-assigned to the least-loaded expert (not dropped)
+    scoring: abi.Scoring | None = None  # routing by scores (moe_gate_scored) instead of `mode`'s softmax gates
+    fp4: bool = False     # dispatch transport in 4 bits (moe_dispatch_fp4) instead of `fp8`'s
 
 
 def _check_input(t, dtype, shape, name):
@@ -60,6 +62,10 @@ class RoutePlan:
         # gate and layout may run on their own stream (see RoutePipeline)
         self.route_stream = self.stream if route_stream is None else route_stream
         T, E, k = s.T, s.E, s.k
+        if s.fp4 and s.fp8:
+            raise ValueError("fp4 and fp8 are two transports of one dispatch")
+        if s.fp4 and (s.H < 32 or s.H % 32):
+            raise ValueError(f"fp4: H is a multiple of 32, got {s.H}")
         i32 = dict(dtype=torch.int32, device=self.device)
         self.topk_idx = torch.empty((max(T, 1), k), **i32)
         self.gates = torch.empty((max(T, 1), k), dtype=torch.float32, device=self.device)
@@ -70,7 +76,10 @@ class RoutePlan:
         self.layout = abi.Layout(T, E, k, s.P, s.capacity, self.device)
         self.r_max = self.layout.r_max
         rows = max(self.r_max, 1)
-        if s.fp8:
+        if s.fp4:
+            self.packed = torch.empty((rows, s.H // 2), dtype=torch.uint8, device=self.device)
+            self.scales = torch.empty((rows, abi.fp4_pitch(s.H)), dtype=torch.uint8, device=self.device)
+        elif s.fp8:
             self.packed = torch.empty((rows, s.H), dtype=torch.uint8, device=self.device)
             self.scales = torch.empty((rows, 2), dtype=torch.float32, device=self.device)
         else:
@@ -100,25 +109,44 @@ class RoutePlan:
                             self.expert_counts.data_ptr(), self.aux_loss.data_ptr(), self.entropy.data_ptr(),
                             self._Lref, self.ws.data_ptr(), self._ws_bytes, self._sr)
         # moe_route (gate + layout, one launch where the batch allows) unless
-        # the overflow is re-assigned
-        self.fused_route = not s.reassign
+        # the overflow is re-assigned or the gate is one by scores
+        self.fused_route = not s.reassign and s.scoring is None
         self._scales_ptr = None if self.scales is None else self.scales.data_ptr()
 
     # the four hot-path calls -------------------------------------------------
-    def gate(self, logits: torch.Tensor):
+    def gate(self, logits: torch.Tensor, bias=None, *, bias_next=None, bias_rate: float = 0.0):
+        """The gate of one batch.  With ``scoring``: by scores, ``bias`` [E]
+        added for the selection, and ``bias_next`` [E] (or ``bias`` itself)
+        receiving the bias moved by ``bias_rate`` towards balance."""
         s = self.shape
         _check_input(logits, torch.float32, (s.T, s.E), "logits")
-        abi._check(self._lib.moe_gate(logits.data_ptr(), s.T, s.E, s.k, s.mode, *self._gate_tail), "moe_gate")
+        if s.scoring is None:
+            if bias is not None or bias_next is not None:
+                raise ValueError("bias: only with scoring")
+            abi._check(self._lib.moe_gate(logits.data_ptr(), s.T, s.E, s.k, s.mode, *self._gate_tail), "moe_gate")
+            return
+        for t, name in ((bias, "bias"), (bias_next, "bias_next")):
+            if t is not None:
+                _check_input(t, torch.float32, (s.E,), name)
+                if t.device != logits.device:
+                    raise ValueError(f"{name}: on {t.device}, the logits are on {logits.device}")
+        c = s.scoring.c(None if bias is None else bias.data_ptr(), None if bias_next is None else bias_next.data_ptr(),
+                        bias_rate)
+        abi._check(self._lib.moe_gate_scored(logits.data_ptr(), s.T, s.E, s.k, c, *self._gate_tail),
+                   "moe_gate_scored")
 
-    def route(self, logits: torch.Tensor):
-        """The routing of one batch: moe_route, or moe_gate and then the
-        layout call when the capacity overflow is re-assigned."""
+    def route(self, logits: torch.Tensor, bias=None, *, bias_next=None, bias_rate: float = 0.0):
+        """The routing of one batch: moe_route, or the gate (see ``gate``) and
+        then the layout call where the gate is one by scores or the capacity
+        overflow is re-assigned."""
         s = self.shape
         if self.fused_route:
+            if bias is not None or bias_next is not None:
+                raise ValueError("bias: only with scoring")
             _check_input(logits, torch.float32, (s.T, s.E), "logits")
             abi._check(self._lib.moe_route(logits.data_ptr(), *self._route_tail), "moe_route")
             return
-        self.gate(logits)
+        self.gate(logits, bias, bias_next=bias_next, bias_rate=bias_rate)
         self.dispatch_layout()
 
     def dispatch_layout(self):
@@ -130,6 +158,10 @@ class RoutePlan:
     def dispatch(self, x: torch.Tensor):
         s = self.shape
         _check_input(x, torch.bfloat16, (s.T, s.H), "x")
+        if s.fp4:
+            abi._check(self._lib.moe_dispatch_fp4(x.data_ptr(), s.T, s.H, self._Lref, self.packed.data_ptr(),
+                                                  self._scales_ptr, self._s), "moe_dispatch_fp4")
+            return
         abi._check(self._lib.moe_dispatch(x.data_ptr(), s.T, s.H, self._Lref, int(s.fp8), self.packed.data_ptr(),
                                           self._scales_ptr, self._s), "moe_dispatch")
 
@@ -163,10 +195,10 @@ class RoutePlan:
                                              self.gates.data_ptr(), sh, s.Ks, s.T, s.H, self.y.data_ptr(), self._s),
                    "moe_combine_fp8")
 
-    def step(self, logits, x, expert_out, shared_out=None):
+    def step(self, logits, x, expert_out, shared_out=None, bias=None):
         """route (gate + layout) -> dispatch -> combine; with FP8 expert
         outputs the combine is quantise (expert side) -> FP8 combine."""
-        self.route(logits)
+        self.route(logits, bias)
         self.dispatch(x)
         if self.shape.fp8_combine:
             self.quantize_expert_out(expert_out)
@@ -219,6 +251,11 @@ class RoutePlan:
         _check_input(logits, torch.float32, (s.T, s.E), "logits")
         dg = self.d_gates[:s.T] if d_gates is None else d_gates
         _check_input(dg, torch.float32, (s.T, s.k), "d_gates")
+        if s.scoring is not None:
+            abi._check(self._lib.moe_gate_scored_backward(
+                logits.data_ptr(), self.topk_idx.data_ptr(), dg.data_ptr(), s.T, s.E, s.k, s.scoring.c(),
+                self.d_logits.data_ptr(), self.ws.data_ptr(), self._ws_bytes, self._s), "moe_gate_scored_backward")
+            return
         abi._check(self._lib.moe_gate_backward(logits.data_ptr(), self.topk_idx.data_ptr(), dg.data_ptr(), s.T, s.E,
                                                s.k, s.mode, self.d_logits.data_ptr(), self.ws.data_ptr(),
                                                self._ws_bytes, self._s), "moe_gate_backward")
@@ -242,7 +279,8 @@ class RouteGraph:
     For small batches the host cost of the step's foreign calls (one per
     kernel) exceeds the kernels' own time; a replay submits every kernel of
     the step in one launch.  The graph reads its inputs from fixed buffers
-    (``logits``, ``x``, ``expert_out`` [r_max, H], ``shared_out``) and leaves
+    (``logits``, ``x``, ``expert_out`` [r_max, H], ``shared_out``, and with
+    scoring ``bias``, zeros until one is given) and leaves
     its results in ``plan`` exactly as ``RoutePlan.step`` does; ``step``
     copies new inputs in and replays.  The graph runs on its own stream;
     ``step`` orders it after the caller's current stream and the caller's
@@ -260,6 +298,7 @@ class RouteGraph:
         self.x = torch.zeros((s.T, s.H), **bf16)
         self.expert_out = torch.zeros((max(p.r_max, 1), s.H), **bf16)
         self.shared_out = torch.zeros((s.Ks, s.T, s.H), **bf16) if s.Ks else None
+        self.bias = None if s.scoring is None else torch.zeros(s.E, dtype=torch.float32, device=self.device)
         self.graph = None
         if s.T == 0:
             return  # nothing to launch: step() is a no-op
@@ -275,7 +314,7 @@ class RouteGraph:
             self._calls()
 
     def _calls(self):
-        self.plan.step(self.logits, self.x, self.expert_out, self.shared_out)
+        self.plan.step(self.logits, self.x, self.expert_out, self.shared_out, self.bias)
 
     def replay(self):
         """Replay on the graph's stream (inputs already in the buffers)."""
@@ -284,13 +323,15 @@ class RouteGraph:
         with torch.cuda.stream(self.stream):
             self.graph.replay()
 
-    def step(self, logits=None, x=None, expert_out=None, shared_out=None) -> RoutePlan:
+    def step(self, logits=None, x=None, expert_out=None, shared_out=None, bias=None) -> RoutePlan:
         """Copy the given inputs into the graph's buffers and replay; returns
         the plan holding the results."""
+        if bias is not None and self.bias is None:
+            raise ValueError("bias: only with scoring")
         cur = torch.cuda.current_stream(self.device)
         self.stream.wait_stream(cur)
         with torch.cuda.stream(self.stream):
-            for src, dst in ((logits, self.logits), (x, self.x), (shared_out, self.shared_out)):
+            for src, dst in ((logits, self.logits), (x, self.x), (shared_out, self.shared_out), (bias, self.bias)):
                 if src is not None:
                     dst.copy_(src, non_blocking=True)
             if expert_out is not None:
@@ -373,7 +414,7 @@ class RoutePipeline:
             self.data_stream.wait_stream(st)
         ev.record(self.data_stream)
 
-    def step(self, logits, x, expert_out, shared_out=None, out=None, stats_out=None) -> RoutePlan:
+    def step(self, logits, x, expert_out, shared_out=None, out=None, stats_out=None, bias=None) -> RoutePlan:
         """Enqueue one batch; returns the plan whose buffers (y, layout,
         statistics) hold its results once the data stream reaches this
         point, until the plan is reused len(plans) steps later.  With `out`
@@ -386,7 +427,7 @@ class RoutePipeline:
         d = i % len(self.plans)
         p = self.plans[d]
         self.route_stream.wait_event(self._done[d])
-        p.route(logits)
+        p.route(logits, bias)
         self._routed[d].record(self.route_stream)
         p.stream.wait_event(self._routed[d])
         p.dispatch(x)

@@ -111,6 +111,18 @@ moe_status moe_act_backward(const moe_rows *G, const void *dy, int N, int act, c
                             const void *saved_scales, void *du, void *a, moe_stream_t stream);
 
 /*
+ * moe_quantize_fp4, moe_dequantize_fp4 -- the experts' rows in 4 bits, as
+ * moe_dispatch_fp4 packs them, from bf16 and back (exactly: bf16 holds every
+ * value of the format).  Weights [E, N, K] are E * N rows of one group.
+ *   rows [rows, K] bf16, K % 32 == 0; codes [rows, K/2] uint8; scales
+ *   [rows, MOE_FP4_PITCH(K)] uint8.
+ */
+moe_status moe_quantize_fp4(const moe_rows *G, const void *rows, int K, void *codes, void *scales,
+                            moe_stream_t stream);
+moe_status moe_dequantize_fp4(const moe_rows *G, const void *codes, const void *scales, int K, void *rows,
+                              moe_stream_t stream);
+
+/*
  * moe_expert_cut -- how the product of these sizes is cut on the current
  * device, for tests and for tuning; nothing is launched.
  *   cut  out [3], on the host: SMs of a tile (2: a pair), packed rows per

@@ -144,6 +144,49 @@ moe_status moe_gate(const float *logits, int T, int E, int k, int mode,
                     void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
+ * moe_gate_scored -- routing by scores, with a bias for balance and groups
+ * of experts.  For each token t:
+ *     s_e = 1 / (1 + exp(-l_e))            MOE_SCORE_SIGMOID
+ *     s_e = exp(l_e) / sum_i exp(l_i)      MOE_SCORE_SOFTMAX (over all E)
+ *     v_e = s_e + bias_e                   for the selection only
+ *   The experts form `groups` groups of E / groups consecutive ids.  A
+ *   group's value is the sum of its group_top (1 or 2) largest v; the
+ *   top_groups groups with the largest values are kept (equal values: the
+ *   lower group), and of their experts the k with the largest v (equal
+ *   values: the lower id), value descending.
+ *     gates_j = s[sel_j] * scale                                      or, with renorm,
+ *     gates_j = s[sel_j] / (sum_i s[sel_i] + 1e-20) * scale
+ *   The selection is that of s and v in fp64, whatever their distance; the
+ *   gates are evaluated in fp32.
+ *
+ *   logits, topk_idx, gates, expert_counts, ws: as moe_gate.  A logit or
+ *                 bias that is not finite is recorded as
+ *                 MOE_ERR_DEVICE_DATA (the ids stay in [0, E)).
+ *   aux_loss, entropy  out [1] fp64 as moe_gate, or NULL.
+ *   S->bias       [E] fp32, or NULL (zeros).
+ *   S->bias_next  out [E] fp32, or NULL: the bias for the next batch,
+ *                 bias_e + bias_rate if expert e got fewer than T*k / E
+ *                 assignments, bias_e - bias_rate if it got more, bias_e if
+ *                 exactly as many.  May be S->bias itself.
+ * groups divides E, k <= top_groups * (E / groups), group_top <= E / groups.
+ */
+#define MOE_SCORE_SIGMOID 0
+#define MOE_SCORE_SOFTMAX 1
+typedef struct moe_scoring {
+    int32_t score;
+    int32_t groups, top_groups, group_top;  /* 1, 1, 1: no groups */
+    int32_t renorm;
+    float scale;
+    float bias_rate;
+    const float *bias; /* device */
+    float *bias_next;  /* device */
+} moe_scoring;
+moe_status moe_gate_scored(const float *logits, int T, int E, int k, const moe_scoring *S,
+                           int32_t *topk_idx, float *gates, int32_t *expert_counts,
+                           double *aux_loss, double *entropy,
+                           void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
  * moe_dispatch_layout -- per-expert and per-partition counts, prefix
  * offsets and the stable permutation.  [P4] sec. 7 "Dispatch" detail
  * (reorder by target expert id, pack same-destination tokens
@@ -293,6 +336,27 @@ moe_status moe_dispatch_layout_reassign(const int32_t *topk_idx, const int32_t *
  */
 moe_status moe_dispatch(const void *x, int T, int H, const moe_layout *L, int fp8,
                         void *packed, float *scales, moe_stream_t stream);
+
+/*
+ * moe_dispatch_fp4 -- moe_dispatch with the rows in 4 bits: values of 32
+ * consecutive columns (a block) share a power of two.
+ *
+ *   x           [T, H] bf16, H % 32 == 0, H <= 2^20.
+ *   codes   out [r_max, H/2] uint8: two codes to a byte, the even column in
+ *               the low half.  A code is sign (bit 3), exponent (bits 2-1,
+ *               bias 1) and fraction (bit 0): 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   scales  out [r_max, MOE_FP4_PITCH(H)] uint8: one byte a block, the
+ *               power of two 2^(byte - 127); the bytes past H/32 are zero.
+ *   2^X is the smallest power of two, not below 2^-127, with max |x| <=
+ *   6 * 2^X, code = x / 2^X rounded to nearest, ties to the even code.  A
+ *   block with a NaN or an infinity has byte 255 (and codes 7) and decodes
+ *   as NaN; values from 1.75 * 2^127 up may decode as infinity.
+ *   Rows >= R are not written.  dst_row entries >= R are recorded as
+ *   MOE_ERR_DEVICE_DATA and skipped.
+ */
+#define MOE_FP4_PITCH(K) (((K) + 511) / 512 * 16)
+moe_status moe_dispatch_fp4(const void *x, int T, int H, const moe_layout *L, void *codes, void *scales,
+                            moe_stream_t stream);
 
 /*
  * moe_combine -- gather the expert outputs back into token order and
@@ -465,6 +529,21 @@ moe_status moe_dispatch_backward(const void *d_packed, const moe_layout *L, int 
 moe_status moe_gate_backward(const float *logits, const int32_t *topk_idx, const float *d_gates,
                              int T, int E, int k, int mode, float *d_logits,
                              void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_gate_scored_backward -- gradient of moe_gate_scored's gates with
+ * respect to the logits, the scores recomputed from them in fp32.  Selection,
+ * bias and counts carry no gradient; of S only score, renorm and scale enter.
+ *   topk_idx      [T, k] int32 (ids outside [0, E) are recorded as
+ *                 MOE_ERR_DEVICE_DATA and their slots ignored; an id that
+ *                 comes twice gets both slots' gradients).
+ *   d_gates       [T, k] fp32.
+ *   d_logits  out [T, E] fp32.
+ *   ws, ws_bytes  as moe_gate_backward.
+ */
+moe_status moe_gate_scored_backward(const float *logits, const int32_t *topk_idx, const float *d_gates,
+                                    int T, int E, int k, const moe_scoring *S, float *d_logits,
+                                    void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Synchronise `stream`, return the device status recorded in `ws` since the
  * last call (MOE_OK if none) and clear it. */
