@@ -172,6 +172,8 @@ def lib():
     L.moe_quantize_fp4.restype = I
     L.moe_dequantize_fp4.argtypes = [G, P, P, I, P, P]
     L.moe_dequantize_fp4.restype = I
+    L.moe_expert_linear_fp4.argtypes = [G, P, P, I, P, P, I, P, I, P, P, P]
+    L.moe_expert_linear_fp4.restype = I
     L.moe_get_status.argtypes = [P, P]
     L.moe_get_status.restype = I
     L.moe_status_string.argtypes = [I]

@@ -55,6 +55,10 @@ constexpr int kTileM = 128;            // rows of A per block
 constexpr int kStageA = kTileM * 128;  // bytes
 
 constexpr int kLinear = 0, kDgrad = 1, kWgrad = 2, kDgradSaved = 3;
+// what the operands are: bf16, e4m3 (whose scales the epilogue applies), or
+// e2m1 with a power of two for 32 values of k, which the matrix instructions
+// apply (linear only)
+constexpr int kBf16 = 0, kE4m3 = 1, kFp4 = 2;
 
 // accumulator columns (packed rows) that an epilogue group takes at a time
 __host__ __device__ constexpr int chunk(int MODE) { return MODE == kDgradSaved ? 16 : 32; }
@@ -67,31 +71,49 @@ constexpr int kOutBytes = 32 * kPitch;
 constexpr int kCodeBytes = 32 * kPitchCode;
 constexpr int kOnes = 2048;          // wgrad: the bias sums' ones, then
 constexpr int kDwBytes = 32 * 32 * 2;  // for each epilogue warp 32 rows of 32 values of dw
-__host__ __device__ constexpr int group_bytes(int MODE)
+__host__ __device__ constexpr int group_bytes(int MODE, int KIND)
 {
-    return MODE == kWgrad        ? kOnes / 2 + 4 * kDwBytes
+    return KIND == kFp4          ? kOutBytes
+           : MODE == kWgrad      ? kOnes / 2 + 4 * kDwBytes
            : MODE == kDgradSaved ? 3 * 16 * kPitch + 2 * 16 * kPitchCode + 512
                                  : kOutBytes + kCodeBytes + 256 + 1024 + 512;
 }
 constexpr int kControl = 4096;
 
-__host__ __device__ constexpr int stage_bytes(int CG, int BN) { return kStageA + BN / CG * 128; }
+// kFp4: a stage's scales, as tensor memory takes them: 512 bytes for 128 rows
+// and 128 values of k (lane i: rows i, i + 32, i + 64, i + 96, 4 bytes each);
+// A's 128 rows, and all of B's rows in both blocks of a pair
+constexpr int kScaleAtom = 512;
+__host__ __device__ constexpr int scale_atoms(int BN) { return (BN + 127) / 128; }
+__host__ __device__ constexpr int scale_bytes(int BN) { return 2 * (1 + scale_atoms(BN)) * kScaleAtom; }
+__host__ __device__ constexpr int stage_bytes(int CG, int BN, int KIND)
+{
+    return kStageA + BN / CG * 128 + (KIND == kFp4 ? scale_bytes(BN) : 0);
+}
 // the other blocks' sums of a tile whose k is split over a cluster
 __host__ __device__ constexpr int join_bytes(bool SPLIT, int BN) { return SPLIT ? BN * kTileM * 4 : 0; }
 // ring depth: what is left of 227 KB beside the epilogue, the barriers and tile
 // counts, and the alignment to 1 KB; at most 12 stages
-__host__ __device__ constexpr int stages(int CG, int BN, int MODE, bool SPLIT)
+__host__ __device__ constexpr int stages(int CG, int BN, int MODE, int KIND, bool SPLIT)
 {
-    const int n =
-        (227 * 1024 - 2 * group_bytes(MODE) - join_bytes(SPLIT, BN) - kControl - 1024) / stage_bytes(CG, BN);
+    const int n = (227 * 1024 - 2 * group_bytes(MODE, KIND) - join_bytes(SPLIT, BN) - kControl - 1024) /
+                  stage_bytes(CG, BN, KIND);
     return n > 12 ? 12 : n;
 }
-__host__ __device__ constexpr int smem_bytes(int CG, int BN, int MODE, bool SPLIT)
+__host__ __device__ constexpr int smem_bytes(int CG, int BN, int MODE, int KIND, bool SPLIT)
 {
-    return 1024 + stages(CG, BN, MODE, SPLIT) * stage_bytes(CG, BN) + 2 * group_bytes(MODE) + join_bytes(SPLIT, BN) +
-           kControl;
+    return 1024 + stages(CG, BN, MODE, KIND, SPLIT) * stage_bytes(CG, BN, KIND) + 2 * group_bytes(MODE, KIND) +
+           join_bytes(SPLIT, BN) + kControl;
 }
-__host__ __device__ constexpr int tmem_cols(int BN) { return 2 * BN < 32 ? 32 : 2 * BN; }
+// Tensor memory: two accumulators, and for kFp4 two sets of a stage's scales
+// (4 columns an atom) behind them: the next stage's are brought while the
+// products that read the last one's may still be queued.
+__host__ __device__ constexpr int scale_cols(int BN) { return 8 * (1 + scale_atoms(BN)); }
+__host__ __device__ constexpr int tmem_cols(int BN, int KIND)
+{
+    const int need = 2 * BN + (KIND == kFp4 ? 2 * scale_cols(BN) : 0);
+    return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+}
 
 struct Params {
     CUtensorMap ma, mb, mb32, mo;  // mb32: 32 rows of B at a time, for an expert's last tile; mo: bf16 dw
@@ -108,6 +130,8 @@ struct Params {
     int split;     // blocks that share a tile's k (a cluster of 2, 4 or 8), or 1
     const __nv_bfloat16 *bias, *residual;
     const float2 *x_scales, *w_scales;
+    const uint8_t *x_bytes, *w_bytes;  // kFp4: scale bytes of rows and weights
+    int pitch, valid_scales;           // their bytes per row, and how many hold scales
     __nv_bfloat16 *y, *a;
     void *dw, *db;
     uint8_t *saved, *saved_scales;
@@ -260,8 +284,9 @@ __device__ __forceinline__ void place(const uint4 *v, unsigned char *s, int pitc
 // bias, weight scale and activation need no memory in the loop.  Results go
 // through shared memory as bf16 and leave in whole row segments.
 // --------------------------------------------------------------------------
-template <bool FP8>
+template <int KIND>
 struct LinearEpilogue {
+    static constexpr bool FP8 = KIND == kE4m3;
     const Params &p;
     unsigned char *out, *codes;
     float2 *xs;
@@ -575,23 +600,50 @@ __device__ __forceinline__ void store_tile(const Params &p, unsigned char *buf, 
 }
 
 // --------------------------------------------------------------------------
+// kFp4: one warp brings an operand's scale bytes to the stages.  Its lane i
+// reads 8 bytes (256 values of k) of the rows i, i + 32, .. of a tile, kSets
+// stages ahead of their use, and stores those of 4 rows with one 16-byte store
+// as tensor memory takes them: the rows' scales lie in row order, and no copy
+// engine turns 4-byte pieces around.
+// --------------------------------------------------------------------------
+template <int ROWS, typename Next, typename Put>
+__device__ __forceinline__ void feed_scales(const Next &next, const Put &put)
+{
+    constexpr int kSets = 4;
+    uint2 v[kSets][ROWS];
+    bool have[kSets];
+#pragma unroll
+    for (int d = 0; d < kSets; ++d) have[d] = next(v[d]);
+    for (;;) {
+#pragma unroll
+        for (int d = 0; d < kSets; ++d) {
+            if (!have[d] || !put(v[d])) return;
+            have[d] = next(v[d]);
+        }
+    }
+}
+
+// --------------------------------------------------------------------------
 // the kernel
 // --------------------------------------------------------------------------
-template <int CG, int BN, int MODE, bool FP8, bool SPLIT>
+template <int CG, int BN, int MODE, int KIND, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ Params p)
 {
-    constexpr int kStages = stages(CG, BN, MODE, SPLIT);
-    constexpr int kStage = stage_bytes(CG, BN);
+    constexpr bool FP8 = KIND == kE4m3, FP4 = KIND == kFp4;
+    constexpr int kStages = stages(CG, BN, MODE, KIND, SPLIT);
+    constexpr int kStage = stage_bytes(CG, BN, KIND);
+    constexpr int kGroup = group_bytes(MODE, KIND);
+    constexpr int kScales = kStageA + BN / CG * 128;  // kFp4: where a stage's scales start
     constexpr int kBM = kTileM * CG;
     constexpr bool kMnA = MODE != kLinear, kMnB = MODE == kWgrad;
     constexpr int kStepN = MODE == kWgrad ? 64 * CG : CG == 2 ? 32 : 16;
-    constexpr int kElems = FP8 ? 128 : 64;  // values of k per stage
+    constexpr int kElems = KIND == kBf16 ? 64 : 128;  // k of a stage, in units of the tensor maps
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char *stg = smem + kStages * kStage;
-    float *join = reinterpret_cast<float *>(stg + 2 * group_bytes(MODE));
-    Control *c = reinterpret_cast<Control *>(stg + 2 * group_bytes(MODE) + join_bytes(SPLIT, BN));
+    float *join = reinterpret_cast<float *>(stg + 2 * kGroup);
+    Control *c = reinterpret_cast<Control *>(stg + 2 * kGroup + join_bytes(SPLIT, BN));
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     static_assert(CG == 1 || !SPLIT, "a pair does not share its k");
@@ -610,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     if (tid == 0) {
         const unsigned skip = blockIdx.x == 0 ? *(volatile unsigned *)&header->inject_skip_load : 0u;
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&c->full[i], 1);
+            mbar_init(&c->full[i], FP4 ? 1 + 2 * CG : 1);  // the copies, and two warps' scales from each block
             mbar_init(&c->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -627,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         tmap_prefetch(&p.ma);
         tmap_prefetch(&p.mb);
     }
-    if (warp == 2) tmem_alloc<CG>(&c->tmem, tmem_cols(BN));
+    if (warp == 2) tmem_alloc<CG>(&c->tmem, tmem_cols(BN, KIND));
     if (MODE == kWgrad && tid < 128) {
         // the bias sums' B operand: 2 KB of bf16 ones (any layout of them is the same)
         reinterpret_cast<uint4 *>(stg)[tid] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
@@ -806,8 +858,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             const uint64_t da0 = smem_desc(smem_addr(smem), kLeadA, 1024);
             const uint64_t db0 = smem_desc(smem_addr(smem) + kStageA, kLeadB, 1024);
             const uint64_t ones = smem_desc(smem_addr(stg), kLeadB, 1024);
+            const uint64_t ds0 = scale_desc(smem_addr(smem) + kScales);
             const bool one = elect_one();
-            int s = 0, acc = 0;
+            int s = 0, acc = 0, set = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true, ready = false, more = walk.next(t);
             while (more) {
@@ -816,8 +869,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     more = walk.next(t);
                     continue;
                 }
-                const uint32_t idesc = mma_idesc(FP8, kMnA, kMnB, kBM, width(t));
+                const uint32_t idesc =
+                    FP4 ? mma_idesc_fp4(kBM, width(t)) : mma_idesc(FP8, kMnA, kMnB, kBM, width(t));
                 const uint32_t d = tmem + acc * BN;
+                const bool wide = FP4 && width(t) > 128;
                 const bool bias = is_bias(t);
                 // the steps of 16 rows that a tail fills, the stage's last
                 const int last_steps = MODE == kWgrad && span(t).last ? ((t.rows & 63) + 15) / 16 : 0;
@@ -837,12 +892,33 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     const uint64_t da = da0 + (uint64_t)(now * (kStage >> 4)), db = db0 + (uint64_t)(now * (kStage >> 4));
                     const int from = MODE == kWgrad && last_steps != 0 && i == iters - 1 ? 4 - last_steps : 0;
                     if (one) {
+                        if constexpr (FP4) {
+                            // the scales to tensor memory, then four products of
+                            // 64 values of k; two of them share the scales of 128
+                            const uint32_t sfa = tmem + 2 * BN + set * scale_cols(BN), sfb = sfa + 8;
+                            const uint64_t ds = ds0 + (uint64_t)(now * (kStage >> 4));
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (MODE != kWgrad || k >= from)
-                                mma_ss<CG, FP8>(d, da + k * kStepA, bias ? ones : db + k * kStepB, idesc, i != 0 || k != from);
+                            for (int w = 0; w < 2; ++w) {
+                                scales_to_tmem<CG>(sfa + w * 4, ds + w * (kScaleAtom >> 4));
+#pragma unroll
+                                for (int h = 0; h < scale_atoms(BN); ++h)
+                                    if (h == 0 || wide)
+                                        scales_to_tmem<CG>(sfb + (w * scale_atoms(BN) + h) * 4,
+                                                           ds + (2 + w * scale_atoms(BN) + h) * (kScaleAtom >> 4));
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_fp4<CG>(d, da + k * kStepA, db + k * kStepB, idesc | mma_scale_id(k & 1),
+                                            sfa + (k >> 1) * 4, sfb + (k >> 1) * (4 * scale_atoms(BN)), i != 0 || k != 0);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (MODE != kWgrad || k >= from)
+                                    mma_ss<CG, FP8>(d, da + k * kStepA, bias ? ones : db + k * kStepB, idesc, i != 0 || k != from);
+                        }
                         mma_commit<CG>(&c->empty[now]);
                     }
+                    set ^= 1;
                     __syncwarp();
                     if (i == 0) more = walk.next(t);  // the divisions of the next tile hide behind this one
                     ready = __all_sync(0xFFFFFFFFu, next);
@@ -855,6 +931,78 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             }
         }
         __syncwarp();
+    } else if (FP4 && (warp == 2 || warp == 3)) {
+        // ---- scales ---------------------------------------------------------
+        // Warp 2 has A's, warp 3 B's.  What lies past the last row or the
+        // last 32 values of k is zero.
+        const auto feed = [&](auto is_b) {
+            constexpr bool B = decltype(is_b)::value;
+            constexpr int kRows = B ? 4 * scale_atoms(BN) : 4;
+            const uint8_t *at[kRows] = {};
+            const int valid = p.valid_scales;  // bytes of a row that hold scales
+            int i = 0, end = 0, s = 0;
+            uint32_t ph = 1;
+            const auto next = [&](uint2(&v)[kRows]) {
+                while (i == end) {
+                    if (!walk.next(t)) return false;
+                    const Span part = span(t);
+                    i = part.first;
+                    end = part.first + part.count;
+                    const int m0 = t.m * kBM + (int)rank * kTileM, n0 = t.n * p.bn;
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        const int row = r * 32 + lane;
+                        if (B) {
+                            at[r] = row < min(p.bn, t.rows - n0) ? p.x_bytes + (size_t)(t.row0 + n0 + row) * p.pitch
+                                                                 : nullptr;
+                        } else {
+                            // glu: A's rows alternate gate and up columns
+                            const int half = p.glu ? p.M / 2 : p.M, col = p.glu ? (m0 + row) / 2 : m0 + row;
+                            at[r] = col < half ? p.w_bytes + ((size_t)t.e * p.M + (p.glu ? (row & 1) * half : 0) + col) *
+                                                                 p.pitch
+                                               : nullptr;
+                        }
+                    }
+                }
+                const int left = valid - i * 8;  // < 8: the last stage
+                const uint2 keep = left >= 8 ? make_uint2(~0u, ~0u)
+                                             : make_uint2(left >= 4 ? ~0u : (1u << (8 * left)) - 1u,
+                                                          left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1u);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    v[r] = at[r] ? __ldg(reinterpret_cast<const uint2 *>(at[r] + i * 8)) : make_uint2(0u, 0u);
+                    v[r].x &= keep.x;
+                    v[r].y &= keep.y;
+                }
+                ++i;
+                return true;
+            };
+            const auto put = [&](const uint2(&v)[kRows]) {
+                if (!wait(&c->empty[s], ph, c, p.ws)) return false;
+                unsigned char *to = smem + s * kStage + kScales + (B ? 2 * kScaleAtom : 0) + lane * 16;
+#pragma unroll
+                for (int h = 0; h < kRows / 4; ++h) {
+                    *reinterpret_cast<uint4 *>(to + h * kScaleAtom) =
+                        make_uint4(v[4 * h].x, v[4 * h + 1].x, v[4 * h + 2].x, v[4 * h + 3].x);
+                    *reinterpret_cast<uint4 *>(to + (kRows / 4 + h) * kScaleAtom) =
+                        make_uint4(v[4 * h].y, v[4 * h + 1].y, v[4 * h + 2].y, v[4 * h + 3].y);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2) mbar_arrive_release_cluster(cluster_addr(&c->full[s], 0));
+                    else mbar_arrive(&c->full[s]);
+                }
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                return true;
+            };
+            feed_scales<kRows>(next, put);
+        };
+        if (warp == 2) feed(std::false_type());
+        else feed(std::true_type());
     } else if (warp >= kEpiWarp) {
         // ---- epilogue ------------------------------------------------------
         // Two groups of four warps take the chunks of a tile in turn.
@@ -863,8 +1011,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         unsigned char *const dw_tile = stg + kOnes + (warp - kEpiWarp) * kDwBytes;  // wgrad
         int acc = 0, turn = 0;
         uint32_t aph = 0;
-        using Epilogue = std::conditional_t<MODE == kDgradSaved, SavedEpilogue, LinearEpilogue<FP8>>;
-        Epilogue ep(p, stg + g * group_bytes(MODE), g, q, lane);
+        using Epilogue = std::conditional_t<MODE == kDgradSaved, SavedEpilogue, LinearEpilogue<KIND>>;
+        Epilogue ep(p, stg + g * kGroup, g, q, lane);
         // all four warps of the group go on, or none
         const auto agree = [&](bool ok) {
             int all;
@@ -996,7 +1144,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     tc_fence_before();
     if (kCluster) cluster_sync_all();
     else __syncthreads();
-    if (warp == 2) tmem_free<CG>(tmem, tmem_cols(BN));
+    if (warp == 2) tmem_free<CG>(tmem, tmem_cols(BN, KIND));
 }
 
 // --------------------------------------------------------------------------
@@ -1083,7 +1231,7 @@ cudaError_t encode_window(CUtensorMap *m, const void *base, int cols, int rows, 
     return encode(m, false, base, 4, d, st, b);
 }
 
-template <int CG, int BN, int MODE, bool FP8, bool SPLIT>
+template <int CG, int BN, int MODE, int KIND, bool SPLIT>
 cudaError_t launch(const Params &p, cudaStream_t s)
 {
     // No programmatic dependent launch: do not add it.  With it (tensor memory
@@ -1101,9 +1249,9 @@ cudaError_t launch(const Params &p, cudaStream_t s)
     //     and walk the same chunks;
     //   bulk_wait_group, tcgen05.wait::ld: copies and loads already issued,
     //     which depend on nothing else.
-    static_assert(2 * (smem_bytes(CG, BN, MODE, SPLIT) + 1024) > 228 * 1024, "one block on an SM");
-    const auto fn = experts_kernel<CG, BN, MODE, FP8, SPLIT>;
-    cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes(CG, BN, MODE, SPLIT));
+    static_assert(2 * (smem_bytes(CG, BN, MODE, KIND, SPLIT) + 1024) > 228 * 1024, "one block on an SM");
+    const auto fn = experts_kernel<CG, BN, MODE, KIND, SPLIT>;
+    cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes(CG, BN, MODE, KIND, SPLIT));
     if (err != cudaSuccess) return err;
     // the most tiles that offsets over these rows can give
     const long long tm = (p.M + kTileM * CG - 1) / (kTileM * CG);
@@ -1113,7 +1261,7 @@ cudaError_t launch(const Params &p, cudaStream_t s)
 
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes(CG, BN, MODE, SPLIT);
+    cfg.dynamicSmemBytes = smem_bytes(CG, BN, MODE, KIND, SPLIT);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1144,22 +1292,22 @@ cudaError_t launch(const Params &p, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
-template <int MODE, bool FP8>
+template <int MODE, int KIND>
 cudaError_t launch_cut(Params &p, const Cut &c, cudaStream_t s)
 {
     p.bn = c.bn;
     p.split = c.split;
-    if (c.cg == 2) return launch<2, 256, MODE, FP8, false>(p, s);
+    if (c.cg == 2) return launch<2, KIND == kFp4 ? kFp4Wide : 256, MODE, KIND, false>(p, s);
     if constexpr (MODE != kWgrad)
         if (c.bn == 32)
-            return c.split > 1 ? launch<1, 32, MODE, FP8, true>(p, s) : launch<1, 32, MODE, FP8, false>(p, s);
-    return c.split > 1 ? launch<1, 128, MODE, FP8, true>(p, s) : launch<1, 128, MODE, FP8, false>(p, s);
+            return c.split > 1 ? launch<1, 32, MODE, KIND, true>(p, s) : launch<1, 32, MODE, KIND, false>(p, s);
+    return c.split > 1 ? launch<1, 128, MODE, KIND, true>(p, s) : launch<1, 128, MODE, KIND, false>(p, s);
 }
 
-template <bool FP8>
-cudaError_t linear(const moe_rows *G, const void *x, const float *x_scales, int K, const void *w,
-                   const float *w_scales, int N, const void *bias, int act, const void *residual, void *y,
-                   void *saved, void *saved_scales, cudaStream_t s)
+template <int KIND>
+cudaError_t linear(const moe_rows *G, const void *x, const void *x_scales, int K, const void *w, const void *w_scales,
+                   int N, const void *bias, int act, const void *residual, void *y, void *saved, void *saved_scales,
+                   cudaStream_t s)
 {
     Params p = {};
     p.offsets = G->offsets;
@@ -1167,29 +1315,38 @@ cudaError_t linear(const moe_rows *G, const void *x, const float *x_scales, int 
     p.E = G->E;
     p.rows = G->rows;
     p.M = N;
-    p.K = FP8 ? K : 2 * K;
     p.act = act;
     p.glu = act == MOE_ACT_SWIGLU;
     p.bias = static_cast<const __nv_bfloat16 *>(bias);
     p.residual = static_cast<const __nv_bfloat16 *>(residual);
-    p.x_scales = reinterpret_cast<const float2 *>(x_scales);
-    p.w_scales = reinterpret_cast<const float2 *>(w_scales);
+    if (KIND == kE4m3) {
+        p.x_scales = static_cast<const float2 *>(x_scales);
+        p.w_scales = static_cast<const float2 *>(w_scales);
+    } else if (KIND == kFp4) {
+        p.x_bytes = static_cast<const uint8_t *>(x_scales);
+        p.w_bytes = static_cast<const uint8_t *>(w_scales);
+        p.pitch = MOE_FP4_PITCH(K);
+        p.valid_scales = K / 32;
+    }
     p.y = static_cast<__nv_bfloat16 *>(y);
     p.saved = static_cast<uint8_t *>(saved);
     p.saved_scales = static_cast<uint8_t *>(saved_scales);
-    const int elems = FP8 ? 128 : 64;
-    const Cut cut = rows_cut(N, G->rows, G->E, (K + elems - 1) / elems);
+    const bool bytes = KIND != kBf16;  // the tensor maps' unit; two values of kFp4
+    const int cols = KIND == kFp4 ? K / 2 : K, elems = bytes ? 128 : 64;
+    p.K = bytes ? cols : 2 * cols;
+    const Cut cut = KIND == kFp4 ? rows_cut_fp4(N, G->rows, G->E, (cols + 127) / 128)
+                                 : rows_cut(N, G->rows, G->E, (cols + elems - 1) / elems);
     // w as [E][N/halves][halves][K] with the halves inside: one load brings
     // gate and up rows alternating, so that a pair of them ends in one lane
-    const uint64_t h = p.glu ? 2 : 1, n = (uint64_t)N / h;
-    const uint64_t d[4] = {(uint64_t)K, h, n, (uint64_t)G->E};
-    const uint64_t st[3] = {n * K, (uint64_t)K, (uint64_t)N * K};
+    const uint64_t h = p.glu ? 2 : 1, n = (uint64_t)N / h, k = (uint64_t)cols;
+    const uint64_t d[4] = {k, h, n, (uint64_t)G->E};
+    const uint64_t st[3] = {n * k, k, (uint64_t)N * k};
     const uint32_t b[4] = {(uint32_t)elems, (uint32_t)h, (uint32_t)(kTileM / h), 1};
-    cudaError_t err = encode(&p.ma, FP8, w, 4, d, st, b);
-    if (err == cudaSuccess) err = encode_rows(&p.mb, FP8, x, K, G->rows, elems, cut.bn / cut.cg);
-    if (err == cudaSuccess && cut.bn > 32) err = encode_rows(&p.mb32, FP8, x, K, G->rows, elems, 32);
+    cudaError_t err = encode(&p.ma, bytes, w, 4, d, st, b);
+    if (err == cudaSuccess) err = encode_rows(&p.mb, bytes, x, cols, G->rows, elems, cut.bn / cut.cg);
+    if (err == cudaSuccess && cut.bn > 32) err = encode_rows(&p.mb32, bytes, x, cols, G->rows, elems, 32);
     if (err != cudaSuccess) return err;
-    return launch_cut<kLinear, FP8>(p, cut, s);
+    return launch_cut<kLinear, KIND>(p, cut, s);
 }
 
 template <int MODE>
@@ -1213,7 +1370,7 @@ cudaError_t dgrad(const moe_rows *G, const void *dy, int N, const void *w, int K
     if (err == cudaSuccess) err = encode_rows(&p.mb, false, dy, N, G->rows, 64, cut.bn / cut.cg);
     if (err == cudaSuccess && cut.bn > 32) err = encode_rows(&p.mb32, false, dy, N, G->rows, 64, 32);
     if (err != cudaSuccess) return err;
-    return launch_cut<MODE, false>(p, cut, s);
+    return launch_cut<MODE, kBf16>(p, cut, s);
 }
 
 }  // namespace

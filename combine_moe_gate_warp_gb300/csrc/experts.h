@@ -12,6 +12,9 @@ struct Cut {
 };
 // linear and dgrad: m output columns of `rows` rows, k_stages of 128 bytes
 Cut rows_cut(int m, int rows, int E, long long k_stages);
+// rows and weights in 4 bits: scales take the tensor memory of a wider tile
+constexpr int kFp4Wide = 224;
+Cut rows_cut_fp4(int m, int rows, int E, long long k_stages);
 Cut wgrad_cut(int N, int K, int rows, int E);
 
 cudaError_t launch_expert_linear(const moe_rows *G, const void *x, const float *x_scales, int K, const void *w,
@@ -20,6 +23,9 @@ cudaError_t launch_expert_linear(const moe_rows *G, const void *x, const float *
 cudaError_t launch_expert_linear_e4m3(const moe_rows *G, const void *x, const float *x_scales, int K, const void *w,
                                       const float *w_scales, int N, const void *bias, int act, const void *residual,
                                       void *y, void *saved, void *saved_scales, cudaStream_t s);
+cudaError_t launch_expert_linear_fp4(const moe_rows *G, const void *x, const void *x_scales, int K, const void *w,
+                                     const void *w_scales, int N, const void *bias, int act, const void *residual,
+                                     void *y, cudaStream_t s);
 cudaError_t launch_expert_dgrad(const moe_rows *G, const void *dy, int N, const void *w, int K, int act,
                                 const void *saved, const void *saved_scales, void *dx, void *a, cudaStream_t s);
 cudaError_t launch_expert_dgrad_saved(const moe_rows *G, const void *dy, int N, const void *w, int K, int act,

@@ -59,6 +59,25 @@ moe_status moe_expert_linear(const moe_rows *G, const void *x, const float *x_sc
                                                saved_scales, stream_of(stream)));
 }
 
+moe_status moe_expert_linear_fp4(const moe_rows *G, const void *x, const void *x_scales, int K, const void *w,
+                                 const void *w_scales, int N, const void *bias, int act, const void *residual, void *y,
+                                 moe_stream_t stream)
+{
+    moe_status st = check_rows(G);
+    if (st != MOE_OK) return st;
+    if (!act_ok(act)) return MOE_ERR_INVALID_ARG;
+    st = check_sizes(G, K, N);
+    if (st != MOE_OK) return st;
+    if (K % 32 != 0) return MOE_ERR_UNSUPPORTED;
+    if (act == MOE_ACT_SWIGLU && N % 16 != 0) return MOE_ERR_UNSUPPORTED;
+    if (!w || !w_scales || (G->rows > 0 && (!x || !x_scales || !y))) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(x_scales) || !aligned16(w) || !aligned16(w_scales) || !aligned16(bias) ||
+        !aligned16(residual) || !aligned16(y))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_expert_linear_fp4(G, x, x_scales, K, w, w_scales, N, bias, act, residual, y,
+                                                   stream_of(stream)));
+}
+
 moe_status moe_expert_dgrad(const moe_rows *G, const void *dy, int N, const void *w, int K, int act,
                             const void *saved, const void *saved_scales, void *dx, void *a, moe_stream_t stream)
 {
@@ -130,14 +149,18 @@ moe_status moe_dequantize_fp4(const moe_rows *G, const void *codes, const void *
 
 moe_status moe_expert_cut(int product, int e4m3, int rows, int E, int K, int N, int32_t *cut)
 {
-    if (!cut || rows < 0 || product < MOE_EXPERT_LINEAR || product > MOE_EXPERT_WGRAD) return MOE_ERR_INVALID_ARG;
+    const bool fp4 = product == MOE_EXPERT_LINEAR_FP4;
+    if (!cut || rows < 0 || product < MOE_EXPERT_LINEAR || (product > MOE_EXPERT_WGRAD && !fp4))
+        return MOE_ERR_INVALID_ARG;
     if (e4m3 && product != MOE_EXPERT_LINEAR) return MOE_ERR_INVALID_ARG;
     if (E < 1 || E > MOE_MAX_EXPERTS || rows >= (1 << 30) || !cols_ok(K, 8) || !cols_ok(N, 8))
         return MOE_ERR_UNSUPPORTED;
+    if (fp4 && K % 32 != 0) return MOE_ERR_UNSUPPORTED;
     cut[0] = cut[1] = cut[2] = 0;
     if (rows == 0) return MOE_OK;  // nothing is cut
     const int elems = e4m3 ? 128 : 64;
-    const moe::Cut c = product == MOE_EXPERT_LINEAR  ? moe::rows_cut(N, rows, E, (K + elems - 1) / elems)
+    const moe::Cut c = fp4                           ? moe::rows_cut_fp4(N, rows, E, (K + 255) / 256)
+                       : product == MOE_EXPERT_LINEAR ? moe::rows_cut(N, rows, E, (K + elems - 1) / elems)
                        : product == MOE_EXPERT_DGRAD ? moe::rows_cut(K, rows, E, (N + 63) / 64)
                                                      : moe::wgrad_cut(N, K, rows, E);
     cut[0] = c.cg;

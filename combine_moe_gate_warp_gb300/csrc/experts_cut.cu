@@ -14,15 +14,16 @@ namespace moe {
 // `live` experts have `n` of the ragged axis together (`each`: wgrad, whose n
 // is the same for every expert); their sizes are not known on the host, half
 // a tile each is taken for lost.
-static Cut pick(int m, long long n, int live, bool each, long long k_stages, bool narrow)
+static Cut pick(int m, long long n, int live, bool each, long long k_stages, bool narrow, int widest)
 {
     static const Cut cuts[] = {{2, 256, 1}, {2, 224, 1}, {2, 192, 1}, {2, 160, 1}, {2, 128, 1}, {1, 128, 8},
                                {1, 96, 1},  {1, 64, 1},  {1, 32, 8}};
-    Cut best = cuts[0];
+    Cut best = {};
     double least = 0.0;
     const int sms = device_sm_count();
     for (const Cut &c : cuts) {
         if (!narrow && c.bn != 256 && c.bn != 128) continue;  // wgrad loads B by 64 columns
+        if (c.bn > widest) continue;
         const long long tm = (m + 128 * c.cg - 1) / (128 * c.cg);
         long long tn = live == 1 || each ? (n + c.bn - 1) / c.bn * (each ? live : 1) : n / c.bn + (live + 1) / 2;
         if (tn < live) tn = live;
@@ -48,9 +49,14 @@ static Cut pick(int m, long long n, int live, bool each, long long k_stages, boo
 
 Cut rows_cut(int m, int rows, int E, long long k_stages)
 {
-    return pick(m, rows, rows < E ? rows : E, false, k_stages, true);
+    return pick(m, rows, rows < E ? rows : E, false, k_stages, true, 256);
 }
 
-Cut wgrad_cut(int N, int K, int rows, int E) { return pick(N, K, E, true, (rows / E + 63) / 64, false); }
+Cut rows_cut_fp4(int m, int rows, int E, long long k_stages)
+{
+    return pick(m, rows, rows < E ? rows : E, false, k_stages, true, kFp4Wide);
+}
+
+Cut wgrad_cut(int N, int K, int rows, int E) { return pick(N, K, E, true, (rows / E + 63) / 64, false, 256); }
 
 }  // namespace moe

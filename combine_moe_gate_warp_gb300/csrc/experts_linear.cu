@@ -10,7 +10,7 @@ cudaError_t launch_expert_linear(const moe_rows *G, const void *x, const float *
     if (G->rows == 0) return cudaSuccess;
     if (x_scales)
         return launch_expert_linear_e4m3(G, x, x_scales, K, w, w_scales, N, bias, act, residual, y, saved, saved_scales, s);
-    return linear<false>(G, x, x_scales, K, w, w_scales, N, bias, act, residual, y, saved, saved_scales, s);
+    return linear<kBf16>(G, x, x_scales, K, w, w_scales, N, bias, act, residual, y, saved, saved_scales, s);
 }
 
 }  // namespace moe

@@ -7,7 +7,7 @@ cudaError_t launch_expert_linear_e4m3(const moe_rows *G, const void *x, const fl
                                       const float *w_scales, int N, const void *bias, int act, const void *residual,
                                       void *y, void *saved, void *saved_scales, cudaStream_t s)
 {
-    return linear<true>(G, x, x_scales, K, w, w_scales, N, bias, act, residual, y, saved, saved_scales, s);
+    return linear<kE4m3>(G, x, x_scales, K, w, w_scales, N, bias, act, residual, y, saved, saved_scales, s);
 }
 
 }  // namespace moe

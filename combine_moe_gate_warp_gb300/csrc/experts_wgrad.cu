@@ -30,7 +30,7 @@ cudaError_t launch_expert_wgrad(const moe_rows *G, const void *dy, int N, const 
         err = encode(&p.mo, false, dw, 3, d, st, b, CU_TENSOR_MAP_SWIZZLE_64B);
     }
     if (err != cudaSuccess) return err;
-    return launch_cut<kWgrad, false>(p, cut, s);
+    return launch_cut<kWgrad, kBf16>(p, cut, s);
 }
 
 }  // namespace moe

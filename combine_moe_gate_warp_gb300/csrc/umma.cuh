@@ -69,6 +69,13 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// The same, after what this thread has written and seen written: another
+// CTA's instructions read it.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void tmap_prefetch(const CUtensorMap *m)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
@@ -189,6 +196,55 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
                      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                      "l"(a), "l"(b), "r"(idesc), "r"(acc)
                      : "memory");
+}
+
+// 4-bit operands (kind::mxf4): e2m1 values, K-major, 64 of k to an
+// instruction, a power of two (ue8m0) for 32 of k.  The scales of 128 of k lie
+// in tensor memory as 4 bytes of a row: row 32 j + i of the operand in lane i,
+// column j (and in the same lanes of the other three quarters).  An
+// instruction takes the low or the high two bytes, by its scale id.
+__host__ __device__ constexpr uint32_t mma_idesc_fp4(int m, int n)
+{
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27);
+}
+__host__ __device__ constexpr uint32_t mma_scale_id(int half)
+{
+    return ((uint32_t)(2 * half) << 4) | ((uint32_t)(2 * half) << 29);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        bool add)
+{
+    const uint32_t acc = add ? 1u : 0u;
+    if constexpr (CG == 2)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                         d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                         d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
+                     : "memory");
+}
+
+// 32 rows of 16 bytes in shared memory (8 rows, 128 bytes, after one another;
+// no swizzle) to 4 columns of tensor memory, the same in all four quarters of
+// its lanes.  Instructions of the issuing thread that follow see them.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+template <int CG>
+__device__ __forceinline__ void scales_to_tmem(uint32_t to, uint64_t from)
+{
+    if constexpr (CG == 2)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(from) : "memory");
 }
 
 // One arrival on `bar` (both CTAs' barrier at this offset when CG == 2) once

@@ -193,10 +193,11 @@ class ExpertRows:
 
     def cut(self, product: str, N: int, K: int, e4m3: bool = False):
         """(SMs of a tile, rows per tile, blocks that share its sums) of
-        "linear", "dgrad" or "wgrad" with weights [N, K] on the current
-        device, for tests and tuning."""
+        "linear", "dgrad", "wgrad" or "linear_fp4" with weights [N, K] on the
+        current device, for tests and tuning."""
         c = (ctypes.c_int32 * 3)()
-        abi._check(self._lib.moe_expert_cut(("linear", "dgrad", "wgrad").index(product), int(e4m3), self.rows, self.E,
+        code = 4 if product == "linear_fp4" else ("linear", "dgrad", "wgrad").index(product)
+        abi._check(self._lib.moe_expert_cut(code, int(e4m3), self.rows, self.E,
                                             _columns(K, "w"), _columns(N, "w"), c), "moe_expert_cut")
         return tuple(c)
 
@@ -393,6 +394,32 @@ class ExpertRows:
         cp, sp = self._fp4(x, K, "x")
         out, op = self._out_rows(out, K, "out")
         abi._check(self._lib.moe_dequantize_fp4(self._ref, cp, sp, K, op, self._stream()), "moe_dequantize_fp4")
+        return out
+
+    def linear_fp4(self, x: Fp4Rows, w: Fp4Rows, *, bias=None, act: str = "none", residual=None, out=None):
+        """act(x w^T + bias) + residual for each expert's rows, as ``linear``,
+        from rows and weights in 4 bits: x from the dispatch in 4 bits or
+        ``quantize_fp4``, w from ``quantize_weights_fp4``."""
+        a, dev, rows = _act(act), self.device, self.rows
+        if not isinstance(w, Fp4Rows):
+            raise TypeError("w: expected Fp4Rows")
+        N, half, wp = self._weights(w.codes, torch.uint8)
+        K = 2 * half
+        if K > _INT_MAX:
+            raise ValueError(f"w: {K} columns are too many")
+        ws = _check(w.scales, torch.uint8, self._per_expert(N, abi.fp4_pitch(K)), "w.scales", dev)
+        xp, xs = self._fp4(x, K, "x")
+        cols = N // 2 if a == abi.MOE_ACT_SWIGLU else N
+        bp = None if bias is None else _check(bias, torch.bfloat16, self._per_expert(N), "bias", dev)
+        rp = None if residual is None else _check_rows(residual, torch.bfloat16, rows, cols, "residual", dev)
+        if out is None:
+            out = self._new((rows, cols))
+            op = out.data_ptr()
+        else:
+            op = _check_rows(out, torch.bfloat16, rows, cols, "out", dev)
+        st = self._lib.moe_expert_linear_fp4(self._ref, xp, xs, K, wp, ws, N, bp, a, rp, op, self._stream())
+        if st:
+            abi._check(st, "moe_expert_linear_fp4")
         return out
 
     def linear_backward(self, dy, x, w, *, act: str = "none", saved: SavedLayer | None = None, bias: bool = False,

@@ -78,6 +78,21 @@ moe_status moe_expert_linear(const moe_rows *G, const void *x, const float *x_sc
                              void *saved, void *saved_scales, moe_stream_t stream);
 
 /*
+ * moe_expert_linear_fp4 -- moe_expert_linear from rows and weights in 4 bits
+ * (the format of moe_dispatch_fp4), each value its code times its block's
+ * power of two:
+ *     u[r, n] = sum_k x[r, k] * w[e, n, k] + bias[e, n];  y[r] = act(u[r]) + residual[r]
+ *   x [rows, K/2] uint8 codes, x_scales [rows, MOE_FP4_PITCH(K)] uint8;
+ *   w [E, N, K/2], w_scales [E, N, MOE_FP4_PITCH(K)]; K % 32 == 0.
+ *   The products are exact, their sums in fp32.  A block marked 255 makes
+ *   the sums it enters NaN.  Scale bytes past a row's K/32 are not used.
+ *   bias, act, residual, y: as moe_expert_linear.
+ */
+moe_status moe_expert_linear_fp4(const moe_rows *G, const void *x, const void *x_scales, int K, const void *w,
+                                 const void *w_scales, int N, const void *bias, int act, const void *residual, void *y,
+                                 moe_stream_t stream);
+
+/*
  * moe_expert_dgrad -- the gradient with respect to the rows:
  *     d[r, k] = sum_n dy[r, n] * w[e, n, k]
  *   dy [rows, N] bf16, w [E, N, K] bf16.
@@ -132,6 +147,7 @@ moe_status moe_dequantize_fp4(const moe_rows *G, const void *codes, const void *
 #define MOE_EXPERT_LINEAR 0
 #define MOE_EXPERT_DGRAD 1
 #define MOE_EXPERT_WGRAD 2
+#define MOE_EXPERT_LINEAR_FP4 4 /* moe_expert_linear_fp4; e4m3 is 0 */
 moe_status moe_expert_cut(int product, int e4m3, int rows, int E, int K, int N, int32_t *cut);
 
 #ifdef __cplusplus
