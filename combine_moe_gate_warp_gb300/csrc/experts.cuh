@@ -29,6 +29,10 @@
 //   wgrad, the same                                           460 us, 85 %
 //   linear, 128 rows, 32 experts, 2048 -> 2 x 1024            47 us, 5.7 TB/s:
 //     the weights' bytes (and 6 us to start and to finish)
+//   linear in 4 bits, 65536 rows, 16 experts, 5120 -> 2 x 2048 swiglu  465 us,
+//     5.9 PFLOP/s; one expert, 8192 -> 8192: 1315 us, 6.7 PFLOP/s: the matrix
+//     instructions, which are issued without a pause at 7.1-7.7
+//   linear in 4 bits, 128 rows, 32 experts, 2048 -> 2 x 2048   29 us, 4.9 TB/s
 //   linear, 512 rows, 8 experts, 512 -> 2 x 256               6 us from the
 //     first instruction to the last: 0.8 for offsets and barriers, 1 until the
 //     first bytes, 2 for 8 stages, 1.5 for the epilogue
@@ -96,8 +100,7 @@ __host__ __device__ constexpr int join_bytes(bool SPLIT, int BN) { return SPLIT 
 // counts, and the alignment to 1 KB; at most 12 stages
 __host__ __device__ constexpr int stages(int CG, int BN, int MODE, int KIND, bool SPLIT)
 {
-    const int n = (227 * 1024 - 2 * group_bytes(MODE, KIND) - join_bytes(SPLIT, BN) - kControl - 1024) /
-                  stage_bytes(CG, BN, KIND);
+    const int n = (227 * 1024 - 2 * group_bytes(MODE, KIND) - join_bytes(SPLIT, BN) - kControl - 1024) / stage_bytes(CG, BN, KIND);
     return n > 12 ? 12 : n;
 }
 __host__ __device__ constexpr int smem_bytes(int CG, int BN, int MODE, int KIND, bool SPLIT)
@@ -354,7 +357,8 @@ struct LinearEpilogue {
             }
             u[i] += bias;
         }
-        if (p.saved) save(u, row, rows);
+        if constexpr (KIND != kFp4)
+            if (p.saved) save(u, row, rows);
         if (p.glu) {
             // lanes 2i and 2i+1 hold gate and up of a column: of each two
             // rows the even lane finishes the first, the odd lane the second
@@ -394,7 +398,7 @@ struct LinearEpilogue {
         __nv_bfloat16 *y = p.y + (size_t)row * n + col0;
         if (p.glu) copy_out<8, 32>(out, kPitchGlu, y, 2 * n, rows, cols / 8, tid);
         else copy_out<16, 32>(out, kPitch, y, 2 * n, rows, cols / 8, tid);
-        if (p.saved) {
+        if (KIND != kFp4 && p.saved) {
             uint8_t *s = p.saved + (size_t)row * p.M + col0;
             if (p.glu) {
                 copy_out<4, 32>(codes, kPitchCode, s, p.M, rows, cols / 16, tid);
@@ -600,30 +604,6 @@ __device__ __forceinline__ void store_tile(const Params &p, unsigned char *buf, 
 }
 
 // --------------------------------------------------------------------------
-// kFp4: one warp brings an operand's scale bytes to the stages.  Its lane i
-// reads 8 bytes (256 values of k) of the rows i, i + 32, .. of a tile, kSets
-// stages ahead of their use, and stores those of 4 rows with one 16-byte store
-// as tensor memory takes them: the rows' scales lie in row order, and no copy
-// engine turns 4-byte pieces around.
-// --------------------------------------------------------------------------
-template <int ROWS, typename Next, typename Put>
-__device__ __forceinline__ void feed_scales(const Next &next, const Put &put)
-{
-    constexpr int kSets = 4;
-    uint2 v[kSets][ROWS];
-    bool have[kSets];
-#pragma unroll
-    for (int d = 0; d < kSets; ++d) have[d] = next(v[d]);
-    for (;;) {
-#pragma unroll
-        for (int d = 0; d < kSets; ++d) {
-            if (!have[d] || !put(v[d])) return;
-            have[d] = next(v[d]);
-        }
-    }
-}
-
-// --------------------------------------------------------------------------
 // the kernel
 // --------------------------------------------------------------------------
 template <int CG, int BN, int MODE, int KIND, bool SPLIT>
@@ -662,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     if (tid == 0) {
         const unsigned skip = blockIdx.x == 0 ? *(volatile unsigned *)&header->inject_skip_load : 0u;
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&c->full[i], FP4 ? 1 + 2 * CG : 1);  // the copies, and two warps' scales from each block
+            mbar_init(&c->full[i], FP4 ? 1 + CG : 1);  // the copies, and each block's scales
             mbar_init(&c->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -933,76 +913,105 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         __syncwarp();
     } else if (FP4 && (warp == 2 || warp == 3)) {
         // ---- scales ---------------------------------------------------------
-        // Warp 2 has A's, warp 3 B's.  What lies past the last row or the
-        // last 32 values of k is zero.
-        const auto feed = [&](auto is_b) {
-            constexpr bool B = decltype(is_b)::value;
-            constexpr int kRows = B ? 4 * scale_atoms(BN) : 4;
-            const uint8_t *at[kRows] = {};
-            const int valid = p.valid_scales;  // bytes of a row that hold scales
-            int i = 0, end = 0, s = 0;
-            uint32_t ph = 1;
-            const auto next = [&](uint2(&v)[kRows]) {
-                while (i == end) {
-                    if (!walk.next(t)) return false;
-                    const Span part = span(t);
-                    i = part.first;
-                    end = part.first + part.count;
-                    const int m0 = t.m * kBM + (int)rank * kTileM, n0 = t.n * p.bn;
-#pragma unroll
-                    for (int r = 0; r < kRows; ++r) {
-                        const int row = r * 32 + lane;
-                        if (B) {
-                            at[r] = row < min(p.bn, t.rows - n0) ? p.x_bytes + (size_t)(t.row0 + n0 + row) * p.pitch
-                                                                 : nullptr;
-                        } else {
-                            // glu: A's rows alternate gate and up columns
-                            const int half = p.glu ? p.M / 2 : p.M, col = p.glu ? (m0 + row) / 2 : m0 + row;
-                            at[r] = col < half ? p.w_bytes + ((size_t)t.e * p.M + (p.glu ? (row & 1) * half : 0) + col) *
-                                                                 p.pitch
-                                               : nullptr;
-                        }
-                    }
-                }
-                const int left = valid - i * 8;  // < 8: the last stage
-                const uint2 keep = left >= 8 ? make_uint2(~0u, ~0u)
-                                             : make_uint2(left >= 4 ? ~0u : (1u << (8 * left)) - 1u,
-                                                          left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1u);
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    v[r] = at[r] ? __ldg(reinterpret_cast<const uint2 *>(at[r] + i * 8)) : make_uint2(0u, 0u);
-                    v[r].x &= keep.x;
-                    v[r].y &= keep.y;
-                }
-                ++i;
-                return true;
-            };
-            const auto put = [&](const uint2(&v)[kRows]) {
-                if (!wait(&c->empty[s], ph, c, p.ws)) return false;
-                unsigned char *to = smem + s * kStage + kScales + (B ? 2 * kScaleAtom : 0) + lane * 16;
-#pragma unroll
-                for (int h = 0; h < kRows / 4; ++h) {
-                    *reinterpret_cast<uint4 *>(to + h * kScaleAtom) =
-                        make_uint4(v[4 * h].x, v[4 * h + 1].x, v[4 * h + 2].x, v[4 * h + 3].x);
-                    *reinterpret_cast<uint4 *>(to + (kRows / 4 + h) * kScaleAtom) =
-                        make_uint4(v[4 * h].y, v[4 * h + 1].y, v[4 * h + 2].y, v[4 * h + 3].y);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2) mbar_arrive_release_cluster(cluster_addr(&c->full[s], 0));
-                    else mbar_arrive(&c->full[s]);
-                }
-                if (++s == kStages) {
-                    s = 0;
-                    ph ^= 1;
-                }
-                return true;
-            };
-            feed_scales<kRows>(next, put);
+        // The rows' scales lie in row order, tensor memory wants 4 bytes of 4
+        // rows side by side, and no copy engine turns pieces of 4 bytes around.
+        // So a lane reads 8 kSpan bytes (four stages' are a whole sector) of the rows lane, lane + 32, .. of both operands, and stores
+        // 4 bytes of 4 rows with one instruction.  The two warps take every
+        // other kSpan stages: a stage takes one of them about 780 cycles, its
+        // products 530.  65536 rows, 16 experts, 5120 -> 2 x 2048: 465 us; the
+        // rows' 16 bytes through a ring in shared memory 513 us; a warp for
+        // each operand, four stages ahead in registers and unrolled for that,
+        // 860 us: 270 KB of instructions, and the block waits for them.
+        // A warp does not wait for the stages that it leaves out.  Its last wait
+        // told it that the ring has been read up to kStages before that stage;
+        // a parity asked for more than kStages later could be that of an
+        // earlier round and let it overwrite what is still to be read.
+        constexpr int kRowsB = (BN + 31) / 32, kRows = 4 + kRowsB, kSpan = kStages > 4 ? 4 : 2;
+        static_assert(!FP4 || kSpan + 1 <= kStages, "the ring is as long as the way from wait to wait");
+        int s = 0, turn = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        const auto step = [&](int n) {
+            s += n;
+            if (s >= kStages) {
+                s -= kStages;
+                ph ^= 1;
+            }
         };
-        if (warp == 2) feed(std::false_type());
-        else feed(std::true_type());
+        while (ok && walk.next(t)) {
+            const Span part = span(t);
+            const int end = part.first + part.count, m0 = t.m * kBM + (int)rank * kTileM, n0 = t.n * p.bn;
+            const uint8_t *at[kRows];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {  // glu: A's rows alternate gate and up columns
+                const int row = r * 32 + lane, half = p.glu ? p.M / 2 : p.M, col = p.glu ? (m0 + row) / 2 : m0 + row;
+                at[r] = col < half ? p.w_bytes + ((size_t)t.e * p.M + (p.glu ? (row & 1) * half : 0) + col) * p.pitch
+                                   : nullptr;
+            }
+#pragma unroll
+            for (int r = 0; r < kRowsB; ++r) {
+                const int row = r * 32 + lane;
+                at[4 + r] = row < min(p.bn, t.rows - n0) ? p.x_bytes + (size_t)(t.row0 + n0 + row) * p.pitch : nullptr;
+            }
+            for (int i = part.first; ok && i < end;) {
+                const int span0 = i / kSpan * kSpan, next = min(span0 + kSpan, end);
+                if ((turn++ & 1) != (warp & 1)) {
+                    step(next - i);
+                    i = next;
+                    continue;
+                }
+                const int left = p.valid_scales - span0 * 8;  // scale bytes of a row from here on
+                uint32_t v[kRows][2 * kSpan];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                    for (int h = 0; h < kSpan / 2; ++h) {
+                        const uint4 q = at[r] && h * 16 < left
+                                            ? __ldg(reinterpret_cast<const uint4 *>(at[r] + span0 * 8 + h * 16))
+                                            : make_uint4(0u, 0u, 0u, 0u);
+                        v[r][4 * h] = q.x;
+                        v[r][4 * h + 1] = q.y;
+                        v[r][4 * h + 2] = q.z;
+                        v[r][4 * h + 3] = q.w;
+                    }
+                if (left < 8 * kSpan)  // nothing past a row's scales
+#pragma unroll
+                    for (int k = 0; k < 2 * kSpan; ++k) {
+                        const int n = left - 4 * k;
+                        const uint32_t keep = n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+#pragma unroll
+                        for (int r = 0; r < kRows; ++r) v[r][k] &= keep;
+                    }
+#pragma unroll
+                for (int q = 0; q < kSpan; ++q) {
+                    if (span0 + q < i || span0 + q >= next) continue;
+                    ok = ok && wait(&c->empty[s], ph, c, p.ws);
+                    if (!ok) break;
+                    unsigned char *to = smem + s * kStage + kScales + lane * 16;
+                    const auto word = [&](int r, int end_r, int w) { return r < end_r ? v[r < kRows ? r : 0][2 * q + w] : 0u; };
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        *reinterpret_cast<uint4 *>(to + w * kScaleAtom) =
+                            make_uint4(word(0, 4, w), word(1, 4, w), word(2, 4, w), word(3, 4, w));
+#pragma unroll
+                        for (int h = 0; h < scale_atoms(BN); ++h)
+                            *reinterpret_cast<uint4 *>(to + (2 + w * scale_atoms(BN) + h) * kScaleAtom) =
+                                make_uint4(word(4 * h + 4, kRows, w), word(4 * h + 5, kRows, w),
+                                           word(4 * h + 6, kRows, w), word(4 * h + 7, kRows, w));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    // Not released at cluster scope: a block's scales are read
+                    // by the copy to its own tensor memory, from its own shared
+                    // memory, and the fence above has them there before the
+                    // arrival goes out.  A release, or a fence by an idle warp,
+                    // takes 1900 cycles a stage (1230 us against 513).
+                    if (lane == 0) mbar_arrive_remote(cluster_addr(&c->full[s], lead));
+                    step(1);
+                }
+                i = next;
+            }
+        }
     } else if (warp >= kEpiWarp) {
         // ---- epilogue ------------------------------------------------------
         // Two groups of four warps take the chunks of a tile in turn.

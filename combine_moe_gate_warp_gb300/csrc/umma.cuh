@@ -69,13 +69,6 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same, after what this thread has written and seen written: another
-// CTA's instructions read it.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 __device__ __forceinline__ void tmap_prefetch(const CUtensorMap *m)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
