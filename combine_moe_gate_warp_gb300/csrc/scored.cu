@@ -19,7 +19,6 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr float kTiny = 1e-20f;  // beside the sum of the selected scores
 
 struct GateArgs {
@@ -51,13 +50,19 @@ __device__ __forceinline__ F warp_sum(F v)
 // One token in 64 bits, by a whole warp: lane j < k gets slot j's expert.
 // --------------------------------------------------------------------------
 struct Scratch {
-    double v[MOE_MAX_EXPERTS], group[MOE_MAX_EXPERTS];
-    unsigned char kept[MOE_MAX_EXPERTS];
+    double *v, *group;    // [E], [groups]
+    unsigned char *kept;  // [groups]
+    static __host__ __device__ int bytes(int E, int G) { return 8 * E + 9 * G; }
+    __device__ Scratch(void *p, int E, int G)
+        : v(static_cast<double *>(p)), group(v + E), kept(reinterpret_cast<unsigned char *>(group + G))
+    {
+    }
 };
 
-__device__ __noinline__ int select64(const float *row, const GateArgs &a, Scratch &s, int lane)
+__device__ __noinline__ int select64(const float *row, const GateArgs &a, void *memory, int lane)
 {
     const int E = a.E, per = E / a.S.groups;
+    const Scratch s(memory, E, a.S.groups);
     double m = 0.0, inv = 0.0;
     if (a.S.score == MOE_SCORE_SOFTMAX) {
         float top = -INFINITY;
@@ -129,61 +134,429 @@ __device__ __forceinline__ float sigmoid(float l)
 }
 
 // --------------------------------------------------------------------------
-// A warp per token.
+// The selection on 32-bit keys.  L lanes share a token.  A value v becomes a
+// whole number q of 23 bits, q = (v - lowest) * steps, and with the expert's
+// id below it one key: largest key first means largest value, then lowest id,
+// and a comparison with its exchange is two instructions, min and max.  Lists
+// of KL keys are sorted by Batcher's networks, merged, and merged across the
+// lanes of a token.
+//
+// What q does not decide is found and decided elsewhere: with the bound on
+// q's error below, neighbours in the order that are at most `near` apart, and
+// groups at the border between kept and dropped that are, may be the other
+// way round.  Equal logits with equal biases are equal values, and rightly in
+// the order of their ids; whatever else is that close goes to select64.
+//
+// A warp reads its tokens' logits to shared memory, and the keys take their
+// place there.  Rows start in other banks: row pitch = L modulo 32 (odd, for
+// L = 1).
 // --------------------------------------------------------------------------
-__global__ void __launch_bounds__(32 * kWarps) gate_scored_kernel(const GateArgs a)
+constexpr float kSteps = 8388600.0f;  // of q, below 2^23
+
+// q's error in steps.  The exponential (ex2.approx, 2 steps of 2^-23) with its
+// argument's rounding and the reciprocal (1 step) leave a sigmoid within
+// 1.25 * 2^-22 of its value, 2.5 steps for values that span 1 or more; the
+// bias term and the sum are rounded to steps: 0.5 each, and 0.5 for the bias'
+// product.  4 each, 8 for two, and the cut to whole steps.
+constexpr int kNearSigmoid = 10;
+// Softmax: exp(l - max) (expf, 2 steps of 2^-23, and its argument's rounding)
+// within 1.2 * 2^-22 of it, 2.4 steps.  The sum of E
+// terms, in 8 parts or more, and its reciprocal are within 42 * 2^-24; they
+// scale all scores alike and matter where a bias is added: 21 steps.
+constexpr int kNearSoftmax = 10, kNearSoftmaxBias = 32;
+
+__device__ __forceinline__ unsigned make_key(float steps, int e)  // steps in [2^23, 2^24)
 {
-    __shared__ Scratch s_scratch[kWarps];
+    return (__float_as_uint(steps) << 9) + (unsigned)(511 - e);
+}
+__device__ __forceinline__ int key_id(unsigned key) { return 511 - (int)(key & 511u); }
+
+template <int KL>
+__device__ __forceinline__ void order(unsigned (&x)[KL], int i, int j)  // larger first
+{
+    const unsigned a = max(x[i], x[j]), b = min(x[i], x[j]);
+    x[i] = a;
+    x[j] = b;
+}
+// Batcher's odd-even merge sort
+template <int KL>
+__device__ __forceinline__ void sort_keys(unsigned (&x)[KL])
+{
+#pragma unroll
+    for (int p = 1; p < KL; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j <= KL - 1 - q; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < KL && (i + j) / (2 * p) == (i + j + q) / (2 * p)) order(x, i + j, i + j + q);
+}
+// The KL largest of two sorted lists, sorted; `rest`: the largest of those left out.
+template <int KL>
+__device__ __forceinline__ void merge_keys(unsigned (&x)[KL], const unsigned (&y)[KL], unsigned &rest)
+{
+#pragma unroll
+    for (int i = 0; i < KL; ++i) {
+        rest = max(rest, min(x[i], y[KL - 1 - i]));
+        x[i] = max(x[i], y[KL - 1 - i]);
+    }
+#pragma unroll
+    for (int q = KL / 2; q >= 1; q /= 2)
+#pragma unroll
+        for (int i = 0; i < KL; ++i)
+            if (!(i & q)) order(x, i, i + q);
+}
+
+template <int L, typename F>
+__device__ __forceinline__ F lanes_max(F v)
+{
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+template <int L>
+__device__ __forceinline__ unsigned lanes_min(unsigned v)
+{
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal_fast(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+constexpr int kGateWarps = 4;
+
+__host__ __device__ inline int row_pitch(int E, int L)
+{
+    return L == 1 ? (E | 1) : L == 32 ? E : (E + 31 - L) / 32 * 32 + L;
+}
+// Words of shared memory of a warp: keys and groups, where select64 works once
+// the lists are made; selected ids and scores, the softmax's top and sum.
+__host__ __device__ inline int key_words(int E, int G, int L)
+{
+    const int keys = 32 / L * (row_pitch(E, L) + (G | 1)), work = (Scratch::bytes(E, G) + 3) / 4;
+    return ((keys > work ? keys : work) + 1) / 2 * 2;
+}
+__host__ __device__ inline int warp_words(int E, int G, int k, int L)
+{
+    return key_words(E, G, L) + 32 / L * (2 * k + 2);
+}
+
+template <int KL, int L>
+__global__ void __launch_bounds__(32 * kGateWarps) gate_scored_kernel(const __grid_constant__ GateArgs a)
+{
+    constexpr int kTokens = 32 / L;
+    extern __shared__ __align__(16) unsigned s_dyn[];
+    __shared__ float s_bias[MOE_MAX_EXPERTS];  // less the lowest, in steps + 2^23 (sigmoid)
     __shared__ unsigned s_hist[MOE_MAX_EXPERTS];
+    __shared__ float s_low[kGateWarps], s_high[kGateWarps];
     __shared__ int s_last;
     WsHeader *ws = static_cast<WsHeader *>(a.ws);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_hist[e] = 0u;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L, tok = lane / L;
+    const int E = a.E, k = a.k, G = a.S.groups, per = E / G, pitch = row_pitch(E, L);
+    const bool softmax = a.S.score == MOE_SCORE_SOFTMAX, grouped = a.S.top_groups < G;
+    unsigned *const rows = s_dyn + warp * warp_words(E, G, k, L);
+    unsigned *const groups = rows + kTokens * pitch;
+    unsigned *const sel = rows + key_words(E, G, L);  // [kTokens * k] ids, then their scores
+    float *const score = reinterpret_cast<float *>(sel + kTokens * k);
+    float2 *const soft = reinterpret_cast<float2 *>(score + kTokens * k);  // [kTokens] the softmax's top and sum
+    for (int e = threadIdx.x; e < E; e += blockDim.x) s_hist[e] = 0u;
     pdl_wait();
     pdl_launch_dependents();
-    bool finite = true;
-    if (a.S.bias)
-        for (int e = threadIdx.x; e < a.E; e += blockDim.x) finite &= isfinite(a.S.bias[e]);
-    __syncthreads();
-    for (long long t = (long long)blockIdx.x * kWarps + warp; t < a.T; t += (long long)gridDim.x * kWarps) {
-        const float *row = a.logits + t * a.E;
-        float m = -INFINITY, sum = 0.0f;
-        for (int e = lane; e < a.E; e += 32) {
-            finite &= isfinite(row[e]);
-            m = fmaxf(m, row[e]);
+
+    float check = 0.0f;  // stays 0 over finite values
+    float low = 0.0f, high = 0.0f;
+    if (a.S.bias) {
+        low = INFINITY;
+        high = -INFINITY;
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            const float b = a.S.bias[e];
+            check = fmaf(b, 0.0f, check);
+            low = fminf(low, b);
+            high = fmaxf(high, b);
         }
-        const int id = select64(row, a, s_scratch[warp], lane);
-        float g = 0.0f;
-        if (a.S.score == MOE_SCORE_SOFTMAX) {
-            m = warp_max(m);
-            for (int e = lane; e < a.E; e += 32) sum += expf(row[e] - m);
-            sum = warp_sum(sum);
-            if (lane < a.k) g = __fdiv_rn(expf(row[id] - m), sum);
-        } else if (lane < a.k) {
-            g = sigmoid(row[id]);
+        high = warp_max(high);
+        low = -warp_max(-low);
+        if (lane == 0) {
+            s_low[warp] = low;
+            s_high[warp] = high;
         }
-        if (a.S.renorm) g = __fdiv_rn(g, warp_sum(g) + kTiny);
-        if (lane < a.k) {
-            a.idx[t * a.k + lane] = id;
-            a.gates[t * a.k + lane] = g * a.S.scale;
-            atomicAdd(&s_hist[id], 1u);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kGateWarps; ++w) {
+            low = fminf(low, s_low[w]);
+            high = fmaxf(high, s_high[w]);
         }
     }
-    if (!finite) record_status(ws, MOE_ERR_DEVICE_DATA);
+    const float span = high - low;
+    const float steps = softmax ? 1.0f : kSteps / (1.0f + span);
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        const float b = a.S.bias ? a.S.bias[e] - low : 0.0f;
+        s_bias[e] = softmax ? b : fmaf(b, steps, 8388608.0f);
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+    const int near = softmax ? (a.S.bias ? kNearSoftmaxBias : kNearSoftmax) : kNearSigmoid;
+
+    const long long stride = (long long)gridDim.x * kGateWarps * kTokens;
+    for (long long t0 = ((long long)blockIdx.x * kGateWarps + warp) * kTokens; t0 < a.T; t0 += stride) {
+        const int tokens = (int)min((long long)kTokens, a.T - t0);
+        const float *const tile = a.logits + t0 * E;
+        const bool on = tok < tokens;
+        const float *const row = tile + (on ? tok : 0) * E;  // of this lane's token
+        unsigned *const mine = rows + tok * pitch;
+        {
+            // the rows lie one after the other: a flat copy (zeros past the last token)
+            int r = lane / E, c = lane - r * E;
+            const int dr = 32 / E, dc = 32 - dr * E;
+#pragma unroll 8
+            for (int i = lane; i < kTokens * E; i += 32) {
+                rows[r * pitch + c] = i < tokens * E ? __float_as_uint(__ldg(tile + i)) : 0u;
+                r += dr;
+                c += dc;
+                if (c >= E) {
+                    c -= E;
+                    ++r;
+                }
+            }
+        }
+        __syncwarp();
+
+        // keys in place of the logits
+        if (softmax) {
+            float top = -INFINITY;
+            for (int e = sub; e < E; e += L) top = fmaxf(top, __uint_as_float(mine[e]));
+            top = lanes_max<L>(top);
+            float part[8] = {};
+            for (int e0 = sub; e0 < E; e0 += 8 * L) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int e = e0 + u * L;
+                    if (e < E) {
+                        const float l = __uint_as_float(mine[e]);
+                        check = fmaf(l, 0.0f, check);
+                        const float x = expf(l - top);
+                        part[u] += x;
+                        mine[e] = __float_as_uint(x);
+                    }
+                }
+            }
+            float sum = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
+#pragma unroll
+            for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (sub == 0) soft[tok] = make_float2(top, sum);
+            // without a bias the order is that of exp(l - top)
+            const float inv = a.S.bias ? reciprocal_fast(sum) : 1.0f;
+            const float unit = kSteps / (inv + span);
+            for (int e = sub; e < E; e += L)
+                mine[e] = make_key(fmaf(__uint_as_float(mine[e]), inv * unit, fmaf(s_bias[e], unit, 8388608.0f)), e);
+        } else {
+#pragma unroll 8
+            for (int e = sub; e < E; e += L) {
+                const float l = __uint_as_float(mine[e]);
+                check = fmaf(l, 0.0f, check);
+                const float s = reciprocal_fast(1.0f + exp2_fast(l * -kLog2e));
+                mine[e] = make_key(fmaf(s, steps, s_bias[e]), e);
+            }
+        }
+        bool unsure = false;
+        const auto same = [&](int e, int o) {  // equal values for certain
+            return row[e] == row[o] && (!a.S.bias || a.S.bias[e] == a.S.bias[o]);
+        };
+
+        if (grouped) {
+            __syncwarp();
+            unsigned *const mg = groups + tok * (G | 1);
+            const auto best = [&](int g, unsigned &first, unsigned &second) {
+                // lanes of a token start at different experts: other banks
+                const unsigned *const x = mine + g * per;
+                first = second = 0u;
+                int i = L == 1 ? 0 : sub % per;
+                for (int n = 0; n < per; ++n) {
+                    const unsigned v = x[i];
+                    second = max(second, min(first, v));
+                    first = max(first, v);
+                    if (++i == per) i = 0;
+                }
+            };
+            const bool two = a.S.group_top == 2;
+            for (int g = sub; g < G; g += L) {
+                unsigned first, second;
+                best(g, first, second);
+                mg[g] = ((first >> 9) + (two ? second >> 9 : 0u)) << 8 | (unsigned)(255 - g);
+            }
+            __syncwarp();
+            unsigned least = ~0u, most = 0u;  // kept, dropped
+            for (int g = sub; g < G; g += L) {
+                const unsigned v = mg[g];
+                int before = 0;
+#pragma unroll 8
+                for (int h = 0; h < G; ++h) before += mg[h] > v;
+                if (before < a.S.top_groups) least = min(least, v);
+                else most = max(most, v);
+            }
+            least = lanes_min<L>(least);
+            most = lanes_max<L>(most);
+            const int far = two ? 2 * near : near;
+            if ((int)(least >> 8) - (int)(most >> 8) <= far) {
+                // Groups near the border are in order only if they are equal:
+                // the best of each, whose lead over the rest is certain.
+                unsigned r1, r2;
+                best(255 - (int)(least & 255u), r1, r2);
+                const int a1 = key_id(r1), a2 = key_id(r2);
+                for (int g = sub; g < G; g += L) {
+                    const int v = (int)(mg[g] >> 8);
+                    if (v > (int)(most >> 8) + far || v < (int)(least >> 8) - far) continue;
+                    unsigned f1, f2;
+                    best(g, f1, f2);
+                    const int b1 = key_id(f1), b2 = key_id(f2);
+                    unsure |= two ? !((same(a1, b1) && same(a2, b2)) || (same(a1, b2) && same(a2, b1))) : !same(a1, b1);
+                    const unsigned last = two ? f2 : f1;
+                    for (int i = g * per; i < (g + 1) * per; ++i)
+                        unsure |= mine[i] < last && (int)(mine[i] >> 9) >= (int)(last >> 9) - near && !same(i, key_id(last));
+                }
+            }
+            __syncwarp();  // the lanes have looked at the keys
+            for (int g = sub; g < G; g += L)
+                if (mg[g] <= most)
+                    for (int i = 0; i < per; ++i) mine[g * per + i] = 0u;
+        }
+        __syncwarp();
+
+        // the largest keys
+        unsigned list[KL], rest = 0u;
+#pragma unroll
+        for (int u = 0; u < KL; ++u) list[u] = sub + u * L < E ? mine[sub + u * L] : 0u;
+        sort_keys(list);
+        for (int e0 = sub + KL * L; e0 < E; e0 += KL * L) {
+            unsigned x[KL];
+#pragma unroll
+            for (int u = 0; u < KL; ++u) x[u] = e0 + u * L < E ? mine[e0 + u * L] : 0u;
+            sort_keys(x);
+            merge_keys(list, x, rest);
+        }
+#pragma unroll
+        for (int d = 1; d < L; d *= 2) {
+            unsigned x[KL];
+#pragma unroll
+            for (int u = 0; u < KL; ++u) x[u] = __shfl_xor_sync(0xffffffffu, list[u], d);
+            rest = max(rest, __shfl_xor_sync(0xffffffffu, rest, d));
+            merge_keys(list, x, rest);
+        }
+        // neighbours that may be the other way round
+        unsigned last = 0u, after = rest;  // of the selected, and the best of the others
+        bool close = false;
+#pragma unroll
+        for (int u = 0; u < KL; ++u) {
+            if (u + 1 < KL)
+                if (u + 1 < k && (int)(list[u] >> 9) - (int)(list[u + 1] >> 9) <= near) close = true;
+            if (u == k - 1) last = list[u];
+            if (u == k) after = list[u];
+        }
+        const bool edge = after != 0u && (int)(last >> 9) - (int)(after >> 9) <= near;
+        if (close) {
+#pragma unroll
+            for (int u = 0; u + 1 < KL; ++u)
+                if (u + 1 < k && (int)(list[u] >> 9) - (int)(list[u + 1] >> 9) <= near)
+                    unsure |= !same(key_id(list[u]), key_id(list[u + 1]));
+        }
+        if (edge)
+            for (int e = sub; e < E; e += L)
+                if (mine[e] != 0u && mine[e] < last && (int)(mine[e] >> 9) >= (int)(last >> 9) - near)
+                    unsure |= !same(e, key_id(last));
+#pragma unroll
+        for (int u = 0; u < KL; ++u)
+            if (on && u < k && u % L == sub) sel[tok * k + u] = (unsigned)key_id(list[u]);
+        __syncwarp();
+        for (unsigned todo = __ballot_sync(0xffffffffu, on && unsure); todo != 0u;) {
+            const int owner = (__ffs(todo) - 1) / L;
+            todo &= ~((L == 32 ? ~0u : (1u << L) - 1u) << (owner * L));
+            const int id = select64(tile + owner * E, a, rows, lane);
+            if (lane < k) sel[owner * k + lane] = (unsigned)id;
+        }
+        __syncwarp();
+
+        // the gates: one a lane, in the order they are written
+        for (int i = lane; i < tokens * k; i += 32) {
+            const int r = i / k, id = (int)sel[i];
+            const float l = __ldg(tile + r * E + id);
+            score[i] = softmax ? __fdiv_rn(expf(l - soft[r].x), soft[r].y) : sigmoid(l);
+            a.idx[t0 * k + i] = id;
+            atomicAdd(&s_hist[id], 1u);
+        }
+        __syncwarp();
+        for (int i = lane; i < tokens * k; i += 32) {
+            float g = score[i];
+            if (a.S.renorm) {
+                const int first = i / k * k;
+                float sum = 0.0f;
+                for (int j = 0; j < k; ++j) sum += score[first + j];
+                g = __fdiv_rn(g, sum + kTiny);
+            }
+            a.gates[t0 * k + i] = g * a.S.scale;
+        }
+        __syncwarp();
+    }
+    if (check != 0.0f) record_status(ws, MOE_ERR_DEVICE_DATA);  // a NaN is not 0 either
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
         if (s_hist[e]) atomicAdd(&ws->gate_counts[e], s_hist[e]);
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) s_last = (atomicAdd(&ws->gate_ticket, 1u) == gridDim.x - 1);
     __syncthreads();
     if (!s_last) return;
-    publish_stats(ws, a.T, a.k, a.E, a.counts, a.aux, a.ent, [&](int e, unsigned c) {
+    publish_stats(ws, a.T, k, E, a.counts, a.aux, a.ent, [&](int e, unsigned c) {
         if (!a.S.bias_next) return;
-        const long long have = (long long)c * a.E, mean = (long long)a.T * a.k;
+        const long long have = (long long)c * E, mean = (long long)a.T * k;
         const float sign = have < mean ? 1.0f : have > mean ? -1.0f : 0.0f;
         a.S.bias_next[e] = __fadd_rn(a.S.bias ? a.S.bias[e] : 0.0f, __fmul_rn(a.S.bias_rate, sign));
     });
+}
+
+template <int KL, int L>
+cudaError_t launch_scored(const GateArgs &a, cudaStream_t s)
+{
+    const auto fn = gate_scored_kernel<KL, L>;
+    const int smem = kGateWarps * warp_words(a.E, a.S.groups, a.k, L) * 4;
+    cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
+    if (err != cudaSuccess) return err;
+    const int res = resident_grid(reinterpret_cast<const void *>(fn), 32 * kGateWarps, smem);
+    const long long per_block = kGateWarps * (32 / L);
+    long long blocks = ((long long)a.T + per_block - 1) / per_block;
+    if (blocks > res) blocks = res;
+    if (blocks < 1) blocks = 1;
+    return launch_pdl(fn, dim3((unsigned)blocks), dim3(32 * kGateWarps), (size_t)smem, s, a);
+}
+
+// Lanes of a token.  One, where the tokens alone fill the SMs: the lists are
+// not merged across lanes.  32 for the least latency of few tokens.
+int scored_lanes(int T, int E)
+{
+    const int sms = device_sm_count();
+    if (E <= 128 && T >= sms * 512) return 1;
+    return T >= sms * 32 ? 8 : 32;
+}
+
+template <int KL>
+cudaError_t launch_scored_lanes(const GateArgs &a, cudaStream_t s)
+{
+    const int lanes = scored_lanes(a.T, a.E);
+    if (lanes == 1) return launch_scored<KL, 1>(a, s);
+    if (lanes == 8) return launch_scored<KL, 8>(a, s);
+    return launch_scored<KL, 32>(a, s);
 }
 
 // --------------------------------------------------------------------------
@@ -329,11 +702,9 @@ cudaError_t launch_gate_scored(const float *logits, int T, int E, int k, const m
                                float *gates, int32_t *counts, double *aux, double *ent, void *ws, cudaStream_t s)
 {
     const GateArgs a = {logits, T, E, k, *S, idx, gates, counts, aux, ent, ws};
-    const int res = resident_grid(reinterpret_cast<const void *>(gate_scored_kernel), 32 * kWarps, 0);
-    long long blocks = ((long long)T + kWarps - 1) / kWarps;
-    if (blocks > res) blocks = res;
-    if (blocks < 1) blocks = 1;
-    return launch_pdl(gate_scored_kernel, dim3((unsigned)blocks), dim3(32 * kWarps), 0, s, a);
+    if (k <= 4) return launch_scored_lanes<4>(a, s);
+    if (k <= 8) return launch_scored_lanes<8>(a, s);
+    return launch_scored_lanes<16>(a, s);
 }
 
 cudaError_t launch_gate_scored_backward(const float *logits, const int32_t *idx, const float *d_gates, int T, int E,
