@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "gate_stats.cuh"
 #include "launchers.h"
+#include "tma.cuh"
 
 namespace moe {
 namespace {
@@ -127,6 +128,124 @@ __device__ __noinline__ int select64(const float *row, const GateArgs &a, void *
     return slot;
 }
 
+// The k best of a token's candidates in 64 bits, by a whole warp: the k ids in
+// sel, and the other kept experts whose key is at most `near` steps behind the
+// last one's.  The rest are behind for certain.  One candidate a lane; false
+// (and nothing done) if there are more.
+struct Kept {
+    const unsigned *keys;    // of the token's experts
+    const unsigned *groups;  // its kept groups
+    int per, count;          // experts of a group, and of all kept ones
+};
+
+// What a score in 64 bits takes of its row: the softmax's top and, where a bias
+// is added (without one the order is that of exp(l - top)), its sum.
+struct Row64 {
+    double top, sum;
+    __device__ Row64(const float *row, const GateArgs &a, int lane) : top(0.0), sum(1.0)
+    {
+        if (a.S.score != MOE_SCORE_SOFTMAX) return;
+        float t = -INFINITY;
+        for (int e = lane; e < a.E; e += 32) t = fmaxf(t, row[e]);
+        top = warp_max(t);
+        if (!a.S.bias) return;
+        sum = 0.0;
+        for (int e = lane; e < a.E; e += 32) sum += exp((double)row[e] - top);
+        sum = warp_sum(sum);
+    }
+    __device__ double value(const float *row, const GateArgs &a, int e) const
+    {
+        const double l = row[e];
+        double v = a.S.score == MOE_SCORE_SOFTMAX ? exp(l - top) / sum : 1.0 / (1.0 + exp(-l));
+        if (a.S.bias) v += (double)a.S.bias[e];
+        return v == v ? v : -INFINITY;
+    }
+};
+
+__device__ __forceinline__ double warp_max(double v)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+// The groups between `low` and `high`, of which some are kept, in 64 bits and
+// by a whole warp: those above stand first in `kept`, the best of these
+// follow.  False (and nothing done) if there are more than 32.
+__device__ __noinline__ bool groups_near(const float *row, const GateArgs &a, const unsigned *values, int low, int high,
+                                         unsigned *kept, int lane)
+{
+    const int G = a.S.groups, per = a.E / G;
+    int n = 0, above = 0, mine = -1;  // lane b: the border's group b
+    for (int g0 = 0; g0 < G; g0 += 32) {
+        const int g = g0 + lane, v = g < G ? (int)(values[g] >> 8) : 0;
+        above += __popc(__ballot_sync(0xffffffffu, g < G && v > high));
+        const unsigned who = __ballot_sync(0xffffffffu, g < G && v >= low && v <= high);
+        const int c = __popc(who);
+        // the (lane - n)-th of them
+        if (lane >= n && lane < n + c) mine = g0 + __fns(who, 0, lane - n + 1);
+        n += c;
+    }
+    if (n > 32) return false;
+    const Row64 r(row, a, lane);
+    double value = 0.0;
+    for (int b = 0; b < n; ++b) {
+        const int g = __shfl_sync(0xffffffffu, mine, b);
+        double first = -INFINITY, second = -INFINITY;
+        for (int i = lane; i < per; i += 32) {
+            const double v = r.value(row, a, g * per + i);
+            second = fmax(second, fmin(first, v));
+            first = fmax(first, v);
+        }
+        const double m = warp_max(first);
+        double sum = m;
+        if (a.S.group_top == 2) {
+            const int who = __ffs(__ballot_sync(0xffffffffu, first == m)) - 1;
+            sum += warp_max(lane == who ? second : first);
+        }
+        if (lane == b) value = sum;
+    }
+    int before = 0;
+    for (int b = 0; b < n; ++b) {
+        const double v = __shfl_sync(0xffffffffu, value, b);
+        const int g = __shfl_sync(0xffffffffu, mine, b);
+        before += v > value || (v == value && g < mine);
+    }
+    if (lane < n && above + before < a.S.top_groups) kept[above + before] = (unsigned)mine;
+    __syncwarp();
+    return true;
+}
+
+__device__ __noinline__ bool select_near(const float *row, const GateArgs &a, const Kept &kept, unsigned last, int near,
+                                         unsigned *sel, unsigned *list, int lane)
+{
+    int n = a.k;
+    if (lane < n) list[lane] = sel[lane];
+    for (int m0 = 0; m0 < kept.count; m0 += 32) {
+        const int m = m0 + lane, g = m / kept.per;
+        const int e = m < kept.count ? (int)kept.groups[g] * kept.per + m - g * kept.per : 0;
+        const unsigned key = m < kept.count ? kept.keys[e] : 0u;
+        const bool also = key != 0u && key < last && (int)(key >> 9) >= (int)(last >> 9) - near;
+        const unsigned who = __ballot_sync(0xffffffffu, also);
+        const int at = n + __popc(who & ((1u << lane) - 1u));
+        if (also && at < 32) list[at] = (unsigned)e;
+        n += __popc(who);
+    }
+    if (n > 32) return false;
+    __syncwarp();
+    const int id = lane < n ? (int)list[lane] : 0;
+    const double v = Row64(row, a, lane).value(row, a, id);
+    int before = 0;
+    for (int c = 0; c < n; ++c) {
+        const double o = __shfl_sync(0xffffffffu, v, c);
+        const int oid = __shfl_sync(0xffffffffu, id, c);
+        before += o > v || (o == v && oid < id);
+    }
+    if (lane < n && before < a.k) sel[before] = (unsigned)id;
+    __syncwarp();
+    return true;
+}
+
 __device__ __forceinline__ float sigmoid(float l)
 {
     const float e = expf(-fabsf(l));  // no overflow, and digits down to the subnormals
@@ -216,6 +335,13 @@ __device__ __forceinline__ F lanes_max(F v)
     return v;
 }
 template <int L>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+template <int L>
 __device__ __forceinline__ unsigned lanes_min(unsigned v)
 {
 #pragma unroll
@@ -243,22 +369,39 @@ __host__ __device__ inline int row_pitch(int E, int L)
 {
     return L == 1 ? (E | 1) : L == 32 ? E : (E + 31 - L) / 32 * 32 + L;
 }
-// Words of shared memory of a warp: keys and groups, where select64 works once
-// the lists are made; selected ids and scores, the softmax's top and sum.
-__host__ __device__ inline int key_words(int E, int G, int L)
+// Words of shared memory of a warp: keys, groups' values and kept groups,
+// where select64 works once the lists are made; selected ids, and a list for
+// select_near.
+__host__ __device__ inline int key_words(int E, int G, int top, int L)
 {
-    const int keys = 32 / L * (row_pitch(E, L) + (G | 1)), work = (Scratch::bytes(E, G) + 3) / 4;
-    return ((keys > work ? keys : work) + 1) / 2 * 2;
+    const int keys = 32 / L * (row_pitch(E, L) + (G | 1) + (top | 1)), work = (Scratch::bytes(E, G) + 3) / 4;
+    return ((keys > work ? keys : work) + 3) / 4 * 4;
 }
-__host__ __device__ inline int warp_words(int E, int G, int k, int L)
+__host__ __device__ inline int warp_words(int E, int G, int top, int k, int L)
 {
-    return key_words(E, G, L) + 32 / L * (2 * k + 2);
+    return key_words(E, G, top, L) + (32 / L * k + 3) / 4 * 4 + 32;
+}
+
+__device__ __forceinline__ void copy_async4(void *dst, const void *src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async16(void *dst, const void *src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async_all()
+{
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
 template <int KL, int L>
-__global__ void __launch_bounds__(32 * kGateWarps) gate_scored_kernel(const __grid_constant__ GateArgs a)
+__global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const __grid_constant__ GateArgs a)
 {
     constexpr int kTokens = 32 / L;
+    constexpr unsigned kAll = L == 32 ? ~0u : (1u << L) - 1u;  // the lanes of the first token
     extern __shared__ __align__(16) unsigned s_dyn[];
     __shared__ float s_bias[MOE_MAX_EXPERTS];  // less the lowest, in steps + 2^23 (sigmoid)
     __shared__ unsigned s_hist[MOE_MAX_EXPERTS];
@@ -268,11 +411,16 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_scored_kernel(const __gr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L, tok = lane / L;
     const int E = a.E, k = a.k, G = a.S.groups, per = E / G, pitch = row_pitch(E, L);
     const bool softmax = a.S.score == MOE_SCORE_SOFTMAX, grouped = a.S.top_groups < G;
-    unsigned *const rows = s_dyn + warp * warp_words(E, G, k, L);
-    unsigned *const groups = rows + kTokens * pitch;
-    unsigned *const sel = rows + key_words(E, G, L);  // [kTokens * k] ids, then their scores
-    float *const score = reinterpret_cast<float *>(sel + kTokens * k);
-    float2 *const soft = reinterpret_cast<float2 *>(score + kTokens * k);  // [kTokens] the softmax's top and sum
+    const int top = a.S.top_groups;
+    unsigned *const rows = s_dyn + warp * warp_words(E, G, top, k, L);
+    unsigned *const groups = rows + kTokens * pitch;              // values of the groups
+    unsigned *const kept_groups = groups + kTokens * (G | 1);
+    unsigned *const sel = rows + key_words(E, G, top, L) + tok * k;  // [k] ids of this lane's token
+    unsigned *const list = rows + key_words(E, G, top, L) + (kTokens * k + 3) / 4 * 4;
+    unsigned *const mine = rows + tok * pitch, *const mg = groups + tok * (G | 1);
+    unsigned *const mk = kept_groups + tok * (top | 1);
+    // the kept experts: those of `top` groups, or all
+    const Kept kept = {mine, mk, grouped ? per : E, grouped ? top * per : E};
     for (int e = threadIdx.x; e < E; e += blockDim.x) s_hist[e] = 0u;
     pdl_wait();
     pdl_launch_dependents();
@@ -316,14 +464,20 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_scored_kernel(const __gr
         const float *const tile = a.logits + t0 * E;
         const bool on = tok < tokens;
         const float *const row = tile + (on ? tok : 0) * E;  // of this lane's token
-        unsigned *const mine = rows + tok * pitch;
-        {
-            // the rows lie one after the other: a flat copy (zeros past the last token)
+        // zeros past the last token
+        if (L != 1 && (E & 3) == 0) {
+            for (int r = 0; r < kTokens; ++r)
+                for (int e = 4 * lane; e < E; e += 128)
+                    copy_async16(rows + r * pitch + e, tile + (r < tokens ? r * E + e : 0), r < tokens);
+        } else if (E >= 32) {
+            for (int r = 0; r < kTokens; ++r)
+                for (int e = lane; e < E; e += 32)
+                    copy_async4(rows + r * pitch + e, tile + (r < tokens ? r * E + e : 0), r < tokens);
+        } else {  // the rows lie one after the other: a flat copy
             int r = lane / E, c = lane - r * E;
             const int dr = 32 / E, dc = 32 - dr * E;
-#pragma unroll 8
             for (int i = lane; i < kTokens * E; i += 32) {
-                rows[r * pitch + c] = i < tokens * E ? __float_as_uint(__ldg(tile + i)) : 0u;
+                copy_async4(rows + r * pitch + c, tile + (i < tokens * E ? i : 0), i < tokens * E);
                 r += dr;
                 c += dc;
                 if (c >= E) {
@@ -332,13 +486,16 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_scored_kernel(const __gr
                 }
             }
         }
+        copy_async_all();
         __syncwarp();
 
         // keys in place of the logits
+        float total = 1.0f, peak = 0.0f, unit = 1.0f, scale = 1.0f;
         if (softmax) {
-            float top = -INFINITY;
-            for (int e = sub; e < E; e += L) top = fmaxf(top, __uint_as_float(mine[e]));
-            top = lanes_max<L>(top);
+            peak = -INFINITY;
+#pragma unroll 8
+            for (int e = sub; e < E; e += L) peak = fmaxf(peak, __uint_as_float(mine[e]));
+            peak = lanes_max<L>(peak);
             float part[8] = {};
             for (int e0 = sub; e0 < E; e0 += 8 * L) {
 #pragma unroll
@@ -347,38 +504,31 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_scored_kernel(const __gr
                     if (e < E) {
                         const float l = __uint_as_float(mine[e]);
                         check = fmaf(l, 0.0f, check);
-                        const float x = expf(l - top);
+                        const float x = expf(l - peak);
                         part[u] += x;
                         mine[e] = __float_as_uint(x);
                     }
                 }
             }
-            float sum = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
-#pragma unroll
-            for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            if (sub == 0) soft[tok] = make_float2(top, sum);
-            // without a bias the order is that of exp(l - top)
-            const float inv = a.S.bias ? reciprocal_fast(sum) : 1.0f;
-            const float unit = kSteps / (inv + span);
-            for (int e = sub; e < E; e += L)
-                mine[e] = make_key(fmaf(__uint_as_float(mine[e]), inv * unit, fmaf(s_bias[e], unit, 8388608.0f)), e);
-        } else {
-#pragma unroll 8
-            for (int e = sub; e < E; e += L) {
-                const float l = __uint_as_float(mine[e]);
-                check = fmaf(l, 0.0f, check);
-                const float s = reciprocal_fast(1.0f + exp2_fast(l * -kLog2e));
-                mine[e] = make_key(fmaf(s, steps, s_bias[e]), e);
-            }
+            total = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
+            total = lanes_sum<L>(total);
+            // without a bias the order is that of exp(l - peak)
+            const float inv = a.S.bias ? reciprocal_fast(total) : 1.0f;
+            unit = kSteps / (inv + span);
+            scale = inv * unit;
         }
-        bool unsure = false;
+        const auto key = [&](int e) {
+            const float x = __uint_as_float(mine[e]);
+            if (softmax) return make_key(fmaf(x, scale, fmaf(s_bias[e], unit, 8388608.0f)), e);
+            check = fmaf(x, 0.0f, check);
+            return make_key(fmaf(reciprocal_fast(1.0f + exp2_fast(x * -kLog2e)), steps, s_bias[e]), e);
+        };
+        bool unsure = false, unsure_groups = false;
         const auto same = [&](int e, int o) {  // equal values for certain
             return row[e] == row[o] && (!a.S.bias || a.S.bias[e] == a.S.bias[o]);
         };
-
         if (grouped) {
-            __syncwarp();
-            unsigned *const mg = groups + tok * (G | 1);
+            const bool two = a.S.group_top == 2;
             const auto best = [&](int g, unsigned &first, unsigned &second) {
                 // lanes of a token start at different experts: other banks
                 const unsigned *const x = mine + g * per;
@@ -391,21 +541,41 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_scored_kernel(const __gr
                     if (++i == per) i = 0;
                 }
             };
-            const bool two = a.S.group_top == 2;
-            for (int g = sub; g < G; g += L) {
-                unsigned first, second;
-                best(g, first, second);
-                mg[g] = ((first >> 9) + (two ? second >> 9 : 0u)) << 8 | (unsigned)(255 - g);
+            if (L == 1) {
+                for (int g = 0, e = 0; g < G; ++g) {
+                    unsigned first = 0u, second = 0u;
+#pragma unroll 4
+                    for (int i = 0; i < per; ++i, ++e) {
+                        const unsigned v = key(e);
+                        mine[e] = v;
+                        second = max(second, min(first, v));
+                        first = max(first, v);
+                    }
+                    mg[g] = ((first >> 9) + (two ? second >> 9 : 0u)) << 8 | (unsigned)(255 - g);
+                }
+            } else {
+#pragma unroll 4
+                for (int e = sub; e < E; e += L) mine[e] = key(e);
+                __syncwarp();
+                for (int g = sub; g < G; g += L) {
+                    unsigned first, second;
+                    best(g, first, second);
+                    mg[g] = ((first >> 9) + (two ? second >> 9 : 0u)) << 8 | (unsigned)(255 - g);
+                }
+                __syncwarp();
             }
-            __syncwarp();
             unsigned least = ~0u, most = 0u;  // kept, dropped
             for (int g = sub; g < G; g += L) {
                 const unsigned v = mg[g];
                 int before = 0;
 #pragma unroll 8
                 for (int h = 0; h < G; ++h) before += mg[h] > v;
-                if (before < a.S.top_groups) least = min(least, v);
-                else most = max(most, v);
+                if (before < top) {
+                    least = min(least, v);
+                    mk[before] = (unsigned)g;
+                } else {
+                    most = max(most, v);
+                }
             }
             least = lanes_min<L>(least);
             most = lanes_max<L>(most);
@@ -422,38 +592,71 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_scored_kernel(const __gr
                     unsigned f1, f2;
                     best(g, f1, f2);
                     const int b1 = key_id(f1), b2 = key_id(f2);
-                    unsure |= two ? !((same(a1, b1) && same(a2, b2)) || (same(a1, b2) && same(a2, b1))) : !same(a1, b1);
+                    unsure_groups |=
+                        two ? !((same(a1, b1) && same(a2, b2)) || (same(a1, b2) && same(a2, b1))) : !same(a1, b1);
                     const unsigned last = two ? f2 : f1;
                     for (int i = g * per; i < (g + 1) * per; ++i)
-                        unsure |= mine[i] < last && (int)(mine[i] >> 9) >= (int)(last >> 9) - near && !same(i, key_id(last));
+                        unsure_groups |=
+                            mine[i] < last && (int)(mine[i] >> 9) >= (int)(last >> 9) - near && !same(i, key_id(last));
                 }
             }
-            __syncwarp();  // the lanes have looked at the keys
-            for (int g = sub; g < G; g += L)
-                if (mg[g] <= most)
-                    for (int i = 0; i < per; ++i) mine[g * per + i] = 0u;
+            unsigned ask = __ballot_sync(0xffffffffu, on && unsure_groups);
+            unsure_groups = false;
+            while (ask != 0u) {
+                const int who = (__ffs(ask) - 1) / L;
+                ask &= ~(kAll << (who * L));
+                const int low = (int)(__shfl_sync(0xffffffffu, least, who * L) >> 8) - far;
+                const int high = (int)(__shfl_sync(0xffffffffu, most, who * L) >> 8) + far;
+                __syncwarp();
+                if (!groups_near(tile + who * E, a, groups + who * (G | 1), low, high, kept_groups + who * (top | 1), lane))
+                    unsure_groups |= tok == who;
+            }
+        } else {
+#pragma unroll 8
+            for (int e = sub; e < E; e += L) mine[e] = key(e);
+            if (sub == 0) mk[0] = 0u;
         }
         __syncwarp();
 
-        // the largest keys
-        unsigned list[KL], rest = 0u;
+        // The largest keys of the kept experts.  A lane takes every L-th of
+        // them, group after group.
+        unsigned lst[KL], rest = 0u;
+        {
+            int m = sub, i = sub, n = 0;
+            const unsigned *base = mine;
+            const auto move = [&] {  // to the group that expert m of the kept lies in
+                while (i >= kept.per) {
+                    i -= kept.per;
+                    ++n;
+                }
+                if (m < kept.count) base = mine + mk[n] * kept.per;
+            };
+            move();
+            const auto take = [&] {
+                const unsigned v = m < kept.count ? base[i] : 0u;
+                m += L;
+                i += L;
+                if (i >= kept.per) move();
+                return v;
+            };
 #pragma unroll
-        for (int u = 0; u < KL; ++u) list[u] = sub + u * L < E ? mine[sub + u * L] : 0u;
-        sort_keys(list);
-        for (int e0 = sub + KL * L; e0 < E; e0 += KL * L) {
-            unsigned x[KL];
+            for (int u = 0; u < KL; ++u) lst[u] = take();
+            sort_keys(lst);
+            for (int done = KL * L; done < kept.count; done += KL * L) {
+                unsigned x[KL];
 #pragma unroll
-            for (int u = 0; u < KL; ++u) x[u] = e0 + u * L < E ? mine[e0 + u * L] : 0u;
-            sort_keys(x);
-            merge_keys(list, x, rest);
+                for (int u = 0; u < KL; ++u) x[u] = take();
+                sort_keys(x);
+                merge_keys(lst, x, rest);
+            }
         }
 #pragma unroll
         for (int d = 1; d < L; d *= 2) {
             unsigned x[KL];
 #pragma unroll
-            for (int u = 0; u < KL; ++u) x[u] = __shfl_xor_sync(0xffffffffu, list[u], d);
+            for (int u = 0; u < KL; ++u) x[u] = __shfl_xor_sync(0xffffffffu, lst[u], d);
             rest = max(rest, __shfl_xor_sync(0xffffffffu, rest, d));
-            merge_keys(list, x, rest);
+            merge_keys(lst, x, rest);
         }
         // neighbours that may be the other way round
         unsigned last = 0u, after = rest;  // of the selected, and the best of the others
@@ -461,51 +664,94 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_scored_kernel(const __gr
 #pragma unroll
         for (int u = 0; u < KL; ++u) {
             if (u + 1 < KL)
-                if (u + 1 < k && (int)(list[u] >> 9) - (int)(list[u + 1] >> 9) <= near) close = true;
-            if (u == k - 1) last = list[u];
-            if (u == k) after = list[u];
+                if (u + 1 < k && (int)(lst[u] >> 9) - (int)(lst[u + 1] >> 9) <= near) close = true;
+            if (u == k - 1) last = lst[u];
+            if (u == k) after = lst[u];
         }
         const bool edge = after != 0u && (int)(last >> 9) - (int)(after >> 9) <= near;
         if (close) {
 #pragma unroll
             for (int u = 0; u + 1 < KL; ++u)
-                if (u + 1 < k && (int)(list[u] >> 9) - (int)(list[u + 1] >> 9) <= near)
-                    unsure |= !same(key_id(list[u]), key_id(list[u + 1]));
+                if (u + 1 < k && (int)(lst[u] >> 9) - (int)(lst[u + 1] >> 9) <= near)
+                    unsure |= !same(key_id(lst[u]), key_id(lst[u + 1]));
         }
         if (edge)
-            for (int e = sub; e < E; e += L)
-                if (mine[e] != 0u && mine[e] < last && (int)(mine[e] >> 9) >= (int)(last >> 9) - near)
-                    unsure |= !same(e, key_id(last));
+            for (int m = sub; m < kept.count; m += L) {
+                const int e = (int)mk[m / kept.per] * kept.per + m % kept.per;
+                if (mine[e] < last && (int)(mine[e] >> 9) >= (int)(last >> 9) - near) unsure |= !same(e, key_id(last));
+            }
+        constexpr int kMine = KL > L ? KL / L : 1;  // slots of a lane: sub, sub + L, ..
+        int id[kMine];
 #pragma unroll
         for (int u = 0; u < KL; ++u)
-            if (on && u < k && u % L == sub) sel[tok * k + u] = (unsigned)key_id(list[u]);
-        __syncwarp();
-        for (unsigned todo = __ballot_sync(0xffffffffu, on && unsure); todo != 0u;) {
-            const int owner = (__ffs(todo) - 1) / L;
-            todo &= ~((L == 32 ? ~0u : (1u << L) - 1u) << (owner * L));
-            const int id = select64(tile + owner * E, a, rows, lane);
-            if (lane < k) sel[owner * k + lane] = (unsigned)id;
-        }
-        __syncwarp();
-
-        // the gates: one a lane, in the order they are written
-        for (int i = lane; i < tokens * k; i += 32) {
-            const int r = i / k, id = (int)sel[i];
-            const float l = __ldg(tile + r * E + id);
-            score[i] = softmax ? __fdiv_rn(expf(l - soft[r].x), soft[r].y) : sigmoid(l);
-            a.idx[t0 * k + i] = id;
-            atomicAdd(&s_hist[id], 1u);
-        }
-        __syncwarp();
-        for (int i = lane; i < tokens * k; i += 32) {
-            float g = score[i];
-            if (a.S.renorm) {
-                const int first = i / k * k;
-                float sum = 0.0f;
-                for (int j = 0; j < k; ++j) sum += score[first + j];
-                g = __fdiv_rn(g, sum + kTiny);
+            if (u % L == sub) id[u / L] = key_id(lst[u]);
+        unsure = (unsure || unsure_groups) && on;
+        const unsigned any = __ballot_sync(0xffffffffu, unsure), by_group = __ballot_sync(0xffffffffu, on && unsure_groups);
+        if (any != 0u) {
+#pragma unroll
+            for (int u = 0; u < kMine; ++u)
+                if (sub + u * L < k) sel[sub + u * L] = (unsigned)id[u];
+            __syncwarp();
+            unsigned full = 0u;
+            for (unsigned todo = any; todo != 0u;) {
+                const int who = (__ffs(todo) - 1) / L;
+                const unsigned theirs = kAll << (who * L);
+                todo &= ~theirs;
+                if (!(by_group & theirs)) {
+                    const Kept their = {rows + who * pitch, kept_groups + who * (top | 1), kept.per, kept.count};
+                    const unsigned edge_key = __shfl_sync(0xffffffffu, last, who * L);
+                    if (select_near(tile + who * E, a, their, edge_key, near, sel + (who - tok) * k, list, lane)) continue;
+                }
+                full |= theirs;
             }
-            a.gates[t0 * k + i] = g * a.S.scale;
+            // these use the memory of the keys
+            while (full != 0u) {
+                const int who = (__ffs(full) - 1) / L;
+                full &= ~(kAll << (who * L));
+                const int got = select64(tile + who * E, a, rows, lane);
+                if (lane < k) sel[(who - tok) * k + lane] = (unsigned)got;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < kMine; ++u)
+                if (sub + u * L < k) id[u] = (int)sel[sub + u * L];
+        }
+
+        // the gates
+        float g[kMine], sum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+            g[u] = 0.0f;
+            if (on && sub + u * L < k) {
+                const float l = __ldg(row + id[u]);
+                g[u] = softmax ? __fdiv_rn(expf(l - peak), total) : sigmoid(l);
+                atomicAdd(&s_hist[id[u]], 1u);
+            }
+            sum += g[u];
+        }
+        const float norm = a.S.renorm ? lanes_sum<L>(sum) + kTiny : 1.0f;
+        if (on) {
+            int32_t *const oi = a.idx + (t0 + tok) * k;
+            float *const og = a.gates + (t0 + tok) * k;
+#pragma unroll
+            for (int u = 0; u < kMine; ++u) {
+                if (a.S.renorm) g[u] = __fdiv_rn(g[u], norm);
+                g[u] *= a.S.scale;
+            }
+            if (L == 1 && kMine % 4 == 0 && k == KL) {
+#pragma unroll
+                for (int u = 0; u + 3 < kMine; u += 4) {
+                    *reinterpret_cast<int4 *>(oi + u) = make_int4(id[u], id[u + 1], id[u + 2], id[u + 3]);
+                    *reinterpret_cast<float4 *>(og + u) = make_float4(g[u], g[u + 1], g[u + 2], g[u + 3]);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < kMine; ++u)
+                    if (sub + u * L < k) {
+                        oi[sub + u * L] = id[u];
+                        og[sub + u * L] = g[u];
+                    }
+            }
         }
         __syncwarp();
     }
@@ -530,7 +776,7 @@ template <int KL, int L>
 cudaError_t launch_scored(const GateArgs &a, cudaStream_t s)
 {
     const auto fn = gate_scored_kernel<KL, L>;
-    const int smem = kGateWarps * warp_words(a.E, a.S.groups, a.k, L) * 4;
+    const int smem = kGateWarps * warp_words(a.E, a.S.groups, a.S.top_groups, a.k, L) * 4;
     cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
     if (err != cudaSuccess) return err;
     const int res = resident_grid(reinterpret_cast<const void *>(fn), 32 * kGateWarps, smem);
