@@ -249,7 +249,8 @@ __device__ __noinline__ bool select_near(const float *row, const GateArgs &a, co
 __device__ __forceinline__ float sigmoid(float l)
 {
     const float e = expf(-fabsf(l));  // no overflow, and digits down to the subnormals
-    return __fdiv_rn(l < 0.0f ? e : 1.0f, 1.0f + e);
+    const float q = __frcp_rn(1.0f + e);
+    return l < 0.0f ? e * q : q;
 }
 
 // --------------------------------------------------------------------------
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
         const bool on = tok < tokens;
         const float *const row = tile + (on ? tok : 0) * E;  // of this lane's token
         // zeros past the last token
-        if (L != 1 && (E & 3) == 0) {
+        if (L % 4 == 0 && (E & 3) == 0) {
             for (int r = 0; r < kTokens; ++r)
                 for (int e = 4 * lane; e < E; e += 128)
                     copy_async16(rows + r * pitch + e, tile + (r < tokens ? r * E + e : 0), r < tokens);
@@ -718,26 +719,24 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
         }
 
         // the gates
+        const float part_of = __frcp_rn(total);
         float g[kMine], sum = 0.0f;
 #pragma unroll
         for (int u = 0; u < kMine; ++u) {
             g[u] = 0.0f;
             if (on && sub + u * L < k) {
                 const float l = __ldg(row + id[u]);
-                g[u] = softmax ? __fdiv_rn(expf(l - peak), total) : sigmoid(l);
+                g[u] = softmax ? expf(l - peak) * part_of : sigmoid(l);
                 atomicAdd(&s_hist[id[u]], 1u);
             }
             sum += g[u];
         }
-        const float norm = a.S.renorm ? lanes_sum<L>(sum) + kTiny : 1.0f;
+        const float norm = a.S.renorm ? __frcp_rn(lanes_sum<L>(sum) + kTiny) : 1.0f;
         if (on) {
             int32_t *const oi = a.idx + (t0 + tok) * k;
             float *const og = a.gates + (t0 + tok) * k;
 #pragma unroll
-            for (int u = 0; u < kMine; ++u) {
-                if (a.S.renorm) g[u] = __fdiv_rn(g[u], norm);
-                g[u] *= a.S.scale;
-            }
+            for (int u = 0; u < kMine; ++u) g[u] = g[u] * norm * a.S.scale;
             if (L == 1 && kMine % 4 == 0 && k == KL) {
 #pragma unroll
                 for (int u = 0; u + 3 < kMine; u += 4) {
@@ -813,9 +812,13 @@ cudaError_t launch_scored_lanes(const GateArgs &a, cudaStream_t s)
 //   softmax: dl[e] = s_e ([e = sel_j] ds_j - X),  X = sum_j ds_j s_j;
 //            renorm: X = c (D / N) (tiny / N), without the difference of
 //            two nearly equal sums
-// A group of G lanes per token (E rounded up to a power of two, at most 32),
-// lane i of it has experts i, i + G, ... and, if i < k, slot i.  Sigmoid reads
-// the selected logits only.  Bound by HBM: d_logits is written whole.
+// A group of G lanes per token; lane i of it has the units i, i + G, .. of VEC
+// experts (4 where E is a multiple of 4; up to 16 experts a lane, so that a
+// warp's sums serve several tokens) and, if i < k, slot i.  The row is written
+// without its selected experts, which slot i's lane then writes: comparing
+// every expert with every slot took half of the instructions.  Sigmoid reads
+// the selected logits only.  Bound by HBM: d_logits is written whole.  131072
+// tokens, 128 experts, softmax, 138 MB: 24.3 us (5.7 TB/s; 52 us before).
 // --------------------------------------------------------------------------
 constexpr int kBwdThreads = 256;
 
@@ -834,16 +837,16 @@ __device__ __forceinline__ float group_max(float v)
     return v;
 }
 
-template <bool SOFTMAX, int G, int EPL>
+template <bool SOFTMAX, int G, int EPL, int VEC>
 __global__ void __launch_bounds__(kBwdThreads)
 gate_scored_bwd_kernel(const float *__restrict__ logits, const int32_t *__restrict__ idx,
                        const float *__restrict__ d_gates, long long T, int E, int k, int renorm, float scale,
-                       float *__restrict__ d_logits, void *ws)
+                       float *d_logits, void *ws)
 {
+    constexpr int kTokens = 32 / G, N = EPL * VEC;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, sub = lane & (G - 1);
-    constexpr int kTokens = 32 / G;  // of a warp
     const long long step = (long long)gridDim.x * (kBwdThreads / 32) * kTokens;
     for (long long t0 = ((long long)blockIdx.x * (kBwdThreads / 32) + (threadIdx.x >> 5)) * kTokens; t0 < T; t0 += step) {
         const long long t = t0 + lane / G;
@@ -853,6 +856,26 @@ gate_scored_bwd_kernel(const float *__restrict__ logits, const int32_t *__restri
         if (valid && sub < k) {
             sel = __ldg(idx + t * k + sub);
             d = __ldg(d_gates + t * k + sub);
+        }
+        float out[N];
+        if (SOFTMAX) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int e = (sub + G * i) * VEC;
+                const float *at = logits + t * E + e;
+                if constexpr (VEC == 4) {
+                    const float4 v = valid && e < E ? __ldg(reinterpret_cast<const float4 *>(at))
+                                                    : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                    out[4 * i] = v.x;
+                    out[4 * i + 1] = v.y;
+                    out[4 * i + 2] = v.z;
+                    out[4 * i + 3] = v.w;
+                } else {
+                    out[i] = valid && e < E ? __ldg(at) : -INFINITY;
+                }
+            }
+        }
+        if (valid && sub < k) {
             if (sel < 0 || sel >= E) {
                 record_status(ws, MOE_ERR_DEVICE_DATA);
                 sel = -1;
@@ -861,23 +884,21 @@ gate_scored_bwd_kernel(const float *__restrict__ logits, const int32_t *__restri
                 l = __ldg(logits + t * E + sel);
             }
         }
-        float out[EPL], s = 0.0f, slope = 0.0f;
+        float s = 0.0f, slope = 0.0f;
         if (SOFTMAX) {
             float m = -INFINITY, z = 0.0f;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                out[i] = valid && sub + G * i < E ? __ldg(logits + t * E + sub + G * i) : -INFINITY;
-                m = fmaxf(m, out[i]);
-            }
+            for (int i = 0; i < N; ++i) m = fmaxf(m, out[i]);
             m = group_max<G>(m);
+            if (!valid) m = 0.0f;  // exp(-inf - 0) = 0, as past the last expert
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                out[i] = valid && sub + G * i < E ? expf(out[i] - m) : 0.0f;
+            for (int i = 0; i < N; ++i) {
+                out[i] = expf(out[i] - m);
                 z += out[i];
             }
             z = __fdiv_rn(1.0f, group_sum<G>(z));
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) out[i] *= z;
+            for (int i = 0; i < N; ++i) out[i] *= z;
             if (sel >= 0) s = expf(l - m) * z;
         } else if (sel >= 0) {
             const float e = expf(-fabsf(l)), q = __fdiv_rn(1.0f, 1.0f + e);  // s (1 - s) = e / (1 + e)^2
@@ -891,55 +912,76 @@ gate_scored_bwd_kernel(const float *__restrict__ logits, const int32_t *__restri
             all = all * n * (kTiny * n);
         }
         const float own = sel < 0 ? 0.0f : ds * (SOFTMAX ? s : slope);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) out[i] = SOFTMAX ? -out[i] * all : 0.0f;
+        float sum = SOFTMAX ? -s * all : 0.0f;  // of the expert's slots, in their order
         for (int j = 0; j < k; ++j) {
             const int ej = __shfl_sync(0xffffffffu, sel, j, G);
             const float oj = __shfl_sync(0xffffffffu, own, j, G);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (ej == sub + G * i) out[i] += oj;
+            if (ej == sel) sum += oj;
         }
         if (valid)
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (sub + G * i < E) d_logits[t * E + sub + G * i] = out[i];
+            for (int i = 0; i < EPL; ++i) {
+                const int e = (sub + G * i) * VEC;
+                float *at = d_logits + t * E + e;
+                if (e < E) {
+                    if constexpr (VEC == 4)
+                        *reinterpret_cast<float4 *>(at) =
+                            SOFTMAX ? make_float4(-out[4 * i] * all, -out[4 * i + 1] * all, -out[4 * i + 2] * all,
+                                                  -out[4 * i + 3] * all)
+                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    else
+                        *at = SOFTMAX ? -out[i] * all : 0.0f;
+                }
+            }
+        __syncwarp();  // the row before its selected experts
+        if (sel >= 0) d_logits[t * E + sel] = sum;
     }
 }
 
-template <bool SOFTMAX, int G, int EPL>
-cudaError_t launch_bwd(const float *logits, const int32_t *idx, const float *d_gates, int T, int E, int k, int renorm,
-                       float scale, float *d_logits, void *ws, cudaStream_t s)
+struct BwdArgs {
+    const float *logits;
+    const int32_t *idx;
+    const float *d_gates;
+    int T, E, k, renorm;
+    float scale;
+    float *d_logits;
+    void *ws;
+};
+
+template <bool SOFTMAX, int G, int EPL, int VEC>
+cudaError_t launch_bwd(const BwdArgs &a, cudaStream_t s)
 {
-    const auto fn = gate_scored_bwd_kernel<SOFTMAX, G, EPL>;
+    const auto fn = gate_scored_bwd_kernel<SOFTMAX, G, EPL, VEC>;
     const long long per_block = (kBwdThreads / 32) * (32 / G);
-    const long long need = ((long long)T + per_block - 1) / per_block;
+    const long long need = ((long long)a.T + per_block - 1) / per_block;
     const int res = resident_grid(reinterpret_cast<const void *>(fn), kBwdThreads, 0);
-    return launch_pdl(fn, dim3((unsigned)(need < res ? need : res)), dim3(kBwdThreads), 0, s, logits, idx, d_gates,
-                      (long long)T, E, k, renorm, scale, d_logits, ws);
+    return launch_pdl(fn, dim3((unsigned)(need < res ? need : res)), dim3(kBwdThreads), 0, s, a.logits, a.idx, a.d_gates,
+                      (long long)a.T, a.E, a.k, a.renorm, a.scale, a.d_logits, a.ws);
+}
+
+template <bool SOFTMAX, int G>
+cudaError_t launch_bwd_units(const BwdArgs &a, int each, cudaStream_t s)
+{
+    if (each <= 1) return launch_bwd<SOFTMAX, G, 1, 4>(a, s);
+    if (each <= 2) return launch_bwd<SOFTMAX, G, 2, 4>(a, s);
+    return launch_bwd<SOFTMAX, G, 4, 4>(a, s);
 }
 
 template <bool SOFTMAX>
-cudaError_t launch_bwd_e(const float *logits, const int32_t *idx, const float *d_gates, int T, int E, int k,
-                         int renorm, float scale, float *d_logits, void *ws, cudaStream_t s)
+cudaError_t launch_bwd_e(const BwdArgs &a, cudaStream_t s)
 {
-#define MOE_BWD(G, EPL) return launch_bwd<SOFTMAX, G, EPL>(logits, idx, d_gates, T, E, k, renorm, scale, d_logits, ws, s)
-    if (E <= 1) MOE_BWD(1, 1);
-    if (E <= 2) MOE_BWD(2, 1);
-    if (E <= 4) MOE_BWD(4, 1);
-    if (E <= 8) MOE_BWD(8, 1);
-    if (E <= 16) MOE_BWD(16, 1);
-    switch ((E + 31) / 32) {
-    case 1: MOE_BWD(32, 1);
-    case 2: MOE_BWD(32, 2);
-    case 3: MOE_BWD(32, 3);
-    case 4: MOE_BWD(32, 4);
-    case 5: MOE_BWD(32, 5);
-    case 6: MOE_BWD(32, 6);
-    case 7: MOE_BWD(32, 7);
-    default: MOE_BWD(32, 8);
+    if (a.E % 4 == 0) {  // up to 4 units a lane, and a lane for every slot
+        const int units = a.E / 4, lanes = (units + 3) / 4 > a.k ? (units + 3) / 4 : a.k;
+        if (lanes <= 4) return launch_bwd_units<SOFTMAX, 4>(a, (units + 3) / 4, s);
+        if (lanes <= 8) return launch_bwd_units<SOFTMAX, 8>(a, (units + 7) / 8, s);
+        return launch_bwd_units<SOFTMAX, 16>(a, (units + 15) / 16, s);
     }
-#undef MOE_BWD
+    const int lanes = a.E;  // k <= E
+    if (lanes <= 8) return launch_bwd<SOFTMAX, 8, 1, 1>(a, s);
+    if (lanes <= 32) return launch_bwd<SOFTMAX, 16, 2, 1>(a, s);
+    if (lanes <= 64) return launch_bwd<SOFTMAX, 16, 4, 1>(a, s);
+    if (lanes <= 128) return launch_bwd<SOFTMAX, 16, 8, 1>(a, s);
+    return launch_bwd<SOFTMAX, 32, 8, 1>(a, s);
 }
 
 }  // namespace
@@ -957,9 +999,8 @@ cudaError_t launch_gate_scored_backward(const float *logits, const int32_t *idx,
                                         int k, const moe_scoring *S, float *d_logits, void *ws, cudaStream_t s)
 {
     if (T == 0) return cudaSuccess;
-    return S->score == MOE_SCORE_SOFTMAX
-               ? launch_bwd_e<true>(logits, idx, d_gates, T, E, k, S->renorm, S->scale, d_logits, ws, s)
-               : launch_bwd_e<false>(logits, idx, d_gates, T, E, k, S->renorm, S->scale, d_logits, ws, s);
+    const BwdArgs a = {logits, idx, d_gates, T, E, k, S->renorm, S->scale, d_logits, ws};
+    return S->score == MOE_SCORE_SOFTMAX ? launch_bwd_e<true>(a, s) : launch_bwd_e<false>(a, s);
 }
 
 }  // namespace moe
