@@ -267,9 +267,10 @@ __device__ __forceinline__ float sigmoid(float l)
 // way round.  Equal logits with equal biases are equal values, and rightly in
 // the order of their ids; whatever else is that close goes to select64.
 //
-// A warp reads its tokens' logits to shared memory, and the keys take their
-// place there.  Rows start in other banks: row pitch = L modulo 32 (odd, for
-// L = 1).
+// A warp copies its tokens' logits to shared memory, and the keys take their
+// place there.  With several lanes to a token the rows start in other banks:
+// row pitch = L modulo 32.  With one lane the rows lie as in memory, and the
+// lanes whose rows start in the same bank start at different experts.
 // --------------------------------------------------------------------------
 constexpr float kSteps = 8388600.0f;  // of q, below 2^23
 
@@ -368,7 +369,7 @@ constexpr int kGateWarps = 4;
 
 __host__ __device__ inline int row_pitch(int E, int L)
 {
-    return L == 1 ? (E | 1) : L == 32 ? E : (E + 31 - L) / 32 * 32 + L;
+    return L == 1 || L == 32 ? E : (E + 31 - L) / 32 * 32 + L;
 }
 // Words of shared memory of a warp: keys, groups' values and kept groups,
 // where select64 works once the lists are made; selected ids, and a list for
@@ -376,13 +377,19 @@ __host__ __device__ inline int row_pitch(int E, int L)
 __host__ __device__ inline int key_words(int E, int G, int top, int L)
 {
     const int keys = 32 / L * (row_pitch(E, L) + (G | 1) + (top | 1)), work = (Scratch::bytes(E, G) + 3) / 4;
-    return ((keys > work ? keys : work) + 3) / 4 * 4;
+    return ((keys > work ? keys : work) + 15) / 16 * 16;
 }
 __host__ __device__ inline int warp_words(int E, int G, int top, int k, int L)
 {
-    return key_words(E, G, top, L) + (32 / L * k + 3) / 4 * 4 + 32;
+    return key_words(E, G, top, L) + (32 / L * k + 15) / 16 * 16 + 32;
 }
 
+__device__ __forceinline__ unsigned lds_u32(unsigned at)
+{
+    unsigned v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
 __device__ __forceinline__ void copy_async4(void *dst, const void *src, bool there)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 4 : 0)
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
 {
     constexpr int kTokens = 32 / L;
     constexpr unsigned kAll = L == 32 ? ~0u : (1u << L) - 1u;  // the lanes of the first token
-    extern __shared__ __align__(16) unsigned s_dyn[];
+    extern __shared__ __align__(64) unsigned s_dyn[];
     __shared__ float s_bias[MOE_MAX_EXPERTS];  // less the lowest, in steps + 2^23 (sigmoid)
     __shared__ unsigned s_hist[MOE_MAX_EXPERTS];
     __shared__ float s_low[kGateWarps], s_high[kGateWarps];
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
     unsigned *const groups = rows + kTokens * pitch;              // values of the groups
     unsigned *const kept_groups = groups + kTokens * (G | 1);
     unsigned *const sel = rows + key_words(E, G, top, L) + tok * k;  // [k] ids of this lane's token
-    unsigned *const list = rows + key_words(E, G, top, L) + (kTokens * k + 3) / 4 * 4;
+    unsigned *const list = rows + key_words(E, G, top, L) + (kTokens * k + 15) / 16 * 16;
     unsigned *const mine = rows + tok * pitch, *const mg = groups + tok * (G | 1);
     unsigned *const mk = kept_groups + tok * (top | 1);
     // the kept experts: those of `top` groups, or all
@@ -460,13 +467,21 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
     const int near = softmax ? (a.S.bias ? kNearSoftmaxBias : kNearSoftmax) : kNearSigmoid;
 
     const long long stride = (long long)gridDim.x * kGateWarps * kTokens;
-    for (long long t0 = ((long long)blockIdx.x * kGateWarps + warp) * kTokens; t0 < a.T; t0 += stride) {
+    // L == 1: where this lane starts in its row (see above)
+    const int common = E & -E & 31 ? E & -E : 32, turn = L == 1 ? lane * common / 32 : 0;
+    const int turn_group = turn / kept.per, turn_in = turn - turn_group * kept.per;
+    // the logits of a warp's tokens; zeros past the last
+    const auto load = [&](long long t0) {
         const int tokens = (int)min((long long)kTokens, a.T - t0);
         const float *const tile = a.logits + t0 * E;
-        const bool on = tok < tokens;
-        const float *const row = tile + (on ? tok : 0) * E;  // of this lane's token
-        // zeros past the last token
-        if (L % 4 == 0 && (E & 3) == 0) {
+        if (L == 1) {
+            const int there = tokens * E, whole = there & ~3;
+#pragma unroll 4
+            for (int i = 4 * lane; i < 32 * E; i += 128)
+                if (i < whole || i >= there) copy_async16(rows + i, i < whole ? tile + i : tile, i < whole);
+            if (whole != there && lane < 4) copy_async4(rows + whole + lane, tile + (whole + lane < there ? whole + lane : 0),
+                                                        whole + lane < there);
+        } else if (L % 4 == 0 && (E & 3) == 0) {
             for (int r = 0; r < kTokens; ++r)
                 for (int e = 4 * lane; e < E; e += 128)
                     copy_async16(rows + r * pitch + e, tile + (r < tokens ? r * E + e : 0), r < tokens);
@@ -487,22 +502,33 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
                 }
             }
         }
+    };
+    const long long first_token = ((long long)blockIdx.x * kGateWarps + warp) * kTokens;
+    if (first_token < a.T) load(first_token);
+    for (long long t0 = first_token; t0 < a.T; t0 += stride) {
+        const int tokens = (int)min((long long)kTokens, a.T - t0);
+        const float *const tile = a.logits + t0 * E;
+        const bool on = tok < tokens;
+        const float *const row = tile + (on ? tok : 0) * E;  // of this lane's token
         copy_async_all();
         __syncwarp();
 
         // keys in place of the logits
         float total = 1.0f, peak = 0.0f, unit = 1.0f, scale = 1.0f;
         if (softmax) {
+            // a lane's n-th expert
+            const auto nth = [&](int n) { return L == 1 ? (n + turn >= E ? n + turn - E : n + turn) : sub + n * L; };
+            const int each = L == 1 ? E : (E - sub + L - 1) / L;
             peak = -INFINITY;
 #pragma unroll 8
-            for (int e = sub; e < E; e += L) peak = fmaxf(peak, __uint_as_float(mine[e]));
+            for (int n = 0; n < each; ++n) peak = fmaxf(peak, __uint_as_float(mine[nth(n)]));
             peak = lanes_max<L>(peak);
             float part[8] = {};
-            for (int e0 = sub; e0 < E; e0 += 8 * L) {
+            for (int n0 = 0; n0 < each; n0 += 8) {
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    const int e = e0 + u * L;
-                    if (e < E) {
+                    if (n0 + u < each) {
+                        const int e = nth(n0 + u);
                         const float l = __uint_as_float(mine[e]);
                         check = fmaf(l, 0.0f, check);
                         const float x = expf(l - peak);
@@ -543,16 +569,20 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
                 }
             };
             if (L == 1) {
-                for (int g = 0, e = 0; g < G; ++g) {
+                int g = turn_group;
+                for (int n = 0; n < G; ++n) {
                     unsigned first = 0u, second = 0u;
-#pragma unroll 4
-                    for (int i = 0; i < per; ++i, ++e) {
-                        const unsigned v = key(e);
-                        mine[e] = v;
+                    int i = turn_in;
+#pragma unroll 8
+                    for (int m = 0; m < per; ++m) {
+                        const unsigned v = key(g * per + i);
+                        mine[g * per + i] = v;
                         second = max(second, min(first, v));
                         first = max(first, v);
+                        i = i + 1 == per ? 0 : i + 1;
                     }
                     mg[g] = ((first >> 9) + (two ? second >> 9 : 0u)) << 8 | (unsigned)(255 - g);
+                    g = g + 1 == G ? 0 : g + 1;
                 }
             } else {
 #pragma unroll 4
@@ -613,8 +643,13 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
                     unsure_groups |= tok == who;
             }
         } else {
+            int e = L == 1 ? turn : sub;
 #pragma unroll 8
-            for (int e = sub; e < E; e += L) mine[e] = key(e);
+            for (int n = sub; n < E; n += L) {
+                mine[e] = key(e);
+                e += L;
+                if (L == 1 && e == E) e = 0;
+            }
             if (sub == 0) mk[0] = 0u;
         }
         __syncwarp();
@@ -622,7 +657,32 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
         // The largest keys of the kept experts.  A lane takes every L-th of
         // them, group after group.
         unsigned lst[KL], rest = 0u;
-        {
+        if (L == 1 && kept.per % KL == 0) {
+            // whole lists at a time.  The lanes take a list's keys in different
+            // orders: other banks
+            const unsigned from = (unsigned)(lane & (KL - 1)) * 4u;
+#pragma unroll
+            for (int u = 0; u < KL; ++u) lst[u] = 0u;
+            int n = 0, c = 0;
+            for (int done = 0; done < kept.count; done += KL) {
+                unsigned x[KL];
+                const unsigned at = smem_addr(mine + mk[n] * kept.per + c) + from;
+#pragma unroll
+                for (int u = 0; u < KL; ++u) x[u] = lds_u32(at ^ (4u * u));
+                sort_keys(x);
+                if (done == 0) {
+#pragma unroll
+                    for (int u = 0; u < KL; ++u) lst[u] = x[u];
+                } else {
+                    merge_keys(lst, x, rest);
+                }
+                c += KL;
+                if (c == kept.per) {
+                    c = 0;
+                    ++n;
+                }
+            }
+        } else {
             int m = sub, i = sub, n = 0;
             const unsigned *base = mine;
             const auto move = [&] {  // to the group that expert m of the kept lies in
@@ -717,6 +777,9 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
             for (int u = 0; u < kMine; ++u)
                 if (sub + u * L < k) id[u] = (int)sel[sub + u * L];
         }
+
+        __syncwarp();
+        if (t0 + stride < a.T) load(t0 + stride);  // the keys are done with
 
         // the gates
         const float part_of = __frcp_rn(total);
