@@ -284,37 +284,44 @@ class Scoring:
 
     def c(self, bias=None, bias_next=None, bias_rate: float = 0.0) -> moe_scoring:
         return moe_scoring(MOE_SCORE_SOFTMAX if self.score == "softmax" else MOE_SCORE_SIGMOID, self.groups,
-                           self.top_groups, self.group_top, int(self.renorm), self.scale, bias_rate, bias, bias_next)
+                           self.top_groups, self.group_top, self.renorm, self.scale, bias_rate, bias, bias_next)
 
 
-def _sized(t, dtype, numel: int, name: str, device):
+def _sized(t, dtype, numel: int, name: str, index: int):
     """The address of a contiguous tensor of at least `numel` values of this
-    type on `device`; None for None."""
+    type on the CUDA device `index`; None for None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype is not dtype:
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.numel() >= numel and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name}: expected a torch.Tensor") from None
+    if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
     if t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} values, needs {numel}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: must be contiguous")
 
 
-def _here(t, name: str):
+def _here(t, name: str) -> int:
     """The current CUDA device, where `t` has to be: a launch goes there."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    if torch._C._cuda_getDevice() != t.device.index:
+    index = t.get_device()
+    if torch._C._cuda_getDevice() != index:
         raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}: make its "
                          "current (torch.cuda.device)")
-    return t.device
+    return index
+
+
+def _raw_stream(stream, index: int):
+    """The handle of `stream`, or of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def moe_gate_scored(logits, k: int, scoring: Scoring, bias, topk_idx, gates, expert_counts, aux_loss, entropy, ws, *,
@@ -326,18 +333,16 @@ def moe_gate_scored(logits, k: int, scoring: Scoring, bias, topk_idx, gates, exp
     if logits.dim() != 2:
         raise ValueError(f"logits: expected [T, E], got {tuple(logits.shape)}")
     T, E = logits.shape
-    f32 = torch.float32
+    f32, i32, f64 = torch.float32, torch.int32, torch.float64
     for t, name in ((bias, "bias"), (bias_next, "bias_next")):
         if t is not None and t.numel() != E:
             raise ValueError(f"{name}: {t.numel()} values for {E} experts")
     c = scoring.c(_sized(bias, f32, E, "bias", dev), _sized(bias_next, f32, E, "bias_next", dev), bias_rate)
     _check(lib().moe_gate_scored(_sized(logits, f32, T * E, "logits", dev), T, E, k, c,
-                                 _sized(topk_idx, torch.int32, T * k, "topk_idx", dev),
-                                 _sized(gates, f32, T * k, "gates", dev),
-                                 _sized(expert_counts, torch.int32, E, "expert_counts", dev),
-                                 _sized(aux_loss, torch.float64, 1, "aux_loss", dev),
-                                 _sized(entropy, torch.float64, 1, "entropy", dev),
-                                 _sized(ws, torch.uint8, 1, "ws", dev), ws.numel(), _stream(stream)),
+                                 _sized(topk_idx, i32, T * k, "topk_idx", dev), _sized(gates, f32, T * k, "gates", dev),
+                                 _sized(expert_counts, i32, E, "expert_counts", dev),
+                                 _sized(aux_loss, f64, 1, "aux_loss", dev), _sized(entropy, f64, 1, "entropy", dev),
+                                 _sized(ws, torch.uint8, 1, "ws", dev), ws.numel(), _raw_stream(stream, dev)),
            "moe_gate_scored")
 
 
@@ -348,11 +353,12 @@ def moe_gate_scored_backward(logits, topk_idx, d_gates, scoring: Scoring, d_logi
         raise ValueError("logits and topk_idx: expected [T, E] and [T, k]")
     T, E = logits.shape
     k = topk_idx.shape[1]
-    _check(lib().moe_gate_scored_backward(_sized(logits, torch.float32, T * E, "logits", dev),
+    f32 = torch.float32
+    _check(lib().moe_gate_scored_backward(_sized(logits, f32, T * E, "logits", dev),
                                           _sized(topk_idx, torch.int32, T * k, "topk_idx", dev),
-                                          _sized(d_gates, torch.float32, T * k, "d_gates", dev), T, E, k, scoring.c(),
-                                          _sized(d_logits, torch.float32, T * E, "d_logits", dev),
-                                          _sized(ws, torch.uint8, 1, "ws", dev), ws.numel(), _stream(stream)),
+                                          _sized(d_gates, f32, T * k, "d_gates", dev), T, E, k, scoring.c(),
+                                          _sized(d_logits, f32, T * E, "d_logits", dev),
+                                          _sized(ws, torch.uint8, 1, "ws", dev), ws.numel(), _raw_stream(stream, dev)),
            "moe_gate_scored_backward")
 
 
@@ -368,8 +374,8 @@ def moe_dispatch_fp4(x, T: int, H: int, layout: "Layout", codes, scales, stream=
     r = layout.c.r_max
     _check(lib().moe_dispatch_fp4(_sized(x, torch.bfloat16, T * H, "x", dev), T, H, ctypes.byref(layout.c),
                                   _sized(codes, torch.uint8, r * (H // 2), "codes", dev),
-                                  _sized(scales, torch.uint8, r * fp4_pitch(H), "scales", dev), _stream(stream)),
-           "moe_dispatch_fp4")
+                                  _sized(scales, torch.uint8, r * fp4_pitch(H), "scales", dev),
+                                  _raw_stream(stream, dev)), "moe_dispatch_fp4")
 
 
 def _check_layout_fits(layout: "Layout", T: int, E: int, k: int, P: int, capacity: int, where: str):

@@ -261,6 +261,11 @@ __device__ __forceinline__ float sigmoid(float l)
 // of KL keys are sorted by Batcher's networks, merged, and merged across the
 // lanes of a token.
 //
+// What bounds it: instructions (110 a token at 64 experts) and, with 20 warps an SM, their latency; HBM at a fifth.  262144 tokens,
+// 64 experts in 8 groups, top-8 of 4 groups: 65 us; 16384 tokens, 256 experts
+// in 16 groups: 28 us, 4 of them for the near ties; one call of a few tokens
+// 9 us.  All of it in 64 bits, a warp for each token: 2994, 430 and 17 us.
+//
 // What q does not decide is found and decided elsewhere: with the bound on
 // q's error below, neighbours in the order that are at most `near` apart, and
 // groups at the border between kept and dropped that are, may be the other
@@ -371,17 +376,19 @@ __host__ __device__ inline int row_pitch(int E, int L)
 {
     return L == 1 || L == 32 ? E : (E + 31 - L) / 32 * 32 + L;
 }
-// Words of shared memory of a warp: keys, groups' values and kept groups,
-// where select64 works once the lists are made; selected ids, and a list for
-// select_near.
-__host__ __device__ inline int key_words(int E, int G, int top, int L)
+// Words of shared memory of a warp: keys, where select64 works once the lists
+// are made; groups' values, and in their place the ids that select_near and
+// select64 find; kept groups; a list for select_near.
+__host__ __device__ inline int up16(int n) { return (n + 15) / 16 * 16; }
+__host__ __device__ inline int key_words(int E, int G, int L)
 {
-    const int keys = 32 / L * (row_pitch(E, L) + (G | 1) + (top | 1)), work = (Scratch::bytes(E, G) + 3) / 4;
-    return ((keys > work ? keys : work) + 15) / 16 * 16;
+    const int keys = 32 / L * row_pitch(E, L), work = (Scratch::bytes(E, G) + 3) / 4;
+    return up16(keys > work ? keys : work);
 }
+__host__ __device__ inline int group_pitch(int G, int k) { return (G > k ? G : k) | 1; }
 __host__ __device__ inline int warp_words(int E, int G, int top, int k, int L)
 {
-    return key_words(E, G, top, L) + (32 / L * k + 15) / 16 * 16 + 32;
+    return key_words(E, G, L) + up16(32 / L * (group_pitch(G, k) + (top | 1))) + 32;
 }
 
 __device__ __forceinline__ unsigned lds_u32(unsigned at)
@@ -421,52 +428,18 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
     const bool softmax = a.S.score == MOE_SCORE_SOFTMAX, grouped = a.S.top_groups < G;
     const int top = a.S.top_groups;
     unsigned *const rows = s_dyn + warp * warp_words(E, G, top, k, L);
-    unsigned *const groups = rows + kTokens * pitch;              // values of the groups
-    unsigned *const kept_groups = groups + kTokens * (G | 1);
-    unsigned *const sel = rows + key_words(E, G, top, L) + tok * k;  // [k] ids of this lane's token
-    unsigned *const list = rows + key_words(E, G, top, L) + (kTokens * k + 15) / 16 * 16;
-    unsigned *const mine = rows + tok * pitch, *const mg = groups + tok * (G | 1);
-    unsigned *const mk = kept_groups + tok * (top | 1);
+    const int gp = group_pitch(G, k);
+    unsigned *const groups = rows + key_words(E, G, L), *const kept_groups = groups + kTokens * gp;
+    unsigned *const list = groups + up16(kTokens * (gp + (top | 1)));
+    unsigned *const mine = rows + tok * pitch, *const mk = kept_groups + tok * (top | 1);
+    unsigned *const mg = groups + tok * gp;   // values of the groups of this lane's token
+    unsigned *const sel = mg;                 // [k] its ids, later
     // the kept experts: those of `top` groups, or all
     const Kept kept = {mine, mk, grouped ? per : E, grouped ? top * per : E};
     for (int e = threadIdx.x; e < E; e += blockDim.x) s_hist[e] = 0u;
     pdl_wait();
     pdl_launch_dependents();
 
-    float check = 0.0f;  // stays 0 over finite values
-    float low = 0.0f, high = 0.0f;
-    if (a.S.bias) {
-        low = INFINITY;
-        high = -INFINITY;
-        for (int e = threadIdx.x; e < E; e += blockDim.x) {
-            const float b = a.S.bias[e];
-            check = fmaf(b, 0.0f, check);
-            low = fminf(low, b);
-            high = fmaxf(high, b);
-        }
-        high = warp_max(high);
-        low = -warp_max(-low);
-        if (lane == 0) {
-            s_low[warp] = low;
-            s_high[warp] = high;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kGateWarps; ++w) {
-            low = fminf(low, s_low[w]);
-            high = fmaxf(high, s_high[w]);
-        }
-    }
-    const float span = high - low;
-    const float steps = softmax ? 1.0f : kSteps / (1.0f + span);
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        const float b = a.S.bias ? a.S.bias[e] - low : 0.0f;
-        s_bias[e] = softmax ? b : fmaf(b, steps, 8388608.0f);
-    }
-    __syncthreads();
-    const int near = softmax ? (a.S.bias ? kNearSoftmaxBias : kNearSoftmax) : kNearSigmoid;
-
-    const long long stride = (long long)gridDim.x * kGateWarps * kTokens;
     // L == 1: where this lane starts in its row (see above)
     const int common = E & -E & 31 ? E & -E : 32, turn = L == 1 ? lane * common / 32 : 0;
     const int turn_group = turn / kept.per, turn_in = turn - turn_group * kept.per;
@@ -504,7 +477,41 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
         }
     };
     const long long first_token = ((long long)blockIdx.x * kGateWarps + warp) * kTokens;
-    if (first_token < a.T) load(first_token);
+    if (first_token < a.T) load(first_token);  // while the biases are looked at
+    float check = 0.0f;  // stays 0 over finite values
+    float low = 0.0f, high = 0.0f;
+    if (a.S.bias) {
+        low = INFINITY;
+        high = -INFINITY;
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            const float b = a.S.bias[e];
+            check = fmaf(b, 0.0f, check);
+            low = fminf(low, b);
+            high = fmaxf(high, b);
+        }
+        high = warp_max(high);
+        low = -warp_max(-low);
+        if (lane == 0) {
+            s_low[warp] = low;
+            s_high[warp] = high;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kGateWarps; ++w) {
+            low = fminf(low, s_low[w]);
+            high = fmaxf(high, s_high[w]);
+        }
+    }
+    const float span = high - low;
+    const float steps = softmax ? 1.0f : kSteps / (1.0f + span);
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        const float b = a.S.bias ? a.S.bias[e] - low : 0.0f;
+        s_bias[e] = softmax ? b : fmaf(b, steps, 8388608.0f);
+    }
+    __syncthreads();
+    const int near = softmax ? (a.S.bias ? kNearSoftmaxBias : kNearSoftmax) : kNearSigmoid;
+
+    const long long stride = (long long)gridDim.x * kGateWarps * kTokens;
     for (long long t0 = first_token; t0 < a.T; t0 += stride) {
         const int tokens = (int)min((long long)kTokens, a.T - t0);
         const float *const tile = a.logits + t0 * E;
@@ -639,7 +646,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
                 const int low = (int)(__shfl_sync(0xffffffffu, least, who * L) >> 8) - far;
                 const int high = (int)(__shfl_sync(0xffffffffu, most, who * L) >> 8) + far;
                 __syncwarp();
-                if (!groups_near(tile + who * E, a, groups + who * (G | 1), low, high, kept_groups + who * (top | 1), lane))
+                if (!groups_near(tile + who * E, a, groups + who * gp, low, high, kept_groups + who * (top | 1), lane))
                     unsure_groups |= tok == who;
             }
         } else {
@@ -761,7 +768,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
                 if (!(by_group & theirs)) {
                     const Kept their = {rows + who * pitch, kept_groups + who * (top | 1), kept.per, kept.count};
                     const unsigned edge_key = __shfl_sync(0xffffffffu, last, who * L);
-                    if (select_near(tile + who * E, a, their, edge_key, near, sel + (who - tok) * k, list, lane)) continue;
+                    if (select_near(tile + who * E, a, their, edge_key, near, groups + who * gp, list, lane)) continue;
                 }
                 full |= theirs;
             }
@@ -770,7 +777,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
                 const int who = (__ffs(full) - 1) / L;
                 full &= ~(kAll << (who * L));
                 const int got = select64(tile + who * E, a, rows, lane);
-                if (lane < k) sel[(who - tok) * k + lane] = (unsigned)got;
+                if (lane < k) groups[who * gp + lane] = (unsigned)got;
             }
             __syncwarp();
 #pragma unroll
@@ -849,12 +856,17 @@ cudaError_t launch_scored(const GateArgs &a, cudaStream_t s)
     return launch_pdl(fn, dim3((unsigned)blocks), dim3(32 * kGateWarps), (size_t)smem, s, a);
 }
 
-// Lanes of a token.  One, where the tokens alone fill the SMs: the lists are
-// not merged across lanes.  32 for the least latency of few tokens.
+// Lanes of a token.  One, where the tokens alone keep the SMs busy: the lists
+// are not merged across lanes.  The more experts, the longer a lane takes and
+// the more shared memory its row.  Measured with one lane and with eight:
+// 262144 tokens, 60 experts 71 and 141 us; 65536, 32 experts 18 and 27; 40000,
+// 64 experts 23 and 21; 262144, 128 experts 113 and 131; 65536, 128 experts 63
+// and 37; 16384, 256 experts 40 and 26.  32 lanes for the least latency of few
+// tokens.
 int scored_lanes(int T, int E)
 {
     const int sms = device_sm_count();
-    if (E <= 128 && T >= sms * 512) return 1;
+    if ((E <= 64 && T >= sms * 256) || (E <= 128 && T >= sms * 768)) return 1;
     return T >= sms * 32 ? 8 : 32;
 }
 

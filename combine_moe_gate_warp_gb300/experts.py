@@ -383,8 +383,12 @@ class ExpertRows:
         xp = _check_rows(x, torch.bfloat16, self.rows, K, "x", self.device)
         if out is None:
             out = self.new_fp4(K)
-        cp, sp = self._fp4(out, K, "out")
-        abi._check(self._lib.moe_quantize_fp4(self._ref, xp, K, cp, sp, self._stream()), "moe_quantize_fp4")
+            cp, sp = out.codes.data_ptr(), out.scales.data_ptr()
+        else:
+            cp, sp = self._fp4(out, K, "out")
+        st = self._lib.moe_quantize_fp4(self._ref, xp, K, cp, sp, self._stream())
+        if st:
+            abi._check(st, "moe_quantize_fp4")
         return out
 
     def dequantize_fp4(self, x: Fp4Rows, *, out=None):
