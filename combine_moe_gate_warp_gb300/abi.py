@@ -281,6 +281,9 @@ class Scoring:
     def __post_init__(self):
         if self.score not in ("sigmoid", "softmax"):
             raise ValueError(f"score: sigmoid or softmax, got {self.score!r}")
+        for name in ("groups", "top_groups", "group_top"):
+            if not 1 <= getattr(self, name) <= MOE_MAX_EXPERTS:
+                raise ValueError(f"{name}: 1 to {MOE_MAX_EXPERTS}, got {getattr(self, name)}")
 
     def c(self, bias=None, bias_next=None, bias_rate: float = 0.0) -> moe_scoring:
         return moe_scoring(MOE_SCORE_SOFTMAX if self.score == "softmax" else MOE_SCORE_SIGMOID, self.groups,

@@ -128,16 +128,6 @@ __device__ __noinline__ int select64(const float *row, const GateArgs &a, void *
     return slot;
 }
 
-// The k best of a token's candidates in 64 bits, by a whole warp: the k ids in
-// sel, and the other kept experts whose key is at most `near` steps behind the
-// last one's.  The rest are behind for certain.  One candidate a lane; false
-// (and nothing done) if there are more.
-struct Kept {
-    const unsigned *keys;    // of the token's experts
-    const unsigned *groups;  // its kept groups
-    int per, count;          // experts of a group, and of all kept ones
-};
-
 // What a score in 64 bits takes of its row: the softmax's top and, where a bias
 // is added (without one the order is that of exp(l - top)), its sum.
 struct Row64 {
@@ -216,6 +206,16 @@ __device__ __noinline__ bool groups_near(const float *row, const GateArgs &a, co
     return true;
 }
 
+struct Kept {
+    const unsigned *keys;    // of the token's experts
+    const unsigned *groups;  // its kept groups
+    int per, count;          // experts of a group, and of all kept ones
+};
+
+// The k best of a token's candidates in 64 bits, by a whole warp: the k ids in
+// sel, and the other kept experts whose key is at most `near` steps behind the
+// last one's.  The rest are behind for certain.  One candidate a lane; false
+// (and nothing done) if there are more.
 __device__ __noinline__ bool select_near(const float *row, const GateArgs &a, const Kept &kept, unsigned last, int near,
                                          unsigned *sel, unsigned *list, int lane)
 {
@@ -261,16 +261,20 @@ __device__ __forceinline__ float sigmoid(float l)
 // of KL keys are sorted by Batcher's networks, merged, and merged across the
 // lanes of a token.
 //
-// What bounds it: instructions (110 a token at 64 experts) and, with 20 warps an SM, their latency; HBM at a fifth.  262144 tokens,
-// 64 experts in 8 groups, top-8 of 4 groups: 65 us; 16384 tokens, 256 experts
-// in 16 groups: 28 us, 4 of them for the near ties; one call of a few tokens
-// 9 us.  All of it in 64 bits, a warp for each token: 2994, 430 and 17 us.
+// What bounds it: instructions (110 a token at 64 experts) and, with 20 warps
+// an SM, their latency; HBM is at a fifth.  262144 tokens, 64 experts in 8
+// groups, top-8 of 4 groups: 65 us; 16384 tokens, 256 experts in 16 groups: 26
+// us; a few tokens: 8 us, by the host.  All of it in 64 bits, a warp for each
+// token, took 2994, 430 and 17 us.
 //
 // What q does not decide is found and decided elsewhere: with the bound on
 // q's error below, neighbours in the order that are at most `near` apart, and
 // groups at the border between kept and dropped that are, may be the other
 // way round.  Equal logits with equal biases are equal values, and rightly in
-// the order of their ids; whatever else is that close goes to select64.
+// the order of their ids.  Whatever else is that close is settled in 64 bits by
+// the whole warp: the groups of the border and the candidates alone
+// (groups_near, select_near) or, where those are too many, the token anew
+// (select64).
 //
 // A warp copies its tokens' logits to shared memory, and the keys take their
 // place there.  With several lanes to a token the rows start in other banks:
@@ -282,13 +286,13 @@ constexpr float kSteps = 8388600.0f;  // of q, below 2^23
 // q's error in steps.  The exponential (ex2.approx, 2 steps of 2^-23) with its
 // argument's rounding and the reciprocal (1 step) leave a sigmoid within
 // 1.25 * 2^-22 of its value, 2.5 steps for values that span 1 or more; the
-// bias term and the sum are rounded to steps: 0.5 each, and 0.5 for the bias'
-// product.  4 each, 8 for two, and the cut to whole steps.
+// bias less the lowest, the bias term and the sum are rounded: 0.5 each.  4
+// in all, 8 for two values.
 constexpr int kNearSigmoid = 10;
 // Softmax: exp(l - max) (expf, 2 steps of 2^-23, and its argument's rounding)
-// within 1.2 * 2^-22 of it, 2.4 steps.  The sum of E
-// terms, in 8 parts or more, and its reciprocal are within 42 * 2^-24; they
-// scale all scores alike and matter where a bias is added: 21 steps.
+// is within 1.2 * 2^-22 of it, 2.4 steps, and 1.5 as above: 8 for two.  The sum
+// of E terms, in 8 parts or more, and its reciprocal are within 42 * 2^-24;
+// they scale all scores alike and matter where a bias is added: 21 steps more.
 constexpr int kNearSoftmax = 10, kNearSoftmaxBias = 32;
 
 __device__ __forceinline__ unsigned make_key(float steps, int e)  // steps in [2^23, 2^24)

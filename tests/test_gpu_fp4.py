@@ -168,6 +168,27 @@ def test_dispatch(T, H, E, k, cap):
     assert torch.equal(back[:R].cpu().double(), decode_fp4(codes, scales)[src])
 
 
+def test_the_dispatch_call():
+    T, H = 20, 96
+    plan = RoutePlan(RouteShape(T=T, H=H, E=4, k=2, P=1))
+    plan.route(torch.randn(T, 4, generator=torch.Generator().manual_seed(5)).cuda())
+    x = randn(T, H, seed=1).cuda()
+    codes = torch.zeros(2 * T, H // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(2 * T, fp4_pitch(H), dtype=torch.uint8, device="cuda")
+    abi.moe_dispatch_fp4(x, T, H, plan.layout, codes, scales)
+    want = encode_fp4(x)
+    src = (plan.layout.src_pos // 2).cpu().long()
+    assert plan.status() == 0 and torch.equal(codes.cpu(), want[0][src]) and torch.equal(scales.cpu(), want[1][src])
+    for args in ((x[:5], T, H, plan.layout, codes, scales), (x, T, H, plan.layout, codes[:9], scales),
+                 (x, T, H, plan.layout, codes, scales[:, :8]), (x.float(), T, H, plan.layout, codes, scales)):
+        with pytest.raises(ValueError):
+            abi.moe_dispatch_fp4(*args)
+    with pytest.raises(ValueError, match="two transports"):
+        RoutePlan(RouteShape(T=T, H=H, E=4, k=2, P=1, fp4=True, fp8=1))
+    with pytest.raises(ValueError, match="multiple of 32"):
+        RoutePlan(RouteShape(T=T, H=48, E=4, k=2, P=1, fp4=True))
+
+
 def test_dispatch_of_a_bad_layout():
     plan = RoutePlan(RouteShape(T=40, H=64, E=4, k=2, P=1, fp4=True))
     plan.route(torch.randn(40, 4, generator=torch.Generator().manual_seed(5)).cuda())

@@ -77,7 +77,11 @@ SHAPES = [  # T, E, k, groups, top_groups, group_top
     (1, 64, 8, 8, 4, 2), (3, 1, 1, 1, 1, 1), (5, 2, 2, 2, 2, 1), (33, 8, 2, 1, 1, 1), (257, 60, 6, 5, 3, 1),
     (1000, 64, 8, 8, 4, 2), (513, 256, 8, 16, 6, 2), (300, 256, 16, 32, 9, 2), (129, 255, 5, 85, 40, 2),
     (70, 256, 4, 256, 7, 1), (65, 64, 16, 4, 1, 2), (2048, 16, 1, 4, 2, 2), (31, 33, 3, 11, 11, 2),
-    (40000, 64, 8, 8, 3, 2), (20000, 24, 4, 1, 1, 1), (9000, 160, 6, 8, 3, 2), (17, 96, 12, 12, 5, 1),
+    (40000, 64, 8, 8, 3, 2), (20000, 24, 4, 1, 1, 1),
+    # as many tokens as one lane each takes
+    (39001, 33, 3, 11, 4, 2), (39040, 60, 6, 5, 3, 1), (39007, 17, 16, 1, 1, 1), (40001, 8, 2, 1, 1, 1),
+    (39500, 64, 16, 4, 2, 2), (117001, 128, 8, 16, 5, 2), (117000, 96, 4, 1, 1, 1), (39009, 1, 1, 1, 1, 1),
+    (39002, 62, 5, 31, 30, 1), (39003, 48, 7, 2, 1, 2), (38999, 3, 2, 3, 2, 1), (9000, 160, 6, 8, 3, 2), (17, 96, 12, 12, 5, 1),
 ]
 
 
@@ -341,6 +345,37 @@ def test_own_stream_and_two_at_once():
         ids.fill_(-1)
         graph.replay()
         assert torch.equal(ids.cpu().long(), select64(logits.cpu(), k, "sigmoid", 8, 4, 2))
+
+
+def test_refusals_of_the_call():
+    T, E, k = 6, 16, 4
+    z = lambda *s, **kw: torch.zeros(*s, device="cuda", **kw)  # noqa: E731
+    i32 = dict(dtype=torch.int32)
+    good = dict(logits=z(T, E), k=k, scoring=Scoring(groups=4, top_groups=2, group_top=2), bias=z(E), topk_idx=z(T, k, **i32),
+                gates=z(T, k), expert_counts=z(E, **i32), aux_loss=z(1, dtype=torch.float64), entropy=None,
+                ws=alloc_workspace(T, E, k, 1))
+    moe_gate_scored(**good)
+    for name, bad in (("logits", z(T * E)), ("logits", z(E, T).T), ("logits", z(T, E).double()), ("bias", z(E - 1)),
+                      ("bias", z(E).cpu()), ("topk_idx", z(T, k)), ("topk_idx", z(T, k - 1, **i32)),
+                      ("gates", z(T, 2 * k)[:, ::2]), ("expert_counts", z(E - 1, **i32)), ("aux_loss", z(1)),
+                      ("ws", z(8192, dtype=torch.uint8).int())):
+        with pytest.raises(ValueError):
+            moe_gate_scored(**{**good, name: bad})
+    with pytest.raises(TypeError):
+        moe_gate_scored(**{**good, "gates": [0.0] * 24})
+    with pytest.raises(MoeError):
+        moe_gate_scored(**{**good, "ws": z(64, dtype=torch.uint8)})
+    with pytest.raises(MoeError):
+        moe_gate_scored(**{**good, "scoring": Scoring(groups=5)})
+    with pytest.raises(ValueError):
+        moe_gate_scored(**good, bias_next=z(E + 1))
+    back = dict(logits=z(T, E), topk_idx=z(T, k, **i32), d_gates=z(T, k), scoring=Scoring(), d_logits=z(T, E),
+                ws=good["ws"])
+    moe_gate_scored_backward(**back)
+    for name, bad in (("topk_idx", z(T * k, **i32)), ("d_gates", z(T, k - 1)), ("d_logits", z(T, E - 1)),
+                      ("d_logits", z(T, E).half())):
+        with pytest.raises(ValueError):
+            moe_gate_scored_backward(**{**back, name: bad})
 
 
 def test_refusals_of_the_plan():

@@ -101,6 +101,9 @@ def test_the_binding_refuses(abi):
     from combine_moe_gate_warp_gb300 import ExpertRows, Fp4Rows, RouteShape, Scoring
     with pytest.raises(ValueError, match="score"):
         Scoring("tanh")
+    for kw in (dict(groups=0), dict(groups=257), dict(groups=(1 << 32) + 1), dict(top_groups=0), dict(group_top=-1)):
+        with pytest.raises(ValueError, match="to 256"):
+            Scoring(**kw)
     with pytest.raises(ValueError, match="CUDA"):
         abi.moe_gate_scored(torch.zeros(4, 8), 2, Scoring(), None, None, None, None, None, None, None)
     with pytest.raises(ValueError, match="CUDA"):
