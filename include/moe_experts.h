@@ -16,7 +16,7 @@
  * are held in fp32 and rounded once, to nearest even, as they are written.
  *
  * Supported range: 1 <= E <= 256, 0 <= rows < 2^30, K and N multiples of 8
- * up to 2^20 (K a multiple of 16 for e4m3; N a multiple of 16 with
+ * up to 2^20 (K a multiple of 16 for e4m3, of 32 in 4 bits; N a multiple of 16 with
  * MOE_ACT_SWIGLU; a saved layer's columns a multiple of 32, 64 with
  * MOE_ACT_SWIGLU), E * N < 2^31.  Anything else is MOE_ERR_UNSUPPORTED.
  */
