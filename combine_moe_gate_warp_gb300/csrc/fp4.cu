@@ -8,8 +8,8 @@
 // blocks lie side by side, so it moves 2 KB of bf16 in, 512 bytes and 32
 // bytes out.  Bound by HBM: each value of x is read once, each code written
 // once for each of its rows.  Of 4096 columns: 65536 tokens to 2 experts each
-// 139 us (5.9 TB/s; 163 with the packed rows looked up after the token's row),
-// 131072 packed rows to 4 bits 209 us (6.5 TB/s) and back 221 us (6.1 TB/s).
+// 130 us (6.3 TB/s; 163 with one block in flight a thread), 131072 packed rows
+// to 4 bits 209 us (6.5 TB/s) and back 221 us (6.1 TB/s).
 #include "fp4.cuh"
 #include "experts.h"
 #include "launchers.h"
@@ -19,7 +19,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // packed rows of a token that are looked up beside its load
 
 // A thread's place in a matrix of `rows` rows of `blocks` units, which it
 // walks by the grid's stride.
@@ -117,24 +116,30 @@ dispatch_fp4_kernel(const __nv_bfloat16 *__restrict__ x, long long T, int blocks
     pdl_launch_dependents();
     const uint64_t pol = l2_stream_policy(true);
     const int rows_valid = min(r_max, __ldg(R_ptr));
-    for (Place p(blocks, 0); p.row < T; p.advance()) {
+    const auto pack = [&](const Place &p, const Block32 &b) {
         const int32_t *dst = dst_row + p.row * k;
-        const Block32 b = load32(x + (p.row * blocks + p.col) * 32, wide, pol);
-        int r[kAhead];  // beside the row, not after it
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) r[j] = j < k ? __ldg(dst + j) : -1;
         unsigned byte;
         const uint4 c = encode32(b, byte);
-        const auto put = [&](int row) {
-            if (row >= rows_valid) {
+        for (int j = 0; j < k; ++j) {
+            const int r = __ldg(dst + j);
+            if (r >= rows_valid) {
                 if (p.col == 0) record_status(ws, MOE_ERR_DEVICE_DATA);
-            } else if (row >= 0) {
-                store32(codes, scales, row, p.col, blocks, pitch, c, byte, pol);
+            } else if (r >= 0) {
+                store32(codes, scales, r, p.col, blocks, pitch, c, byte, pol);
             }
-        };
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) put(r[j]);
-        for (int j = kAhead; j < k; ++j) put(__ldg(dst + j));
+        }
+    };
+    // two blocks in flight: the way from a token's values to its packed rows is
+    // three loads and stores long
+    for (Place p(blocks, 0); p.row < T; p.advance()) {
+        const Place first = p;
+        const Block32 b = load32(x + (p.row * blocks + p.col) * 32, wide, pol);
+        p.advance();
+        const bool two = p.row < T;
+        Block32 c = b;
+        if (two) c = load32(x + (p.row * blocks + p.col) * 32, wide, pol);
+        pack(first, b);
+        if (two) pack(p, c);
     }
 }
 
