@@ -12,6 +12,8 @@
 // second run elsewhere or a backward pass could repeat.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "gate_stats.cuh"
 #include "launchers.h"
@@ -261,9 +263,9 @@ __device__ __forceinline__ float sigmoid(float l)
 // of KL keys are sorted by Batcher's networks, merged, and merged across the
 // lanes of a token.
 //
-// What bounds it: instructions (110 a token at 64 experts) and, with 20 warps
+// What bounds it: instructions (110 a token at 64 experts) and, with 16 warps
 // an SM, their latency; HBM is at a fifth.  262144 tokens, 64 experts in 8
-// groups, top-8 of 4 groups: 65 us; 16384 tokens, 256 experts in 16 groups: 26
+// groups, top-8 of 4 groups: 61 us; 16384 tokens, 256 experts in 16 groups: 26
 // us; a few tokens: 8 us, by the host.  All of it in 64 bits, a warp for each
 // token, took 2994, 430 and 17 us.
 //
@@ -417,7 +419,7 @@ __device__ __forceinline__ void copy_async_all()
 }
 
 template <int KL, int L>
-__global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const __grid_constant__ GateArgs a)
+__global__ void __launch_bounds__(32 * kGateWarps, 4) gate_scored_kernel(const __grid_constant__ GateArgs a)
 {
     constexpr int kTokens = 32 / L;
     constexpr unsigned kAll = L == 32 ? ~0u : (1u << L) - 1u;  // the lanes of the first token
@@ -555,11 +557,14 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
             unit = kSteps / (inv + span);
             scale = inv * unit;
         }
-        const auto key = [&](int e) {
-            const float x = __uint_as_float(mine[e]);
-            if (softmax) return make_key(fmaf(x, scale, fmaf(s_bias[e], unit, 8388608.0f)), e);
-            check = fmaf(x, 0.0f, check);
-            return make_key(fmaf(reciprocal_fast(1.0f + exp2_fast(x * -kLog2e)), steps, s_bias[e]), e);
+        // the key of the value (softmax: exp(l - peak), else the logit) at x[i],
+        // expert e0 + i
+        const auto key = [&](auto soft, const unsigned *x, const float *bias, int e0, int i) {
+            const float v = __uint_as_float(x[i]);
+            if constexpr (decltype(soft)::value)
+                return make_key(fmaf(v, scale, fmaf(bias[i], unit, 8388608.0f)), e0 + i);
+            check = fmaf(v, 0.0f, check);
+            return make_key(fmaf(reciprocal_fast(1.0f + exp2_fast(v * -kLog2e)), steps, bias[i]), e0 + i);
         };
         bool unsure = false, unsure_groups = false;
         const auto same = [&](int e, int o) {  // equal values for certain
@@ -580,24 +585,34 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
                 }
             };
             if (L == 1) {
-                int g = turn_group;
-                for (int n = 0; n < G; ++n) {
-                    unsigned first = 0u, second = 0u;
-                    int i = turn_in;
+                const auto fill = [&](auto soft) {
+                    int g = turn_group;
+                    for (int n = 0; n < G; ++n) {
+                        unsigned first = 0u, second = 0u;
+                        unsigned *const x = mine + g * per;
+                        const float *const bias = s_bias + g * per;
+                        int i = turn_in;
 #pragma unroll 8
-                    for (int m = 0; m < per; ++m) {
-                        const unsigned v = key(g * per + i);
-                        mine[g * per + i] = v;
-                        second = max(second, min(first, v));
-                        first = max(first, v);
-                        i = i + 1 == per ? 0 : i + 1;
+                        for (int m = 0; m < per; ++m) {
+                            const unsigned v = key(soft, x, bias, g * per, i);
+                            x[i] = v;
+                            second = max(second, min(first, v));
+                            first = max(first, v);
+                            i = i + 1 == per ? 0 : i + 1;
+                        }
+                        mg[g] = ((first >> 9) + (two ? second >> 9 : 0u)) << 8 | (unsigned)(255 - g);
+                        g = g + 1 == G ? 0 : g + 1;
                     }
-                    mg[g] = ((first >> 9) + (two ? second >> 9 : 0u)) << 8 | (unsigned)(255 - g);
-                    g = g + 1 == G ? 0 : g + 1;
-                }
+                };
+                if (softmax) fill(std::true_type());
+                else fill(std::false_type());
             } else {
+                const auto fill = [&](auto soft) {
 #pragma unroll 4
-                for (int e = sub; e < E; e += L) mine[e] = key(e);
+                    for (int e = sub; e < E; e += L) mine[e] = key(soft, mine, s_bias, 0, e);
+                };
+                if (softmax) fill(std::true_type());
+                else fill(std::false_type());
                 __syncwarp();
                 for (int g = sub; g < G; g += L) {
                     unsigned first, second;
@@ -654,13 +669,17 @@ __global__ void __launch_bounds__(32 * kGateWarps, 5) gate_scored_kernel(const _
                     unsure_groups |= tok == who;
             }
         } else {
-            int e = L == 1 ? turn : sub;
+            const auto fill = [&](auto soft) {
+                int e = L == 1 ? turn : sub;
 #pragma unroll 8
-            for (int n = sub; n < E; n += L) {
-                mine[e] = key(e);
-                e += L;
-                if (L == 1 && e == E) e = 0;
-            }
+                for (int n = sub; n < E; n += L) {
+                    mine[e] = key(soft, mine, s_bias, 0, e);
+                    e += L;
+                    if (L == 1 && e == E) e = 0;
+                }
+            };
+            if (softmax) fill(std::true_type());
+            else fill(std::false_type());
             if (sub == 0) mk[0] = 0u;
         }
         __syncwarp();
