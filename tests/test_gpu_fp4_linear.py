@@ -8,7 +8,7 @@ import torch
 from combine_moe_gate_warp_gb300 import (ExpertRows, Fp4Rows, RoutePlan, RouteShape, Scoring, abi, fp4_pitch,
                                          quantize_weights_fp4)
 from expert_util import BF16, act64, act_error, assert_near, normal, offsets_of, spans, sum_error
-from scored_util import decode_fp4, encode_fp4
+from scored_util import backward_error, decode_fp4, encode_fp4, gates64
 
 pytestmark = pytest.mark.gpu
 
@@ -298,3 +298,59 @@ def test_refusals():
     with pytest.raises(ValueError, match="bias"):
         r.linear_fp4(x, w, bias=torch.zeros(2, 8, dtype=torch.bfloat16, device="cuda"))
     assert fp4_pitch(64) == 16
+
+
+def test_a_training_step():
+    """Scores, dispatch in 4 bits, the experts' product in 4 bits and the
+    combine, then the gradients of all of them: the quantisers are passed
+    straight through, the products' gradients take the values that the codes
+    stand for.  Against 64 bits; each bf16 on the way is off by half a step,
+    2^-8 of its value, and fp32 sums add less than another tenth of that."""
+    T, H, N, E, k = 300, 288, 160, 8, 3
+    scoring = Scoring("sigmoid", 4, 3, 2, scale=1.25)
+    plan = RoutePlan(RouteShape(T=T, H=H, E=E, k=k, P=1, scoring=scoring, fp4=True))
+    out = RoutePlan(RouteShape(T=T, H=N, E=E, k=k, P=1, scoring=scoring))  # the combine's columns are the product's
+    rows = ExpertRows.of(plan)
+    g = torch.Generator().manual_seed(1)
+    logits = torch.randn(T, E, generator=g).cuda()
+    x, dy = normal(T, H, seed=2), normal(T, N, seed=3)
+    w = quantize_weights_fp4((torch.randn(E, N, H, generator=g) * H ** -0.5).bfloat16().cuda())
+    plan.route(logits)
+    plan.dispatch(x)
+    out.route(logits)
+    eo = rows.linear_fp4(Fp4Rows(plan.packed, plan.scales), w)
+    out.combine(eo)
+    # backward
+    out.combine_backward(dy, eo)
+    out.gate_backward(logits)
+    d_rows = out.d_expert_out
+    w_values = ExpertRows(rows=E * N).dequantize_fp4(Fp4Rows(w.codes.view(E * N, -1), w.scales.view(E * N, -1))).view(E, N, H)
+    x_rows = rows.dequantize_fp4(Fp4Rows(plan.packed, plan.scales))
+    dw, _ = rows.wgrad(d_rows, x_rows)
+    plan.dispatch_backward(rows.dgrad(d_rows, w_values))
+    assert plan.status() == 0 and out.status() == 0
+    # the same in 64 bits
+    xq = decode_fp4(*encode_fp4(x)).cuda()
+    wq = values(w)
+    assert torch.equal(w_values.double(), wq)
+    ids, gates = plan.topk_idx.long(), plan.gates.double()
+    e_out = torch.einsum("th,tknh->tkn", xq, wq[ids])
+    y = (e_out * gates[..., None]).sum(1)
+    mags = (torch.einsum("th,tknh->tkn", xq.abs(), wq[ids].abs()) * gates[..., None]).sum(1)
+    assert_near(out.y, y, 2.1 * BF16 * mags, "y")
+    d = dy.double()
+    gd = gates[..., None] * d[:, None]                       # [T, k, N]
+    dx, mx = (torch.einsum("tkn,tknh->th", a, b) for a, b in ((gd, wq[ids]), (gd.abs(), wq[ids].abs())))
+    assert_near(plan.dx, dx, 3.1 * BF16 * mx, "dx")
+    for e in range(E):
+        on = (ids == e).double()[..., None] * gd             # its slots' gradients
+        want, mag = on.sum(1).T @ xq, on.abs().sum(1).T @ xq.abs()
+        assert_near(dw[e], want, 2.1 * BF16 * mag, f"dw of expert {e}")
+    # a product's own fp32 sum is off by the share that its magnitudes leave
+    terms = torch.einsum("th,tknh->tkn", xq.abs(), wq[ids].abs())
+    off = BF16 * e_out.abs() + 1.01 * sum_error(H, terms)
+    assert_near(out.d_gates, (e_out * d[:, None]).sum(2), 1.1 * (off * d[:, None].abs()).sum(2), "d_gates")
+    ref = logits.cpu().double().requires_grad_()
+    (gates64(ref, ids.cpu(), "sigmoid", True, 1.25) * out.d_gates.cpu().double()).sum().backward()
+    bound = backward_error(logits.cpu(), ids.cpu(), out.d_gates.cpu(), E, "sigmoid", True, 1.25)
+    assert_near(out.d_logits.cpu(), ref.grad, bound, "d_logits")
