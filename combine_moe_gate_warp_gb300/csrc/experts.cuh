@@ -29,9 +29,9 @@
 //   wgrad, the same                                           460 us, 85 %
 //   linear, 128 rows, 32 experts, 2048 -> 2 x 1024            47 us, 5.7 TB/s:
 //     the weights' bytes (and 6 us to start and to finish)
-//   linear in 4 bits, 65536 rows, 16 experts, 5120 -> 2 x 2048 swiglu  465 us,
-//     5.9 PFLOP/s; one expert, 8192 -> 8192: 1315 us, 6.7 PFLOP/s: the matrix
-//     instructions, which are issued without a pause at 7.1-7.7
+//   linear in 4 bits, 65536 rows, 16 experts, 5120 -> 2 x 2048 swiglu  445 us,
+//     6.2 PFLOP/s; one expert, 8192 -> 8192: 1258 us, 7.0 PFLOP/s: the matrix
+//     instructions, 6.8-7.7 if nothing had to bring their scales
 //   linear in 4 bits, 128 rows, 32 experts, 2048 -> 2 x 2048   29 us, 4.9 TB/s
 //   linear, 512 rows, 8 experts, 512 -> 2 x 256               6 us from the
 //     first instruction to the last: 0.8 for offsets and barriers, 1 until the
@@ -135,6 +135,7 @@ struct Params {
     const float2 *x_scales, *w_scales;
     const uint8_t *x_bytes, *w_bytes;  // kFp4: scale bytes of rows and weights
     int pitch, valid_scales;           // their bytes per row, and how many hold scales
+    int sectors;                       // rows of scales start at multiples of 32 bytes
     __nv_bfloat16 *y, *a;
     void *dw, *db;
     uint8_t *saved, *saved_scales;
@@ -229,6 +230,17 @@ struct Walk {
         return true;
     }
 };
+
+// 32 bytes, read once, with one request
+__device__ __forceinline__ u32x8 load_sector(const void *at)
+{
+    u32x8 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x), "=r"(v.hi.y), "=r"(v.hi.z),
+                   "=r"(v.hi.w)
+                 : "l"(at));
+    return v;
+}
 
 __device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
@@ -915,13 +927,15 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         // ---- scales ---------------------------------------------------------
         // The rows' scales lie in row order, tensor memory wants 4 bytes of 4
         // rows side by side, and no copy engine turns pieces of 4 bytes around.
-        // So a lane reads 8 kSpan bytes (four stages' are a whole sector) of the rows lane, lane + 32, .. of both operands, and stores
-        // 4 bytes of 4 rows with one instruction.  The two warps take every
-        // other kSpan stages: a stage takes one of them about 780 cycles, its
-        // products 530.  65536 rows, 16 experts, 5120 -> 2 x 2048: 465 us; the
-        // rows' 16 bytes through a ring in shared memory 513 us; a warp for
-        // each operand, four stages ahead in registers and unrolled for that,
-        // 860 us: 270 KB of instructions, and the block waits for them.
+        // So a lane reads 8 kSpan bytes (of four stages: a whole sector) of the
+        // rows lane, lane + 32, .. of both operands, and stores 4 bytes of 4
+        // rows with one instruction.  The two warps take every other kSpan
+        // stages: a stage takes one of them about 780 cycles, its products
+        // 530.  65536 rows, 16 experts, 5120 -> 2 x 2048: 445 us; a sector with
+        // two requests 465 us; the rows' bytes through a ring in shared memory
+        // 513 us; a warp for each operand, four stages ahead in registers and
+        // unrolled for that, 860 us: 270 KB of instructions, and the block
+        // waits for them.  Without any loads here 410 us.
         // A warp does not wait for the stages that it leaves out.  Its last wait
         // told it that the ring has been read up to kStages before that stage;
         // a parity asked for more than kStages later could be that of an
@@ -962,18 +976,28 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 }
                 const int left = p.valid_scales - span0 * 8;  // scale bytes of a row from here on
                 uint32_t v[kRows][2 * kSpan];
+                if (kSpan == 4 && p.sectors) {
 #pragma unroll
-                for (int r = 0; r < kRows; ++r)
+                    for (int r = 0; r < kRows; ++r) {
+                        const u32x8 q = at[r] ? load_sector(at[r] + span0 * 8) : u32x8{};
+                        const uint32_t w[8] = {q.lo.x, q.lo.y, q.lo.z, q.lo.w, q.hi.x, q.hi.y, q.hi.z, q.hi.w};
 #pragma unroll
-                    for (int h = 0; h < kSpan / 2; ++h) {
-                        const uint4 q = at[r] && h * 16 < left
-                                            ? __ldg(reinterpret_cast<const uint4 *>(at[r] + span0 * 8 + h * 16))
-                                            : make_uint4(0u, 0u, 0u, 0u);
-                        v[r][4 * h] = q.x;
-                        v[r][4 * h + 1] = q.y;
-                        v[r][4 * h + 2] = q.z;
-                        v[r][4 * h + 3] = q.w;
+                        for (int k = 0; k < 2 * kSpan; ++k) v[r][k] = w[k];
                     }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                        for (int h = 0; h < kSpan / 2; ++h) {
+                            const uint4 q = at[r] && h * 16 < left
+                                                ? __ldg(reinterpret_cast<const uint4 *>(at[r] + span0 * 8 + h * 16))
+                                                : make_uint4(0u, 0u, 0u, 0u);
+                            v[r][4 * h] = q.x;
+                            v[r][4 * h + 1] = q.y;
+                            v[r][4 * h + 2] = q.z;
+                            v[r][4 * h + 3] = q.w;
+                        }
+                }
                 if (left < 8 * kSpan)  // nothing past a row's scales
 #pragma unroll
                     for (int k = 0; k < 2 * kSpan; ++k) {
@@ -1005,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     // by the copy to its own tensor memory, from its own shared
                     // memory, and the fence above has them there before the
                     // arrival goes out.  A release, or a fence by an idle warp,
-                    // takes 1900 cycles a stage (1230 us against 513).
+                    // takes 1900 cycles a stage (1230 us against 513 at the time).
                     if (lane == 0) mbar_arrive_remote(cluster_addr(&c->full[s], lead));
                     step(1);
                 }
@@ -1336,6 +1360,8 @@ cudaError_t linear(const moe_rows *G, const void *x, const void *x_scales, int K
         p.w_bytes = static_cast<const uint8_t *>(w_scales);
         p.pitch = MOE_FP4_PITCH(K);
         p.valid_scales = K / 32;
+        p.sectors = p.pitch % 32 == 0 && reinterpret_cast<uintptr_t>(x_scales) % 32 == 0 &&
+                    reinterpret_cast<uintptr_t>(w_scales) % 32 == 0;
     }
     p.y = static_cast<__nv_bfloat16 *>(y);
     p.saved = static_cast<uint8_t *>(saved);

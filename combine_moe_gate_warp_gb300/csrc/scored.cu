@@ -161,9 +161,9 @@ __device__ __forceinline__ double warp_max(double v)
     return v;
 }
 
-// The groups between `low` and `high`, of which some are kept, in 64 bits and
-// by a whole warp: those above stand first in `kept`, the best of these
-// follow.  False (and nothing done) if there are more than 32.
+// The kept groups, where those between `low` and `high` are ordered in 64 bits,
+// by a whole warp: those above, and the best of these.  False if there are more
+// than 32 of these.
 __device__ __noinline__ bool groups_near(const float *row, const GateArgs &a, const unsigned *values, int low, int high,
                                          unsigned *kept, int lane)
 {
@@ -171,7 +171,9 @@ __device__ __noinline__ bool groups_near(const float *row, const GateArgs &a, co
     int n = 0, above = 0, mine = -1;  // lane b: the border's group b
     for (int g0 = 0; g0 < G; g0 += 32) {
         const int g = g0 + lane, v = g < G ? (int)(values[g] >> 8) : 0;
-        above += __popc(__ballot_sync(0xffffffffu, g < G && v > high));
+        const unsigned over = __ballot_sync(0xffffffffu, g < G && v > high);
+        if (g < G && v > high) kept[above + __popc(over & ((1u << lane) - 1u))] = (unsigned)g;
+        above += __popc(over);
         const unsigned who = __ballot_sync(0xffffffffu, g < G && v >= low && v <= high);
         const int c = __popc(who);
         // the (lane - n)-th of them
@@ -347,8 +349,8 @@ __device__ __forceinline__ F lanes_max(F v)
     for (int d = L / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
     return v;
 }
-template <int L>
-__device__ __forceinline__ float lanes_sum(float v)
+template <int L, typename F>
+__device__ __forceinline__ F lanes_sum(F v)
 {
 #pragma unroll
     for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
@@ -458,8 +460,10 @@ __global__ void __launch_bounds__(32 * kGateWarps, 4) gate_scored_kernel(const _
 #pragma unroll 4
             for (int i = 4 * lane; i < 32 * E; i += 128)
                 if (i < whole || i >= there) copy_async16(rows + i, i < whole ? tile + i : tile, i < whole);
-            if (whole != there && lane < 4) copy_async4(rows + whole + lane, tile + (whole + lane < there ? whole + lane : 0),
-                                                        whole + lane < there);
+            if (whole != there && lane < 4) {
+                const int i = whole + lane;
+                copy_async4(rows + i, tile + (i < there ? i : 0), i < there);
+            }
         } else if (L % 4 == 0 && (E & 3) == 0) {
             for (int r = 0; r < kTokens; ++r)
                 for (int e = 4 * lane; e < E; e += 128)
@@ -622,16 +626,61 @@ __global__ void __launch_bounds__(32 * kGateWarps, 4) gate_scored_kernel(const _
                 __syncwarp();
             }
             unsigned least = ~0u, most = 0u;  // kept, dropped
-            for (int g = sub; g < G; g += L) {
-                const unsigned v = mg[g];
-                int before = 0;
+            if (G <= (L == 1 ? 16 : 64)) {
+                // few groups: each one's place among all
+                for (int g = sub; g < G; g += L) {
+                    const unsigned v = mg[g];
+                    int before = 0;
 #pragma unroll 8
-                for (int h = 0; h < G; ++h) before += mg[h] > v;
-                if (before < top) {
-                    least = min(least, v);
-                    mk[before] = (unsigned)g;
-                } else {
-                    most = max(most, v);
+                    for (int h = 0; h < G; ++h) before += mg[h] > v;
+                    if (before < top) {
+                        least = min(least, v);
+                        mk[before] = (unsigned)g;
+                    } else {
+                        most = max(most, v);
+                    }
+                }
+            } else {
+                // many: a value between the last kept and the first dropped, by
+                // halving.  The values differ, so there is one.  169897 tokens,
+                // 112 experts in 56 groups: 160 us, by the places 253; with 8
+                // lanes 21757 tokens, 192 experts in 96 groups: 80 and 90 us,
+                // 87590 tokens, 82 experts in 41 groups: 115 and 101.
+                unsigned lo = ~0u, hi = 0u;
+                for (int g = sub; g < G; g += L) {
+                    lo = min(lo, mg[g]);
+                    hi = max(hi, mg[g]);
+                }
+                lo = lanes_min<L>(lo) - 1u;  // all are above lo, none above hi
+                hi = lanes_max<L>(hi);
+                unsigned cut = lo;
+                bool found = false;
+                while (!__all_sync(0xffffffffu, found)) {
+                    const unsigned mid = lo + (hi - lo) / 2u;
+                    int n = 0;
+#pragma unroll 8
+                    for (int g = sub; g < G; g += L) n += mg[g] > mid;
+                    n = lanes_sum<L>(n);
+                    if (n == top) {
+                        cut = mid;
+                        found = true;
+                    }
+                    if (n > top) lo = mid;
+                    else hi = mid;
+                }
+                int at = 0;
+                for (int g0 = 0; g0 < G; g0 += L) {
+                    const int g = g0 + sub;
+                    const unsigned v = g < G ? mg[g] : 0u;
+                    const bool in = g < G && v > cut;
+                    const unsigned who = __ballot_sync(0xffffffffu, in) >> (tok * L) & kAll;
+                    if (in) {
+                        mk[at + __popc(who & ((1u << sub) - 1u))] = (unsigned)g;
+                        least = min(least, v);
+                    } else if (g < G) {
+                        most = max(most, v);
+                    }
+                    at += __popc(who);
                 }
             }
             least = lanes_min<L>(least);
@@ -777,7 +826,8 @@ __global__ void __launch_bounds__(32 * kGateWarps, 4) gate_scored_kernel(const _
         for (int u = 0; u < KL; ++u)
             if (u % L == sub) id[u / L] = key_id(lst[u]);
         unsure = (unsure || unsure_groups) && on;
-        const unsigned any = __ballot_sync(0xffffffffu, unsure), by_group = __ballot_sync(0xffffffffu, on && unsure_groups);
+        const unsigned any = __ballot_sync(0xffffffffu, unsure);
+        const unsigned by_group = __ballot_sync(0xffffffffu, on && unsure_groups);
         if (any != 0u) {
 #pragma unroll
             for (int u = 0; u < kMine; ++u)
@@ -1087,7 +1137,11 @@ cudaError_t launch_bwd_e(const BwdArgs &a, cudaStream_t s)
 cudaError_t launch_gate_scored(const float *logits, int T, int E, int k, const moe_scoring *S, int32_t *idx,
                                float *gates, int32_t *counts, double *aux, double *ent, void *ws, cudaStream_t s)
 {
-    const GateArgs a = {logits, T, E, k, *S, idx, gates, counts, aux, ent, ws};
+    GateArgs a = {logits, T, E, k, *S, idx, gates, counts, aux, ent, ws};
+    // Groups by their best expert, as many as slots or more: the k best experts
+    // of all are in them.  (Groups before the one of such an expert have an
+    // expert each that comes before it, fewer than k.)
+    if (S->group_top == 1 && k <= S->top_groups) a.S.groups = a.S.top_groups = 1;
     if (k <= 4) return launch_scored_lanes<4>(a, s);
     if (k <= 8) return launch_scored_lanes<8>(a, s);
     return launch_scored_lanes<16>(a, s);

@@ -354,3 +354,27 @@ def test_a_training_step():
     (gates64(ref, ids.cpu(), "sigmoid", True, 1.25) * out.d_gates.cpu().double()).sum().backward()
     bound = backward_error(logits.cpu(), ids.cpu(), out.d_gates.cpu(), E, "sigmoid", True, 1.25)
     assert_near(out.d_logits.cpu(), ref.grad, bound, "d_logits")
+
+
+@pytest.mark.parametrize("K", [544, 1024, 2048])
+@pytest.mark.parametrize("rows", [3, 700])
+def test_operands_at_any_16_bytes(K, rows):
+    """Codes and scales that start 16 bytes past a multiple of 32."""
+    N = 160
+    x, w = fp4(rows, K, seed=1, spread=2.0), fp4(N, K, seed=2, std=K ** -0.5, spread=2.0)
+    want = ExpertRows(rows=rows).linear_fp4(x, w)
+
+    def moved(t):
+        flat = torch.full((t.numel() + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        at = 16 + (-flat.data_ptr()) % 32
+        out = flat[at:at + t.numel()].view(t.shape)
+        out.copy_(t)
+        assert out.data_ptr() % 32 == 16
+        return out
+
+    a, b = (Fp4Rows(moved(q.codes), moved(q.scales)) for q in (x, w))
+    for xs in (x, a):
+        for ws in (w, b):
+            assert torch.equal(ExpertRows(rows=rows).linear_fp4(xs, ws), want)
+    u, e = linear64(values(x), values(w)[None], [rows])
+    assert_near(want, u, e + BF16 * (u.abs() + e), "y")

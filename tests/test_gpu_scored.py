@@ -64,7 +64,8 @@ def check(logits, k, scoring, bias=None, near=False):
     assert torch.equal(got, want), f"{int(wrong.sum())} of {T} tokens"
     g = gates64(logits, want, scoring.score, scoring.renorm, scoring.scale)
     off = (gates.cpu().double() - g).abs()
-    assert bool((off <= gates_error(g, logits, want, scoring.score, scoring.renorm, scoring.scale)).all()), f"gates off by {off.max()}"
+    bound = gates_error(g, logits, want, scoring.score, scoring.renorm, scoring.scale)
+    assert bool((off <= bound).all()), f"gates off by {off.max()}"
     n = torch.bincount(want.flatten(), minlength=E)
     assert torch.equal(counts.cpu().long(), n)
     p = n.double() / (T * k)
@@ -81,7 +82,11 @@ SHAPES = [  # T, E, k, groups, top_groups, group_top
     # as many tokens as one lane each takes
     (39001, 33, 3, 11, 4, 2), (39040, 60, 6, 5, 3, 1), (39007, 17, 16, 1, 1, 1), (40001, 8, 2, 1, 1, 1),
     (39500, 64, 16, 4, 2, 2), (117001, 128, 8, 16, 5, 2), (117000, 96, 4, 1, 1, 1), (39009, 1, 1, 1, 1, 1),
-    (39002, 62, 5, 31, 30, 1), (39003, 48, 7, 2, 1, 2), (38999, 3, 2, 3, 2, 1), (9000, 160, 6, 8, 3, 2), (17, 96, 12, 12, 5, 1),
+    (39002, 62, 5, 31, 30, 1), (39003, 48, 7, 2, 1, 2), (38999, 3, 2, 3, 2, 1),
+    # many groups, and groups by their best that hold fewer than k of them
+    (39100, 64, 8, 32, 9, 2), (39101, 60, 5, 20, 13, 2), (6000, 256, 8, 128, 40, 2), (300, 256, 16, 128, 9, 2),
+    (39102, 64, 6, 32, 3, 1), (5000, 128, 4, 64, 2, 1), (5001, 160, 9, 80, 5, 1), (39103, 40, 1, 20, 19, 2),
+    (9000, 160, 6, 8, 3, 2), (17, 96, 12, 12, 5, 1),
 ]
 
 
@@ -99,7 +104,9 @@ def test_selection(T, E, k, groups, top, two, score):
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("T,E,k,groups,top,two", [(700, 64, 8, 8, 4, 2), (700, 256, 8, 16, 6, 2), (6000, 64, 6, 8, 4, 1),
-                                                  (50000, 64, 8, 8, 4, 2), (500, 60, 4, 1, 1, 1)])
+                                                  (50000, 64, 8, 8, 4, 2), (500, 60, 4, 1, 1, 1),
+                                                  (40000, 64, 8, 32, 9, 2), (5000, 256, 8, 128, 40, 2),
+                                                  (40000, 64, 4, 32, 3, 1)])
 def test_ties_and_near_ties(T, E, k, groups, top, two, score):
     s = Scoring(score, groups, top, two)
     # every score the same: the lowest ids
