@@ -29,9 +29,10 @@
 //   wgrad, the same                                           460 us, 85 %
 //   linear, 128 rows, 32 experts, 2048 -> 2 x 1024            47 us, 5.7 TB/s:
 //     the weights' bytes (and 6 us to start and to finish)
-//   linear in 4 bits, 65536 rows, 16 experts, 5120 -> 2 x 2048 swiglu  445 us,
-//     6.2 PFLOP/s; one expert, 8192 -> 8192: 1258 us, 7.0 PFLOP/s: the matrix
-//     instructions, 6.8-7.7 if nothing had to bring their scales
+//   linear in 4 bits, 65536 rows, 16 experts, 5120 -> 2 x 2048 swiglu  408 us,
+//     6.7 PFLOP/s; one expert, 8192 -> 8192: 1258 us, 7.0 PFLOP/s: the matrix
+//     instructions and the way of their scales; below some 3000 of k the
+//     epilogue: 229 us at 256, 256 us at 2048
 //   linear in 4 bits, 128 rows, 32 experts, 2048 -> 2 x 2048   29 us, 4.9 TB/s
 //   linear, 512 rows, 8 experts, 512 -> 2 x 256               6 us from the
 //     first instruction to the last: 0.8 for offsets and barriers, 1 until the
@@ -371,7 +372,9 @@ struct LinearEpilogue {
         }
         if constexpr (KIND != kFp4)
             if (p.saved) save(u, row, rows);
-        if (p.glu) {
+        if constexpr (KIND == kFp4) {
+            apply(u, pitch);
+        } else if (p.glu) {
             // lanes 2i and 2i+1 hold gate and up of a column: of each two
             // rows the even lane finishes the first, the odd lane the second
             const bool odd = lane & 1;
@@ -420,6 +423,43 @@ struct LinearEpilogue {
             }
         }
         group_sync(g);
+    }
+    // Activation, residual and rounding of a chunk for kFp4, whose products may
+    // be shorter than this: each step for all rows before the next, nothing
+    // tested in between.  65536 rows, 256 -> 2 x 2048: 229 us, with the tests
+    // and the residual's load beside each store (as in finish) 306 us; 5120 ->
+    // 2 x 2048: 408 and 445 us.
+    __device__ __forceinline__ void apply(float (&u)[32], int pitch)
+    {
+        const bool odd = p.glu && (lane & 1);
+        unsigned char *const o = out + (p.glu ? (odd ? pitch : 0) + (q * 16 + lane / 2) * 2 : (q * 32 + lane) * 2);
+        if (p.glu) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? u[i] : u[i + 1], 1);
+                const float gate = odd ? got : u[i], up = odd ? u[i + 1] : got;
+                u[i] = gate * logistic(gate) * up;
+            }
+        } else if (p.act == MOE_ACT_SILU) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = act_value(u[i], MOE_ACT_SILU);
+        } else if (p.act == MOE_ACT_GELU) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = act_value(u[i], MOE_ACT_GELU);
+        }
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (!p.glu || i % 2 == 0)
+                    u[i] += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(o + i * pitch));
+        }
+        if (p.glu) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) st_shared_bf16(o + i * kPitchGlu, u[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) st_shared_bf16(o + i * kPitch, u[i]);
+        }
     }
     // u in 8 bits: the 32 columns of a block are the 32 lanes of a warp, or
     // for swiglu every other lane of two warps
@@ -931,8 +971,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         // rows lane, lane + 32, .. of both operands, and stores 4 bytes of 4
         // rows with one instruction.  The two warps take every other kSpan
         // stages: a stage takes one of them about 780 cycles, its products
-        // 530.  65536 rows, 16 experts, 5120 -> 2 x 2048: 445 us; a sector with
-        // two requests 465 us; the rows' bytes through a ring in shared memory
+        // 530.  65536 rows, 16 experts, 5120 -> 2 x 2048: 445 us (before the
+        // epilogue below); a sector with two requests 465 us; the rows' bytes through a ring in shared memory
         // 513 us; a warp for each operand, four stages ahead in registers and
         // unrolled for that, 860 us: 270 KB of instructions, and the block
         // waits for them.  Without any loads here 410 us.
