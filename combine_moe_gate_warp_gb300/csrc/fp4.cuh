@@ -18,12 +18,6 @@ __device__ __forceinline__ unsigned fp4_byte(unsigned amax)
     const int b = (int)(amax >> 7) - 2 + ((amax & 0x7Fu) > 0x40u ? 1 : 0);
     return amax >= 0x7F80u ? 255u : (unsigned)max(b, 0);
 }
-// The same from fp32 bits (sign cleared).
-__device__ __forceinline__ unsigned fp4_byte_f32(unsigned amax)
-{
-    const int b = (int)(amax >> 23) - 2 + ((amax & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-    return amax >= 0x7F800000u ? 255u : (unsigned)max(b, 0);
-}
 // 2^(127 - byte), exact (byte <= 253 for a finite amax)
 __device__ __forceinline__ float fp4_inverse(unsigned byte) { return __uint_as_float((254u - byte) << 23); }
 
