@@ -162,15 +162,17 @@ constexpr unsigned long long kStageLimitNs = 2000;
 
 // Wait for phase `parity`, at most the block's limit.  False once the limit has
 // passed or another role of the block has given up; then every role leaves
-// its loop.
+// its loop.  CLUSTER: another block's mbar_hand_over arrives there.
+template <bool CLUSTER>
 __device__ __forceinline__ bool poll(uint64_t *bar, uint32_t parity, Control *c, void *ws)
 {
+    const auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
     for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
+        if (done()) return true;
     const unsigned long long t0 = global_timer_ns();
     for (;;) {
         for (int i = 0; i < 16; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+            if (done()) return true;
         if (*(volatile int *)&c->abort) return false;
         if (global_timer_ns() - t0 > c->limit) {
             *(volatile int *)&c->abort = 1;
@@ -181,9 +183,10 @@ __device__ __forceinline__ bool poll(uint64_t *bar, uint32_t parity, Control *c,
 }
 
 // The same for a whole warp, which goes on together.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Control *c, void *ws)
 {
-    return __all_sync(0xFFFFFFFFu, poll(bar, parity, c, ws));
+    return __all_sync(0xFFFFFFFFu, poll<CLUSTER>(bar, parity, c, ws));
 }
 
 // a / b for 0 <= a < 2^30 and b > 0 with a quotient below 2^22: the rounded
@@ -662,6 +665,7 @@ template <int CG, int BN, int MODE, int KIND, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ Params p)
 {
     constexpr bool FP8 = KIND == kE4m3, FP4 = KIND == kFp4;
+    constexpr bool kHandOver = FP4 && CG == 2;  // the second block's scales, to the first's copy of them
     constexpr int kStages = stages(CG, BN, MODE, KIND, SPLIT);
     constexpr int kStage = stage_bytes(CG, BN, KIND);
     constexpr int kGroup = group_bytes(MODE, KIND);
@@ -912,15 +916,17 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 if (!ok) break;
                 tc_fence_after();
                 for (int i = 0; i < iters; ++i) {
-                    ok = ready || wait(&c->full[s], ph, c, p.ws);
+                    ok = ready || wait<kHandOver>(&c->full[s], ph, c, p.ws);
                     if (!ok) break;
+                    if (kHandOver) take_over();
                     tc_fence_after();
                     const int now = s;
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1;
                     }
-                    const bool next = mbar_test_wait(&c->full[s], ph);
+                    const bool next =
+                        kHandOver ? mbar_test_wait_cluster(&c->full[s], ph) : mbar_test_wait(&c->full[s], ph);
                     const uint64_t da = da0 + (uint64_t)(now * (kStage >> 4)), db = db0 + (uint64_t)(now * (kStage >> 4));
                     const int from = MODE == kWgrad && last_steps != 0 && i == iters - 1 ? 4 - last_steps : 0;
                     if (one) {
@@ -1065,12 +1071,17 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    // Not released at cluster scope: a block's scales are read
-                    // by the copy to its own tensor memory, from its own shared
-                    // memory, and the fence above has them there before the
-                    // arrival goes out.  A release, or a fence by an idle warp,
-                    // takes 1900 cycles a stage (1230 us against 513 at the time).
-                    if (lane == 0) mbar_arrive_remote(cluster_addr(&c->full[s], lead));
+                    // The first block's thread starts the copy that reads the
+                    // second's scales, so they are released at cluster scope:
+                    // what lies in shared memory alone, which takes no time
+                    // that could be measured (440 us, with an arrival of the
+                    // block's own scope 438).  A fence of all memory takes
+                    // 1900 cycles a stage (1230 us against 513 at the time).
+                    if (lane == 0) {
+                        const uint32_t full = cluster_addr(&c->full[s], lead);
+                        if (kHandOver) mbar_hand_over(full);
+                        else mbar_arrive_remote(full);
+                    }
                     step(1);
                 }
                 i = next;

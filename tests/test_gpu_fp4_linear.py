@@ -378,3 +378,31 @@ def test_operands_at_any_16_bytes(K, rows):
             assert torch.equal(ExpertRows(rows=rows).linear_fp4(xs, ws), want)
     u, e = linear64(values(x), values(w)[None], [rows])
     assert_near(want, u, e + BF16 * (u.abs() + e), "y")
+
+
+@pytest.mark.parametrize("width,rows,m", [(128, 3001, 520), (160, 12001, 520), (192, 1501, 2056), (224, 8001, 264)])
+def test_a_pair_reads_the_scales_of_its_stage(width, rows, m):
+    """Scales that differ from block to block and row to row, over many rounds
+    of the ring, in products of whole numbers whose sums fp32 holds: a scale of
+    another stage, in either block of a pair, gives other bits.  The values are
+    1, 0 or -1 times 2^0 to 2^3, so a sum stays below K * 2^6 < 2^24."""
+    K = 8224
+    assert ExpertRows(rows=rows).cut("linear_fp4", m, K) == (2, width, 1)
+    for seed in range(6):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+
+        def whole(*shape):
+            v = torch.randint(0, 3, (*shape, K), generator=g, device="cuda")
+            s = torch.randint(127, 131, (*shape, K // 32), generator=g, device="cuda")
+            c = torch.tensor([2, 0, 10], device="cuda")[v]  # the codes of 1, 0 and -1
+            scales = torch.zeros(*shape, fp4_pitch(K), dtype=torch.uint8, device="cuda")
+            scales[..., :K // 32] = s.to(torch.uint8)
+            q = Fp4Rows((c[..., 0::2] | c[..., 1::2] << 4).to(torch.uint8), scales)
+            return q, ((1 - v) << (s - 127).repeat_interleave(32, -1)).double()
+
+        (x, xv), (w, wv) = whole(rows), whole(m)
+        want = (xv @ wv.T).bfloat16()
+        r = ExpertRows(rows=rows)
+        for _ in range(3):
+            assert torch.equal(r.linear_fp4(x, w), want)
+        assert r.status() == 0
