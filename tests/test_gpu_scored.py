@@ -396,3 +396,31 @@ def test_refusals_of_the_plan():
     plan = RoutePlan(RouteShape(T=4, H=64, E=8, k=2, P=1, scoring=Scoring(groups=8, top_groups=1)))
     with pytest.raises(MoeError):
         plan.route(logits)  # one group of one expert does not hold two
+
+
+@pytest.mark.parametrize("T", [70, 6000, 40000])
+def test_scores_that_64_bits_make_equal(T):
+    """A softmax score is exp(l - max) / sum in 64 bits, on every way to the
+    answer: few near candidates or more than a warp's lanes, with a bias of
+    zeros or without one, and in a group's value.  exp(-1.2e-16) is 1 - 2^-53;
+    divided by the sums below it and 1 give the same score, a tie that goes to
+    the lower id, while the product with 1 / sum, or no division, tells them
+    apart.  The sums are whole: every order of adding gives them."""
+    below = -1.2e-16
+    for n in (3, 6, 48, 60):  # equal scores
+        assert (1 - 2.0 ** -53) / n == 1 / n
+        logits = torch.full((T, 64), -1000.0)
+        logits[:, 1:n] = 0.0
+        logits[:, 0] = below
+        logits[1::2] = logits[1::2].roll(4, 1)
+        k = min(n, 8)
+        for bias in (None, torch.zeros(64)):
+            idx, _ = check(logits, k, Scoring("softmax"), bias)
+            assert torch.equal(idx.cpu().long(), torch.arange(k) + 4 * (torch.arange(T) % 2)[:, None])
+    # groups by their best, and by the sum of two
+    for two in (1, 2):
+        logits = torch.full((T, 64), -1000.0)
+        logits[:, 9], logits[:, 17], logits[:, 40] = below, 0.0, 0.0
+        for bias in (None, torch.zeros(64)):
+            idx, _ = check(logits, 2, Scoring("softmax", 8, 1, two), bias)
+            assert torch.equal(idx.cpu().long(), torch.tensor([9, 8]).expand(T, 2))
