@@ -406,3 +406,16 @@ def test_a_pair_reads_the_scales_of_its_stage(width, rows, m):
         for _ in range(3):
             assert torch.equal(r.linear_fp4(x, w), want)
         assert r.status() == 0
+
+
+def test_falling_offsets_write_no_row_twice():
+    """The third expert starts below the largest offset so far: it is left
+    empty, with every row that only it would have."""
+    K, N = 96, 40
+    x, w = fp4(20, K, seed=1), fp4(3, N, K, seed=2)
+    good = ExpertRows(offsets_of([5, 5, 10]), rows=20).linear_fp4(x, w)
+    r = ExpertRows(torch.tensor([0, 5, 3, 20], dtype=torch.int32, device="cuda"), rows=20)
+    out = torch.full((20, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    r.linear_fp4(x, w, out=out)
+    assert r.status() == abi.MOE_ERR_DEVICE_DATA
+    assert torch.equal(out[:5], good[:5]) and bool((out[5:] == 7.0).all())
