@@ -710,8 +710,10 @@ __global__ void __launch_bounds__(32 * kGateWarps, 4) gate_scored_kernel(const _
                         two ? !((same(a1, b1) && same(a2, b2)) || (same(a1, b2) && same(a2, b1))) : !same(a1, b1);
                     const unsigned last = two ? f2 : f1;
                     for (int i = g * per; i < (g + 1) * per; ++i)
-                        unsure_groups |=
-                            mine[i] < last && (int)(mine[i] >> 9) >= (int)(last >> 9) - near && !same(i, key_id(last));
+                        if (mine[i] < last && (int)(mine[i] >> 9) >= (int)(last >> 9) - near)
+                            // one that equals the second, and with it may be above a near first
+                            unsure_groups |= !same(i, key_id(last)) ||
+                                             (two && (int)(f1 >> 9) - (int)(f2 >> 9) <= near && !same(b1, b2));
                 }
             }
             unsigned ask = __ballot_sync(0xffffffffu, on && unsure_groups);

@@ -155,3 +155,18 @@ def test_drawn_shapes(score):
         logits = (randn(T, E, seed=n) * pick(0.3, 1.0, 3.0)).bfloat16().float()
         bias = pick(None, 1e-4, 0.02, 1.0)
         check(logits, k, s, None if bias is None else randn(E, seed=n, std=bias), 1e-3)
+
+
+@pytest.mark.parametrize("T", [40, 6000, 40000])
+def test_three_near_values_in_a_group_of_two(T):
+    """A group's two best are the two equal ones above a near third, which
+    comes first by its id and takes the place of the first in fp32."""
+    for score, high, low in (("sigmoid", 30.0, 20.0), ("sigmoid", 1.5, 1.5 - 2.0 ** -23), ("softmax", 1.5, 1.5 - 2.0 ** -23)):
+        logits = torch.full((T, 24), -9.0)
+        logits[:, 1], logits[:, 4] = high, low                    # high + low
+        logits[:, 9], logits[:, 10], logits[:, 12] = low, high, high  # high + high
+        logits[1::2] = logits[1::2].roll(8, 1)
+        s = Scoring(score, 3, 1, 2)
+        check(logits, 4, s)
+        check(logits, 4, s, torch.zeros(24))
+        assert torch.equal(select64(logits, 1, score, 3, 1, 2)[:, 0], 10 + 8 * (torch.arange(T) % 2))
