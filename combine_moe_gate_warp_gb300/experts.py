@@ -394,6 +394,8 @@ class ExpertRows:
     def dequantize_fp4(self, x: Fp4Rows, *, out=None):
         """Rows in 4 bits as bf16 [rows, K], which holds every value exactly:
         for a weight gradient, or any product that takes bf16."""
+        if not isinstance(x, Fp4Rows):
+            raise TypeError("x: expected Fp4Rows")
         K = 2 * _columns(x.codes.shape[-1], "x.codes")
         cp, sp = self._fp4(x, K, "x")
         out, op = self._out_rows(out, K, "out")

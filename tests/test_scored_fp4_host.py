@@ -127,3 +127,11 @@ def test_the_binding_refuses(abi):
         r.quantize_fp4(x, out=q.codes)
     with pytest.raises(ValueError, match="CUDA"):
         r.quantize_fp4(x, out=q)
+
+
+def test_rows_of_another_kind_are_a_type_error(abi):
+    from combine_moe_gate_warp_gb300 import ExpertRows
+    r = ExpertRows(rows=4, device="cpu")
+    for bad in (torch.zeros(4, 32, dtype=torch.uint8), None, (1, 2)):
+        with pytest.raises(TypeError, match="Fp4Rows"):
+            r.dequantize_fp4(bad)
