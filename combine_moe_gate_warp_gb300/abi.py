@@ -286,6 +286,8 @@ class Scoring:
                 raise ValueError(f"{name}: 1 to {MOE_MAX_EXPERTS}, got {getattr(self, name)}")
 
     def c(self, bias=None, bias_next=None, bias_rate: float = 0.0) -> moe_scoring:
+        if bias_rate and bias_next is None:
+            raise ValueError("bias_rate: needs bias_next, which receives the moved bias")
         return moe_scoring(MOE_SCORE_SOFTMAX if self.score == "softmax" else MOE_SCORE_SIGMOID, self.groups,
                            self.top_groups, self.group_top, self.renorm, self.scale, bias_rate, bias, bias_next)
 

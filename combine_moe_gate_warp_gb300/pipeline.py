@@ -121,7 +121,7 @@ class RoutePlan:
         s = self.shape
         _check_input(logits, torch.float32, (s.T, s.E), "logits")
         if s.scoring is None:
-            if bias is not None or bias_next is not None:
+            if bias is not None or bias_next is not None or bias_rate:
                 raise ValueError("bias: only with scoring")
             abi._check(self._lib.moe_gate(logits.data_ptr(), s.T, s.E, s.k, s.mode, *self._gate_tail), "moe_gate")
             return
@@ -141,7 +141,7 @@ class RoutePlan:
         overflow is re-assigned."""
         s = self.shape
         if self.fused_route:
-            if bias is not None or bias_next is not None:
+            if bias is not None or bias_next is not None or bias_rate:
                 raise ValueError("bias: only with scoring")
             _check_input(logits, torch.float32, (s.T, s.E), "logits")
             abi._check(self._lib.moe_route(logits.data_ptr(), *self._route_tail), "moe_route")

@@ -168,6 +168,7 @@ moe_status moe_gate(const float *logits, int T, int E, int k, int mode,
  *                 bias_e + bias_rate if expert e got fewer than T*k / E
  *                 assignments, bias_e - bias_rate if it got more, bias_e if
  *                 exactly as many.  May be S->bias itself.
+ *   S->bias_rate  enters bias_next only (finite also without it).
  * groups divides E, k <= top_groups * (E / groups), group_top <= E / groups.
  */
 #define MOE_SCORE_SIGMOID 0

@@ -424,3 +424,18 @@ def test_scores_that_64_bits_make_equal(T):
         for bias in (None, torch.zeros(64)):
             idx, _ = check(logits, 2, Scoring("softmax", 8, 1, two), bias)
             assert torch.equal(idx.cpu().long(), torch.tensor([9, 8]).expand(T, 2))
+
+
+def test_a_rate_that_nothing_takes_is_refused():
+    logits, bias = torch.zeros(4, 8, device="cuda"), torch.zeros(8, device="cuda")
+    plan = RoutePlan(RouteShape(T=4, H=64, E=8, k=2, P=1, scoring=Scoring()))
+    for call in (plan.gate, plan.route):
+        with pytest.raises(ValueError, match="bias_next"):
+            call(logits, bias, bias_rate=1e-3)
+        call(logits, bias, bias_next=bias, bias_rate=0.0)
+    plan = RoutePlan(RouteShape(T=4, H=64, E=8, k=2, P=1))
+    for call in (plan.gate, plan.route):
+        with pytest.raises(ValueError, match="only with scoring"):
+            call(logits, bias_rate=1e-3)
+    with pytest.raises(ValueError, match="bias_next"):
+        gate(logits, 2, Scoring(), bias, None, 1e-3)

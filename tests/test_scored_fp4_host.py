@@ -135,3 +135,12 @@ def test_rows_of_another_kind_are_a_type_error(abi):
     for bad in (torch.zeros(4, 32, dtype=torch.uint8), None, (1, 2)):
         with pytest.raises(TypeError, match="Fp4Rows"):
             r.dequantize_fp4(bad)
+
+
+def test_a_rate_without_a_place_for_the_moved_bias(abi):
+    from combine_moe_gate_warp_gb300 import Scoring
+    with pytest.raises(ValueError, match="bias_next"):
+        Scoring().c(bias_rate=1e-3)
+    with pytest.raises(ValueError, match="bias_next"):
+        Scoring().c(bias=OFF.value, bias_rate=1e-3)
+    assert Scoring().c(bias_next=64, bias_rate=0.5).bias_rate == 0.5 and Scoring().c().bias_rate == 0.0
