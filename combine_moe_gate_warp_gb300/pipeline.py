@@ -326,8 +326,12 @@ class RouteGraph:
     def step(self, logits=None, x=None, expert_out=None, shared_out=None, bias=None) -> RoutePlan:
         """Copy the given inputs into the graph's buffers and replay; returns
         the plan holding the results."""
-        if bias is not None and self.bias is None:
-            raise ValueError("bias: only with scoring")
+        if bias is not None:
+            if self.bias is None:
+                raise ValueError("bias: only with scoring")
+            if bias.dtype != torch.float32 or bias.shape != self.bias.shape:  # a copy would convert or repeat it
+                raise ValueError(f"bias: expected {tuple(self.bias.shape)} of torch.float32, got {tuple(bias.shape)} of "
+                                 f"{bias.dtype}")
         cur = torch.cuda.current_stream(self.device)
         self.stream.wait_stream(cur)
         with torch.cuda.stream(self.stream):

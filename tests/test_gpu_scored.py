@@ -439,3 +439,16 @@ def test_a_rate_that_nothing_takes_is_refused():
             call(logits, bias_rate=1e-3)
     with pytest.raises(ValueError, match="bias_next"):
         gate(logits, 2, Scoring(), bias, None, 1e-3)
+
+
+def test_the_graph_s_bias_is_one_of_each_expert():
+    """As RoutePlan.gate takes it: no single value for all experts, no other type."""
+    graph = RouteGraph(RouteShape(T=4, H=64, E=8, k=2, P=1, scoring=Scoring()))
+    bias = torch.linspace(0, 1, 8, device="cuda")
+    graph.step(bias=bias)
+    for bad in (bias[:1], bias[3], bias[:4], bias.double(), bias.expand(2, 8)):
+        with pytest.raises(ValueError, match="bias"):
+            graph.step(bias=bad)
+    assert torch.equal(graph.bias, bias)
+    with pytest.raises(ValueError, match="only with scoring"):
+        RouteGraph(RouteShape(T=4, H=64, E=8, k=2, P=1)).step(bias=bias)
