@@ -29,10 +29,11 @@
 //   wgrad, the same                                           460 us, 85 %
 //   linear, 128 rows, 32 experts, 2048 -> 2 x 1024            47 us, 5.7 TB/s:
 //     the weights' bytes (and 6 us to start and to finish)
-//   linear in 4 bits, 65536 rows, 16 experts, 5120 -> 2 x 2048 swiglu  408 us,
-//     6.7 PFLOP/s; one expert, 8192 -> 8192: 1258 us, 7.0 PFLOP/s: the matrix
-//     instructions and the way of their scales; below some 3000 of k the
-//     epilogue: 229 us at 256, 256 us at 2048
+//   linear in 4 bits, 65536 rows, 16 experts, 5120 -> 2 x 2048 swiglu  440 us,
+//     6.2 PFLOP/s (395 us in a row on two sets of inputs, 7.0); one expert, 8192
+//     -> 8192: 1258 us, 7.0 PFLOP/s: the matrix instructions and the way of
+//     their scales; below some 3000 of k the epilogue: 226 us at 256, 234 at
+//     1024, 266 at 2048
 //   linear in 4 bits, 128 rows, 32 experts, 2048 -> 2 x 2048   29 us, 4.9 TB/s
 //   linear, 512 rows, 8 experts, 512 -> 2 x 256               6 us from the
 //     first instruction to the last: 0.8 for offsets and barriers, 1 until the

@@ -273,11 +273,19 @@ __device__ __forceinline__ float sigmoid(float l)
 // of KL keys are sorted by Batcher's networks, merged, and merged across the
 // lanes of a token.
 //
-// What bounds it: instructions (110 a token at 64 experts) and, with 16 warps
-// an SM, their latency; HBM is at a fifth.  262144 tokens, 64 experts in 8
-// groups, top-8 of 4 groups: 61 us; 16384 tokens, 256 experts in 16 groups: 26
-// us; a few tokens: 8 us, by the host.  All of it in 64 bits, a warp for each
-// token, took 2994, 430 and 17 us.
+// What bounds it: the latency of its instructions, of which 16 warps an SM (128
+// registers a thread) issue 0.46 a cycle and scheduler; alone the 109 a token
+// at 64 experts would take 23 us.  HBM is at a fifth.  262144 tokens, 64
+// experts in 8 groups, top-8 of 4 groups: 62 us; 16384 tokens, 256 experts in
+// 16 groups: 26 us; a few tokens: 8 us, by the host.  All of it in 64 bits, a
+// warp for each token, took 2994, 430 and 17 us.
+//
+// The time depends on the values: q has steps of the whole span of scores and
+// biases, and whatever lies within a few of them goes to 64 bits.  262144
+// tokens as above, L2 flushed: logits of spread 1 and 3 without a bias 66 and
+// 68 us, 4 79, 6 (half of the tokens have scores that round alike) 248, 8 609;
+// one expert's bias at -1: 68 us, at -100 136, at -10000 1408, at -10^6 and
+// below 7327.
 //
 // What q does not decide is found and decided elsewhere: with the bound on
 // q's error below, neighbours in the order that are at most `near` apart, and
