@@ -29,11 +29,11 @@
 //   wgrad, the same                                           460 us, 85 %
 //   linear, 128 rows, 32 experts, 2048 -> 2 x 1024            47 us, 5.7 TB/s:
 //     the weights' bytes (and 6 us to start and to finish)
-//   linear in 4 bits, 65536 rows, 16 experts, 5120 -> 2 x 2048 swiglu  440 us,
-//     6.2 PFLOP/s (395 us in a row on two sets of inputs, 7.0); one expert, 8192
-//     -> 8192: 1258 us, 7.0 PFLOP/s: the matrix instructions and the way of
-//     their scales; below some 3000 of k the epilogue: 226 us at 256, 234 at
-//     1024, 266 at 2048
+//   linear in 4 bits, 65536 rows, 16 experts, 5120 -> 2 x 2048 swiglu  465 us,
+//     5.9 PFLOP/s (432 us in a row on two sets of inputs, 6.4); one expert, 8192
+//     -> 8192: 1270 us, 6.9 PFLOP/s: the matrix instructions and the way of
+//     their scales; below some 3000 of k the epilogue: 224 us at 256, 232 at
+//     1024, 262 at 2048
 //   linear in 4 bits, 128 rows, 32 experts, 2048 -> 2 x 2048   29 us, 4.9 TB/s
 //   linear, 512 rows, 8 experts, 512 -> 2 x 256               6 us from the
 //     first instruction to the last: 0.8 for offsets and barriers, 1 until the
@@ -110,13 +110,24 @@ __host__ __device__ constexpr int smem_bytes(int CG, int BN, int MODE, int KIND,
     return 1024 + stages(CG, BN, MODE, KIND, SPLIT) * stage_bytes(CG, BN, KIND) + 2 * group_bytes(MODE, KIND) +
            join_bytes(SPLIT, BN) + kControl;
 }
-// Tensor memory: two accumulators, and for kFp4 two sets of a stage's scales
-// (4 columns an atom) behind them: the next stage's are brought while the
-// products that read the last one's may still be queued.
+// Tensor memory: two accumulators, and for kFp4 sets of a stage's scales behind
+// them (4 columns an atom).  A copy of scales runs before the products that are
+// issued after it, but nothing holds it back behind the products that are
+// issued before it and may still be queued: it must not touch what they read.
+// With a set for each stage of the ring, the stage's barriers see to that.  The
+// widest pair has room for two sets, and waits for the products of the stage
+// two back (65536 rows, 16 experts, 5120 -> 2 x 2048: 465 us, without 440;
+// polling by one thread or without a pause 472 to 513: what it takes from the
+// warps that bring the scales).
 __host__ __device__ constexpr int scale_cols(int BN) { return 8 * (1 + scale_atoms(BN)); }
-__host__ __device__ constexpr int tmem_cols(int BN, int KIND)
+__host__ __device__ constexpr int scale_sets(int BN, int stages)
 {
-    const int need = 2 * BN + (KIND == kFp4 ? 2 * scale_cols(BN) : 0);
+    const int room = (512 - 2 * BN) / scale_cols(BN);
+    return room < stages ? room : stages;
+}
+__host__ __device__ constexpr int tmem_cols(int BN, int sets)
+{
+    const int need = 2 * BN + sets * scale_cols(BN);
     return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
 }
 
@@ -669,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     constexpr bool kHandOver = FP4 && CG == 2;  // the second block's scales, to the first's copy of them
     constexpr int kStages = stages(CG, BN, MODE, KIND, SPLIT);
     constexpr int kStage = stage_bytes(CG, BN, KIND);
+    constexpr int kSets = FP4 ? scale_sets(BN, kStages) : 0, kColumns = tmem_cols(BN, kSets);
     constexpr int kGroup = group_bytes(MODE, KIND);
     constexpr int kScales = kStageA + BN / CG * 128;  // kFp4: where a stage's scales start
     constexpr int kBM = kTileM * CG;
@@ -716,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         tmap_prefetch(&p.ma);
         tmap_prefetch(&p.mb);
     }
-    if (warp == 2) tmem_alloc<CG>(&c->tmem, tmem_cols(BN, KIND));
+    if (warp == 2) tmem_alloc<CG>(&c->tmem, kColumns);
     if (MODE == kWgrad && tid < 128) {
         // the bias sums' B operand: 2 KB of bf16 ones (any layout of them is the same)
         reinterpret_cast<uint4 *>(stg)[tid] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
@@ -897,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             const uint64_t ones = smem_desc(smem_addr(stg), kLeadB, 1024);
             const uint64_t ds0 = scale_desc(smem_addr(smem) + kScales);
             const bool one = elect_one();
-            int s = 0, acc = 0, set = 0;
+            int s = 0, acc = 0, set = 0, begun = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true, ready = false, more = walk.next(t);
             while (more) {
@@ -920,6 +932,18 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     ok = ready || wait<kHandOver>(&c->full[s], ph, c, p.ws);
                     if (!ok) break;
                     if (kHandOver) take_over();
+                    if (FP4 && kSets < kStages) {  // the products that read this set of scales
+                        if (begun == kSets) {
+                            ok = wait(&c->empty[s >= kSets ? s - kSets : s - kSets + kStages], s >= kSets ? ph : ph ^ 1, c,
+                                      p.ws);
+                            if (!ok) break;
+                        } else {
+                            ++begun;
+                        }
+                        set = set + 1 >= kSets ? 0 : set + 1;
+                    } else {
+                        set = s;
+                    }
                     tc_fence_after();
                     const int now = s;
                     if (++s == kStages) {
@@ -957,7 +981,6 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                         }
                         mma_commit<CG>(&c->empty[now]);
                     }
-                    set ^= 1;
                     __syncwarp();
                     if (i == 0) more = walk.next(t);  // the divisions of the next tile hide behind this one
                     ready = __all_sync(0xFFFFFFFFu, next);
@@ -1229,7 +1252,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     tc_fence_before();
     if (kCluster) cluster_sync_all();
     else __syncthreads();
-    if (warp == 2) tmem_free<CG>(tmem, tmem_cols(BN, KIND));
+    if (warp == 2) tmem_free<CG>(tmem, kColumns);
 }
 
 // --------------------------------------------------------------------------
