@@ -116,9 +116,8 @@ __host__ __device__ constexpr int smem_bytes(int CG, int BN, int MODE, int KIND,
 // issued before it and may still be queued: it must not touch what they read.
 // With a set for each stage of the ring, the stage's barriers see to that.  The
 // widest pair has room for two sets, and waits for the products of the stage
-// two back (65536 rows, 16 experts, 5120 -> 2 x 2048: 465 us, without 440;
-// polling by one thread or without a pause 472 to 513: what it takes from the
-// warps that bring the scales).
+// two back (65536 rows, 16 experts, 5120 -> 2 x 2048: 465 us, without 440; with
+// a wait that polls, or by the issuing thread alone, 472 to 513).
 __host__ __device__ constexpr int scale_cols(int BN) { return 8 * (1 + scale_atoms(BN)); }
 __host__ __device__ constexpr int scale_sets(int BN, int stages)
 {

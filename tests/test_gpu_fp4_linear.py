@@ -380,14 +380,18 @@ def test_operands_at_any_16_bytes(K, rows):
     assert_near(want, u, e + BF16 * (u.abs() + e), "y")
 
 
-@pytest.mark.parametrize("width,rows,m", [(128, 3001, 520), (160, 12001, 520), (192, 1501, 2056), (224, 8001, 264)])
-def test_a_pair_reads_the_scales_of_its_stage(width, rows, m):
+@pytest.mark.parametrize("cut,rows,m", [((2, 128, 1), 3001, 520), ((2, 160, 1), 12001, 520), ((2, 192, 1), 1501, 2056),
+                                        ((2, 224, 1), 8001, 264), ((1, 32, 1), 2090, 136), ((1, 32, 4), 32, 2160),
+                                        ((1, 32, 8), 58, 40), ((1, 64, 1), 641, 1544), ((1, 128, 2), 2477, 136),
+                                        ((1, 128, 4), 34, 2136), ((1, 128, 8), 536, 40)])
+def test_a_product_reads_the_scales_of_its_stage(cut, rows, m):
     """Scales that differ from block to block and row to row, over many rounds
     of the ring, in products of whole numbers whose sums fp32 holds: a scale of
-    another stage, in either block of a pair, gives other bits.  The values are
-    1, 0 or -1 times 2^0 to 2^3, so a sum stays below K * 2^6 < 2^24."""
+    another stage, in shared or in tensor memory, in either block of a pair,
+    gives other bits.  The values are 1, 0 or -1 times 2^0 to 2^3, so a sum
+    stays below K * 2^6 < 2^24."""
     K = 8224
-    assert ExpertRows(rows=rows).cut("linear_fp4", m, K) == (2, width, 1)
+    assert ExpertRows(rows=rows).cut("linear_fp4", m, K) == cut
     for seed in range(6):
         g = torch.Generator(device="cuda").manual_seed(seed)
 
